@@ -16,7 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libzc.so")
-SOURCES = ["zc_api.cu", "zc_stats.cu", "zc_encode.cu", "zc_decode.cu", "zc_static.cu", "zc_small.cu", "zc_fused.cu"]
+SOURCES = ["zc_api.cu", "zc_stats.cu", "zc_encode.cu", "zc_decode.cu", "zc_static.cu", "zc_small.cu", "zc_fused.cu",
+           "experts/ex_api.cu", "experts/ex_sort.cu", "experts/ex_rows.cu", "experts/ex_quantize.cu",
+           "experts/ex_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -30,8 +32,8 @@ def _nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    return files + [os.path.join(INCLUDE, "zc.h"), os.path.abspath(__file__)]
+    files = [os.path.join(d, f) for top in (CSRC, INCLUDE) for d, _, names in os.walk(top) for f in names]
+    return files + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
@@ -50,7 +52,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     flags = FLAGS + list(extra_flags or [])
 
     def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
+        obj = os.path.join(BUILD_DIR, src.replace("/", "_").replace(".cu", ".o"))
         cmd = [nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -1,0 +1,116 @@
+// ex_common.cuh -- what the exchange and expert kernels share: row vectors, types, launch helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "zc_common.cuh"
+#include "zc_moe.h"
+
+namespace zc {
+namespace ex {
+
+// B bytes of a row moved at once.
+template <int B>
+struct Bytes;
+template <>
+struct Bytes<16> { using type = uint4; };
+template <>
+struct Bytes<4> { using type = uint32_t; };
+template <>
+struct Bytes<2> { using type = unsigned short; };
+
+// The values of a vector as fp32, and back (rounded to nearest even).
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_float(float v) { return v; }
+
+template <typename T, int B>
+union Pack {
+  typename Bytes<B>::type raw;
+  T v[B / sizeof(T)];
+  __device__ Pack() {}
+};
+
+// The widest vector that every one of these row sets allows: 16 bytes, else 4, else one value.
+inline int vector_bytes(size_t element, size_t row_values, std::initializer_list<const void*> bases,
+                        std::initializer_list<size_t> pitches) {
+  uintptr_t all = row_values * element;
+  for (const void* b : bases) all |= reinterpret_cast<uintptr_t>(b);
+  for (size_t p : pitches) all |= p * element;
+  return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+}
+
+inline size_t type_bytes(int type) { return type == ZC_TYPE_FP32 ? 4 : 2; }
+
+// A launch that may start while the kernel before it (of the same call) still runs; it waits
+// for that kernel's writes with griddepcontrol.wait.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool after_own,
+                   A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after_own ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// ------------------------------------------------------------------ launchers
+
+struct RowShape {
+  size_t tokens, hidden;
+  int k, experts, type;
+};
+
+size_t sort_workspace(size_t slots, int experts);
+cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts, int* position, int* offsets,
+                        void* workspace, cudaStream_t stream);
+cudaError_t launch_dispatch(const RowShape& s, const void* x, size_t x_pitch, void* rows, size_t rows_pitch,
+                            const int* position, const int* offsets, int* status, cudaStream_t stream);
+cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitch, const float* weights,
+                           const int* position, const int* offsets, void* out, size_t out_pitch, int* status,
+                           cudaStream_t stream);
+cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_out_pitch, const void* rows,
+                                size_t rows_pitch, const float* weights, const int* position, const int* offsets,
+                                void* d_rows, size_t d_rows_pitch, float* d_weights, int* status, cudaStream_t stream);
+
+size_t column_blocks(size_t rows, int groups);
+cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, size_t cols, int fmt, uint8_t* values,
+                            uint8_t* scales, cudaStream_t stream);
+cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_t rows, size_t cols, int groups,
+                                    const int* offsets, int fmt, uint8_t* values, uint8_t* scales, int* block_offsets,
+                                    int* status, cudaStream_t stream);
+cudaError_t launch_quantize_weight(const void* w, int type, int groups, size_t rows, size_t cols, int fmt,
+                                   uint8_t* values, uint8_t* scales, uint8_t* values_t, uint8_t* scales_t,
+                                   cudaStream_t stream);
+
+struct Product {
+  const uint8_t *a, *a_scales, *b, *b_scales;
+  int a_fmt, b_fmt, groups, out_type;
+  size_t rows, n, k, out_pitch;
+  const int* offsets;
+  void* out;
+};
+// rows: the capacity in blocks for weight_grad.
+cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_weight_grad(const Product& p, const DeviceInfo& dev, cudaStream_t stream);
+
+}  // namespace ex
+}  // namespace zc

@@ -1,0 +1,188 @@
+"""8-bit floating point in blocks of 128 with a power-of-two scale each, and the experts' products on it.
+
+    w, w_t = quantize_weight(weight)                      # [experts, n, k] -> blocks of 128 x 128, and the transpose
+    y = matmul(quantize(x), w, offsets)                   # rows offsets[e] .. offsets[e + 1] - 1 times expert e's w^T
+    dx = matmul(quantize(dy), w_t, offsets)
+    dw = weight_grad(quantize_columns(dy, offsets), quantize_columns(x, offsets))   # [experts, n, k]
+
+``offsets`` is int32 [experts + 1] on the device, as ``moe.Plan.offsets``; None stands for one group of all the rows.
+A scale is the smallest power of two that brings its block's largest finite magnitude into the format's range, so
+scaling is exact and only the rounding to 8 bits loses anything.  Sums are taken in float32.  Every call runs on
+``stream`` (default: the current one) and does not synchronize.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from ._tensors import MAX_EXPERTS, TYPES, call, check, current, fn, on, on_device, rows_of
+
+BLOCK = 128
+FORMATS = {"e4m3": 0, "e5m2": 1}
+_FLOAT8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+@dataclass(frozen=True, eq=False)
+class Matrix:
+    """A matrix (or one for each expert) in 8-bit blocks.
+
+    data     uint8 [rows, pitch] or [experts, rows, pitch], pitch = 128 ceil(cols / 128); zeros past cols
+    scales   uint8 [words, rows, 4] or [experts, words, rows, 4], words = ceil(pitch / 512): the scale of row r and
+             block b is 2^(scales[..., b // 4, r, b % 4] - 127)
+    cols     values in a row
+    fmt      "e4m3" or "e5m2"
+    offsets  from quantize_columns: the first block of each group, int32 [groups + 1]
+    """
+
+    data: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+    fmt: str = "e4m3"
+    offsets: torch.Tensor | None = None
+
+    def __post_init__(self):
+        check(self.fmt in FORMATS, f"fmt must be one of {', '.join(FORMATS)}, got {self.fmt!r}")
+        d, s = self.data, self.scales
+        if d.dtype != torch.uint8 or s.dtype != torch.uint8:
+            raise TypeError("data and scales must be uint8")
+        check(d.device == s.device, f"data is on {d.device}, scales on {s.device}")
+        check(d.dim() in (2, 3) and s.dim() == d.dim() + 1, f"data {tuple(d.shape)} and scales {tuple(s.shape)} do not fit")
+        check(d.is_contiguous() and s.is_contiguous(), "data and scales must be contiguous")
+        pitch = _pitch(self.cols)
+        check(self.cols >= 0 and d.shape[-1] == pitch, f"rows of {self.cols} values take {pitch} bytes, got {d.shape[-1]}")
+        check(tuple(s.shape) == (*d.shape[:-2], -(-pitch // 512), d.shape[-2], 4),
+              f"scales of {tuple(d.shape)} cannot have the shape {tuple(s.shape)}")
+
+    @property
+    def rows(self) -> int:
+        return self.data.shape[-2]
+
+    def values(self) -> torch.Tensor:
+        """The 8-bit values without their scales (a view)."""
+        v = self.data.view(_FLOAT8[self.fmt])
+        return v if self.cols == v.shape[-1] else v[..., : self.cols]
+
+    def scale_values(self) -> torch.Tensor:
+        """The scales as float32 powers of two, in their own layout."""
+        return self.scales.view(torch.float8_e8m0fnu).float()
+
+
+def _pitch(cols):
+    return -(-cols // BLOCK) * BLOCK
+
+
+def _empty(lead, rows, cols, device):
+    pitch = _pitch(cols)
+    return (torch.empty((*lead, rows, pitch), dtype=torch.uint8, device=device),
+            torch.empty((*lead, -(-pitch // 512), rows, 4), dtype=torch.uint8, device=device))
+
+
+def _format(fmt):
+    check(fmt in FORMATS, f"fmt must be one of {', '.join(FORMATS)}, got {fmt!r}")
+    return FORMATS[fmt]
+
+
+def _input(name, x):
+    on_device(name, x, tuple(TYPES), 2)
+    check(x.shape[1] >= 1, f"{name} must have at least one column")
+
+
+def _offsets(offsets):
+    if offsets is None:
+        return 1, None
+    on_device("offsets", offsets, (torch.int32,), 1)
+    check(2 <= offsets.numel() <= MAX_EXPERTS + 1, f"offsets must have 2 to {MAX_EXPERTS + 1} entries")
+    check(offsets.is_contiguous(), "offsets must be contiguous")
+    return offsets.numel() - 1, offsets.data_ptr()
+
+
+def quantize(x, fmt: str = "e4m3", stream=None) -> Matrix:
+    """x [rows, cols] (bfloat16, float16 or float32, any row stride) in blocks of 128 along its rows."""
+    f = _format(fmt)
+    _input("x", x)
+    rows, cols = x.shape
+    with on(stream, x):
+        x, pitch = rows_of(x)
+        data, scales = _empty((), rows, cols, x.device)
+        call("zc_fp8_quantize", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, f, data.data_ptr(), scales.data_ptr(),
+             current())
+    return Matrix(data, scales, cols, fmt)
+
+
+def quantize_columns(x, offsets=None, fmt: str = "e4m3", stream=None) -> Matrix:
+    """The transpose of x [rows, cols] in blocks of 128 of each group's rows, each group starting a block of its own.
+
+    The result has `cols` rows; its ``offsets`` hold the first block of each group.  Blocks behind the last group's
+    are zeros."""
+    f = _format(fmt)
+    groups, at = _offsets(offsets)
+    _input("x", x)
+    rows, cols = x.shape
+    with on(stream, x, offsets):
+        x, pitch = rows_of(x)
+        wide = fn("zc_fp8_column_blocks")(rows, groups) * BLOCK
+        data, scales = _empty((), cols, wide, x.device)
+        starts = torch.empty(groups + 1, dtype=torch.int32, device=x.device)
+        call("zc_fp8_quantize_columns", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, groups, at, f,
+             data.data_ptr(), scales.data_ptr(), starts.data_ptr(), current())
+    return Matrix(data, scales, wide, fmt, starts)
+
+
+def quantize_weight(w, fmt: str = "e4m3", transposed: bool = True, stream=None) -> tuple[Matrix, Matrix | None]:
+    """Weights [n, k] or [experts, n, k] in blocks of 128 x 128, and (with `transposed`) the same values transposed."""
+    f = _format(fmt)
+    on_device("w", w, tuple(TYPES))
+    check(w.dim() in (2, 3) and min(w.shape) >= 1, f"w must be [n, k] or [experts, n, k], got {tuple(w.shape)}")
+    lead, n, k = w.shape[:-2], *w.shape[-2:]
+    groups = lead[0] if lead else 1
+    check(groups <= MAX_EXPERTS, f"at most {MAX_EXPERTS} experts")
+    with on(stream, w):
+        w = w.contiguous()
+        data, scales = _empty(lead, n, k, w.device)
+        data_t, scales_t = _empty(lead, k, n, w.device) if transposed else (None, None)
+        call("zc_fp8_quantize_weight", w.data_ptr(), TYPES[w.dtype], groups, n, k, f, data.data_ptr(),
+             scales.data_ptr(), data_t.data_ptr() if transposed else None, scales_t.data_ptr() if transposed else None,
+             current())
+    return Matrix(data, scales, k, fmt), Matrix(data_t, scales_t, n, fmt) if transposed else None
+
+
+def _out_type(dtype):
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {dtype}")
+    return TYPES[dtype]
+
+
+def matmul(a: Matrix, b: Matrix, offsets=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """a [rows, k] times the transpose of its group's b [n, k]: [rows, n], zeros for rows behind the last group.
+
+    b holds one matrix for each group (data [groups, n, pitch]), or a single one without offsets."""
+    t = _out_type(out_dtype)
+    groups, at = _offsets(offsets)
+    on_device("a", a.data, None, 2)
+    on_device("b", b.data)
+    check(a.cols == b.cols and a.cols >= 1, f"a has rows of {a.cols} values, b of {b.cols}")
+    check((b.data.shape[0] if b.data.dim() == 3 else 1) == groups, f"b must hold {groups} matrices, got {tuple(b.data.shape)}")
+    rows, n = a.rows, b.rows
+    with on(stream, a.data, a.scales, b.data, b.scales, offsets):
+        out = torch.empty((rows, n), dtype=out_dtype, device=a.data.device)
+        call("zc_fp8_matmul", a.data.data_ptr(), a.scales.data_ptr(), FORMATS[a.fmt], rows, b.data.data_ptr(),
+             b.scales.data_ptr(), FORMATS[b.fmt], groups, n, a.cols, at, out.data_ptr(), n, t, current())
+    return out
+
+
+def weight_grad(dy: Matrix, x: Matrix, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The gradient of matmul's weights, [groups, n, k], from quantize_columns of dy [rows, n] and x [rows, k]
+    (with the same offsets); zeros for a group without rows."""
+    t = _out_type(out_dtype)
+    check(dy.offsets is not None and x.offsets is not None, "dy and x must come from quantize_columns")
+    on_device("dy", dy.data, None, 2)
+    on_device("x", x.data, None, 2)
+    check(dy.cols == x.cols and dy.offsets.numel() == x.offsets.numel(), "dy and x must have the same groups")
+    groups = x.offsets.numel() - 1
+    with on(stream, dy.data, dy.scales, x.data, x.scales, x.offsets):
+        out = torch.empty((groups, dy.rows, x.rows), dtype=out_dtype, device=x.data.device)
+        call("zc_fp8_weight_grad", dy.data.data_ptr(), dy.scales.data_ptr(), FORMATS[dy.fmt], x.data.data_ptr(),
+             x.scales.data_ptr(), FORMATS[x.fmt], x.cols // BLOCK, groups, dy.rows, x.rows, x.offsets.data_ptr(),
+             out.data_ptr(), t, current())
+    return out
