@@ -1,0 +1,116 @@
+// ex_tcgen05.cuh -- PTX wrappers for the tensor cores (tcgen05), tensor memory and TMA tile loads.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "ex_common.cuh"
+
+namespace zc {
+namespace ex {
+
+// ------------------------------------------------------------------ bounded waits
+
+// Nanoseconds after which a wait gives up: far beyond any product's run time.
+constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for a phase of `bar`; false when the limit ran out or another wait of the CTA gave up.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile unsigned* failed) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long start = now_ns();
+  for (unsigned i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i % 256 == 0 && (*failed || now_ns() - start > kWaitLimitNs)) {
+      *failed = 1;
+      return false;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ TMA tile loads (this CTA's memory)
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ------------------------------------------------------------------ tensor memory and products
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* smem_result, unsigned columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_result)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, unsigned columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void tcgen05_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptors.  Operand tiles: rows of 128 bytes, 128-byte swizzle, groups
+// of 8 rows 1024 bytes apart.  Scale chunks: no swizzle, 8-row core matrices of 16-byte rows,
+// 128 bytes apart.
+constexpr uint64_t kDescVersion = 1ull << 46;
+__device__ __forceinline__ uint64_t operand_desc(uint32_t smem) {
+  return (smem >> 4) | (uint64_t(1024 >> 4) << 32) | kDescVersion | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t scales_desc(uint32_t smem) {
+  return (smem >> 4) | (uint64_t(128 >> 4) << 32) | kDescVersion;
+}
+
+// Instruction descriptor of a block-scaled 8-bit product (128 x n, K = 32, both operands K-major,
+// power-of-two scales); the scale byte of the word is picked by `byte` for both operands.
+__device__ __forceinline__ uint32_t product_desc(int a_fmt, int b_fmt, int n) {
+  return (static_cast<uint32_t>(a_fmt) << 7) | (static_cast<uint32_t>(b_fmt) << 10) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (uint32_t(128 >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t with_scale_byte(uint32_t desc, unsigned byte) {
+  return desc | (byte << 4) | (byte << 29);
+}
+
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t a_scales,
+                                        uint32_t b_scales, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"(a_scales), "r"(b_scales), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// 32 rows x 16 bytes of shared memory to 4 columns, repeated in the four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+// Arrives at `bar` once every tcgen05 operation this thread issued before is done.
+__device__ __forceinline__ void commit_to(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+}  // namespace ex
+}  // namespace zc
