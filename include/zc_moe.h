@@ -47,8 +47,8 @@ extern "C" {
  * offsets[e + 1] - 1 belong to expert e, and rows from offsets[experts] on to no expert.
  * Rows are `hidden` values of one type; a pitch is the distance between rows in values. */
 
-/* Bytes of workspace that zc_moe_sort and zc_moe_dispatch need.  Pure host function; 0 when an argument is out
- * of range. */
+/* Bytes of workspace that zc_moe_sort and zc_moe_dispatch need: 0 for small calls (the workspace
+ * may then be null) and when an argument is out of range.  Pure host function. */
 size_t zc_moe_sort_workspace(size_t slots, int experts);
 
 /* position and offsets from the ids (id_bytes 4 or 8: signed integers of that size).

@@ -54,22 +54,29 @@ def check(ok, what):
         raise ValueError(what)
 
 
-def on_device(name, t, dtypes=None, dim=None):
-    """A CUDA tensor of the current device, of one of `dtypes`, with `dim` dimensions."""
+def on_device(name, t, device, dtypes=None, dim=None):
+    """Checks for a CUDA tensor of device number `device` (None: the current one), of one of `dtypes`, with `dim`
+    dimensions; returns the device number."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {', '.join(str(d) for d in dtypes)}")
-    check(dim is None or t.dim() == dim, f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
-    check(t.device.index == torch.cuda.current_device(), f"{name} is on {t.device}, not on the current device")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
+    if device is None:
+        device = torch.cuda.current_device()
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return device
 
 
 def rows_of(t):
     """(tensor, pitch): `t` as rows of contiguous values a pitch apart (copied when it is not laid out so)."""
     rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        t = t.contiguous()
-    return t, (t.stride(0) if rows > 1 else cols)
+    pitch, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and pitch < cols):
+        t, pitch = t.contiguous(), cols
+    return t, (pitch if rows > 1 else cols)
 
 
 _same_stream = contextlib.nullcontext()
@@ -86,5 +93,6 @@ def on(stream, *used):
     return torch.cuda.stream(stream)
 
 
-def current():
-    return torch.cuda.current_stream().cuda_stream
+def current(device):
+    """The handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device)

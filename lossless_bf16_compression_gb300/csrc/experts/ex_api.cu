@@ -47,6 +47,19 @@ bool slots_ok(size_t tokens, int k, int experts) {
   return k >= 1 && k <= ZC_MOE_MAX_K && groups_ok(experts) && tokens <= ZC_MOE_MAX_SLOTS / static_cast<size_t>(k);
 }
 
+int check_sort(const void* ids, int id_bytes, size_t tokens, int k, int experts, const int* position,
+               const int* offsets, const void* workspace) {
+  if (!slots_ok(tokens, k, experts) || (id_bytes != 4 && id_bytes != 8)) return ZC_ERR_INVALID_ARG;
+  const size_t slots = tokens * k, scratch = ex::sort_workspace(slots, experts);
+  if (!offsets || (scratch && !workspace) || (slots && (!ids || !position))) return ZC_ERR_INVALID_ARG;
+  if (!aligned(ids, id_bytes) || !aligned(position, 4) || !aligned(offsets, 4) || !aligned(workspace, 16))
+    return ZC_ERR_MISALIGNED;
+  if (clash({{position, 4 * slots}, {offsets, 4 * size_t(experts + 1)}, {workspace, scratch}},
+            {{ids, id_bytes * slots}}))
+    return ZC_ERR_INVALID_ARG;
+  return ZC_OK;
+}
+
 int finish(cudaError_t err) {
   if (err == cudaSuccess) return ZC_OK;
   cudaGetLastError();  // the error is the call's: it does not stay behind
@@ -64,14 +77,9 @@ size_t zc_moe_sort_workspace(size_t slots, int experts) {
 
 int zc_moe_sort(const void* ids, int id_bytes, size_t tokens, int k, int experts, int* position, int* offsets,
                 void* workspace, cudaStream_t stream) {
-  if (!slots_ok(tokens, k, experts) || (id_bytes != 4 && id_bytes != 8)) return ZC_ERR_INVALID_ARG;
+  const int rc = check_sort(ids, id_bytes, tokens, k, experts, position, offsets, workspace);
+  if (rc != ZC_OK) return rc;
   const size_t slots = tokens * k;
-  if (!offsets || !workspace || (slots && (!ids || !position))) return ZC_ERR_INVALID_ARG;
-  if (!aligned(ids, id_bytes) || !aligned(position, 4) || !aligned(offsets, 4) || !aligned(workspace, 16))
-    return ZC_ERR_MISALIGNED;
-  if (clash({{position, 4 * slots}, {offsets, 4 * size_t(experts + 1)}, {workspace, zc_moe_sort_workspace(slots, experts)}},
-            {{ids, id_bytes * slots}}))
-    return ZC_ERR_INVALID_ARG;
   return finish(ex::launch_sort(ids, id_bytes, slots, experts, position, offsets, workspace, stream));
 }
 
@@ -88,9 +96,14 @@ int zc_moe_dispatch(const void* x, size_t x_pitch, int type, const void* ids, in
              {ids, id_bytes * slots},
              {position, 4 * slots},
              {offsets, 4 * size_t(experts + 1)},
-             {workspace, zc_moe_sort_workspace(slots, experts)}}))
+             {workspace, ex::sort_workspace(slots, experts)}}))
     return ZC_ERR_INVALID_ARG;
-  const int rc = zc_moe_sort(ids, id_bytes, tokens, k, experts, position, offsets, workspace, stream);
+  int rc = check_sort(ids, id_bytes, tokens, k, experts, position, offsets, workspace);
+  if (rc != ZC_OK) return rc;
+  if (ex::small_dispatch(slots))
+    return finish(ex::launch_small_dispatch({tokens, hidden, k, experts, type}, ids, id_bytes, x, x_pitch, rows,
+                                            rows_pitch, position, offsets, stream));
+  rc = finish(ex::launch_sort(ids, id_bytes, slots, experts, position, offsets, workspace, stream));
   if (rc != ZC_OK || tokens == 0) return rc;
   DeviceInfo dev;
   if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);

@@ -40,6 +40,35 @@ union Pack {
   __device__ Pack() {}
 };
 
+// A load that happens only where `on` is set, zeros elsewhere: a predicated instruction, not a
+// branch, so that a thread's loads go out together.  For memory no one writes during the kernel.
+template <int B>
+__device__ __forceinline__ typename Bytes<B>::type load_if(const void* p, bool on);
+template <>
+__device__ __forceinline__ uint4 load_if<16>(const void* p, bool on) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"(static_cast<int>(on)));
+  return v;
+}
+template <>
+__device__ __forceinline__ uint32_t load_if<4>(const void* p, bool on) {
+  uint32_t v = 0;
+  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}"
+      : "+r"(v)
+      : "l"(p), "r"(static_cast<int>(on)));
+  return v;
+}
+template <>
+__device__ __forceinline__ unsigned short load_if<2>(const void* p, bool on) {
+  unsigned short v = 0;
+  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+      : "+h"(v)
+      : "l"(p), "r"(static_cast<int>(on)));
+  return v;
+}
+
 // The widest vector that every one of these row sets allows: 16 bytes, else 4, else one value.
 inline int vector_bytes(size_t element, size_t row_values, std::initializer_list<const void*> bases,
                         std::initializer_list<size_t> pitches) {
@@ -84,6 +113,10 @@ cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts
                         void* workspace, cudaStream_t stream);
 cudaError_t launch_dispatch(const RowShape& s, const void* x, size_t x_pitch, void* rows, size_t rows_pitch,
                             const int* position, const int* offsets, int* status, cudaStream_t stream);
+// Few slots: the sort and the dispatch in one launch, without a workspace.
+bool small_dispatch(size_t slots);
+cudaError_t launch_small_dispatch(const RowShape& s, const void* ids, int id_bytes, const void* x, size_t x_pitch,
+                                  void* rows, size_t rows_pitch, int* position, int* offsets, cudaStream_t stream);
 cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitch, const float* weights,
                            const int* position, const int* offsets, void* out, size_t out_pitch, int* status,
                            cudaStream_t stream);

@@ -1,8 +1,6 @@
 // ex_fp8.cuh -- the 8-bit block rule: scale, rounding, and the scales' layout.
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "ex_common.cuh"
 
 namespace zc {
@@ -43,18 +41,6 @@ __device__ __forceinline__ bool finite_bits(uint32_t bits) { return (bits & 0x7F
 __device__ __forceinline__ uint32_t finite_magnitude(float v) {
   const uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
   return m < 0x7F800000u ? m : 0u;
-}
-__device__ __forceinline__ unsigned round8(float v, float inv, int fmt) {
-  return isfinite(v) ? round8x2(v * inv, 0.f, fmt) & 0xFFu : nonfinite8(v, fmt);
-}
-
-// 2^(byte - 127) as fp32, byte in [0, 254].
-__device__ __forceinline__ float scale_value(unsigned byte) {
-  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x400000u);
-}
-__device__ __forceinline__ float value8(unsigned byte, int fmt) {
-  const __nv_fp8_interpretation_t f = fmt == ZC_FP8_E4M3 ? __NV_E4M3 : __NV_E5M2;
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), f)));
 }
 
 }  // namespace ex

@@ -1,159 +1,342 @@
 // ex_quantize.cu -- rows, columns of row groups, and weights rounded to 8 bits in blocks of 128.
-// Bound by HBM: each input value is read once and each 8-bit value written once.
+// Bound by HBM: each input value is read once, into registers, where its block's largest
+// magnitude is found and the values are rounded, and each 8-bit value is written once.
+#include <initializer_list>
+
 #include "ex_fp8.cuh"
 
 namespace zc {
 namespace ex {
 namespace {
 
-// One warp a block of 128 values of a row; lane l takes values l, l + 32, ...
+// Eight consecutive values of a row as they lie in memory, zeros past `left` values (none where left
+// <= 0).  Vec: the address allows 16-byte loads.
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, size_t pitch, size_t rows, size_t cols,
-                                                       int fmt, uint8_t* __restrict__ values,
-                                                       uint8_t* __restrict__ scales) {
-  const int lane = threadIdx.x % 32;
-  const size_t blocks = ceil_div(cols, kBlock), words = ceil_div(blocks, 4);
-  const size_t item = static_cast<size_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (item >= rows * words * 4) return;
-  const size_t r = item / (words * 4), b = item % (words * 4);
-  if (b >= blocks) {
-    if (lane == 0) scales[scale_at(r, b, rows)] = 127;
-    return;
+union Raw8 {
+  uint4 q[sizeof(T) / 2];
+  typename Bytes<sizeof(T)>::type bits[8];
+  T v[8];
+  __device__ Raw8() {}
+};
+template <typename T, bool Vec>
+__device__ __forceinline__ void load8(const T* at, int left, Raw8<T>& r) {
+  if (Vec) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+      r.q[i] = load_if<16>(at + i * (16 / sizeof(T)), left >= 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.bits[i] = load_if<sizeof(T)>(at + i, i < left);
   }
-  float v[4];
+}
+// After all of a thread's vector loads: the values of a row's end that is not a whole vector.
+template <typename T, bool Vec>
+__device__ __forceinline__ void load_end(const T* at, int left, Raw8<T>& r) {
+  if (Vec && left > 0 && left < 8)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.bits[i] = load_if<sizeof(T)>(at + i, i < left);
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_float(r.v[i]);
+}
+
+// The bits of the largest finite magnitude of eight values.
+__device__ __forceinline__ uint32_t magnitude8(const float (&v)[8]) {
   uint32_t m = 0;
-  for (int i = 0; i < 4; ++i) {
-    const size_t c = b * kBlock + i * 32 + lane;
-    v[i] = c < cols ? to_float(x[r * pitch + c]) : 0.f;
-    m = max(m, finite_magnitude(v[i]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  if (!finite_bits(m)) {  // Inf or NaN among them: look again without them
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(v[i]));
   }
-  m = __reduce_max_sync(~0u, m);
-  const int s = block_exponent(m, fmt);
-  for (int i = 0; i < 4; ++i)
-    values[(r * blocks + b) * kBlock + i * 32 + lane] = round8(v[i], inverse_scale(s), fmt);
-  if (lane == 0) scales[scale_at(r, b, rows)] = s + 127;
+  return m;
 }
 
-// block_offsets[g] = blocks of the groups before g.
-__global__ void block_offsets_kernel(const int* __restrict__ offsets, int rows, int groups, int capacity,
-                                     int* __restrict__ block_offsets, int* status) {
-  int at = 0;
-  if (offsets && offsets[0] != 0) set_error(status, ZC_ERR_CORRUPT);
-  for (int g = 0; g < groups; ++g) {
-    block_offsets[g] = at;
+// Four values times f rounded, the first in the low byte.
+template <int Fmt>
+__device__ __forceinline__ uint32_t round8x4(float a, float b, float c, float d, float f) {
+  uint32_t r = round8x2(a * f, b * f, Fmt) | static_cast<uint32_t>(round8x2(c * f, d * f, Fmt)) << 16;
+  // an infinity or NaN does not go through the saturating conversion
+  const auto fix = [&](float v, int i) {
+    if (!isfinite(v)) r = (r & ~(0xFFu << (8 * i))) | nonfinite8(v, Fmt) << (8 * i);
+  };
+  if (!(isfinite(a) && isfinite(b) && isfinite(c) && isfinite(d))) {
+    fix(a, 0);
+    fix(b, 1);
+    fix(c, 2);
+    fix(d, 3);
+  }
+  return r;
+}
+
+// A warp takes four blocks (one scale word) of each of R rows: lane l holds values 8l .. 8l + 7
+// of the first two blocks and of the last two, so 16 lanes share a block.  CTA: 8 R rows, whose
+// scale words lie next to each other.  With R = 4 a lane has 128 bytes of 16-bit input in flight.
+constexpr int kRowWarps = 8;
+template <typename T, bool Vec, int Fmt, int R>
+__global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __restrict__ x, size_t pitch, size_t rows,
+                                                                  int cols, unsigned words,
+                                                                  uint8_t* __restrict__ values,
+                                                                  uint32_t* __restrict__ scales) {
+  const int lane = threadIdx.x % 32;
+  const unsigned word = blockIdx.x % words;
+  const size_t r0 = (static_cast<size_t>(blockIdx.x / words) * kRowWarps + threadIdx.x / 32) * R;
+  const int blocks = (cols + kBlock - 1) / kBlock, wide = blocks * kBlock;
+  const int c0 = static_cast<int>(word) * 4 * kBlock + lane * 8;
+  Raw8<T> raw[R][2];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + h * 2 * kBlock;
+      load8<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < rows ? cols - c : 0, raw[i][h]);
+    }
+  if (Vec && cols % 8)
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + h * 2 * kBlock;
+        load_end<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < rows ? cols - c : 0, raw[i][h]);
+      }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const size_t r = r0 + i;
+    if (r >= rows) break;  // the whole warp
+    int s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float a[8];
+      unpack8(raw[i][h], a);
+      uint32_t m = magnitude8(a);
+#pragma unroll
+      for (int d = 8; d; d /= 2) m = max(m, __shfl_xor_sync(~0u, m, d));
+      s[h] = block_exponent(m, Fmt);
+      const float f = inverse_scale(s[h]);
+      const uint2 q = make_uint2(round8x4<Fmt>(a[0], a[1], a[2], a[3], f),
+                                 round8x4<Fmt>(a[4], a[5], a[6], a[7], f));
+      const int c = c0 + h * 2 * kBlock;
+      if (c < wide) *reinterpret_cast<uint2*>(values + r * wide + c) = q;
+    }
+    // lanes 0 and 16 hold the exponents of blocks 0, 2 and 1, 3 (0 for a block past the last)
+    const uint32_t even = (s[0] + 127) | (s[1] + 127) << 16;
+    const uint32_t odd = __shfl_sync(~0u, even, 16);
+    if (lane == 0) scales[word * rows + r] = even | odd << 8;
+  }
+}
+
+// block_offsets[g] = blocks of the groups before g, by one CTA of 1024 threads.
+__global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restrict__ offsets, int rows, int groups,
+                                                             int* __restrict__ block_offsets, int* status) {
+  __shared__ int sums[32];
+  const int g = threadIdx.x, lane = g % 32, warp = g / 32;
+  int n = 0;
+  if (g < groups) {
     const int a = offsets ? offsets[g] : 0, z = offsets ? offsets[g + 1] : rows;
-    if (a < 0 || z < a || z > rows) set_error(status, ZC_ERR_CORRUPT);
-    else at = min(capacity, at + (z - a + kBlock - 1) / kBlock);
+    if (a < 0 || z < a || z > rows || (g == 0 && a != 0)) set_error(status, ZC_ERR_CORRUPT);
+    else n = (z - a + kBlock - 1) / kBlock;
   }
-  block_offsets[groups] = at;
+  int incl = n;
+  for (int d = 1; d < 32; d *= 2) {
+    const int u = __shfl_up_sync(~0u, incl, d);
+    if (lane >= d) incl += u;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int before = incl - n;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  if (g < groups) block_offsets[g] = before;
+  if (g == groups - 1) block_offsets[groups] = before + n;
+  let_next_start();
 }
 
-// One CTA of 128 threads a block of 128 rows and 32 columns.
-template <typename T>
-__global__ void __launch_bounds__(128) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, size_t rows,
-                                                               size_t cols, int groups,
-                                                               const int* __restrict__ offsets, int fmt,
-                                                               size_t capacity, uint8_t* __restrict__ values,
+// ------------------------------------------------------------------ 128 x 128 tiles
+//
+// 256 threads; thread (row group rg = tid / 16, column group cg = tid % 16) holds rows 8 rg .. 8 rg + 7 of
+// columns 8 cg .. 8 cg + 7: a row of the tile is read as 16 neighbouring vectors.
+
+struct TileShared {
+  alignas(16) uint2 turned[kBlock * 16];  // [column][unit of 8 rows], the unit at place unit ^ (column / 8)
+  alignas(16) uint32_t amax[16][kBlock];
+  float inverse[kBlock];
+};
+
+// The tile's transpose by way of shared memory: column c's bytes of rows 8 rg .. as one unit.  The
+// places are chosen so that the 16 column groups of a store, and the 8 lanes of a load, hit
+// different banks.
+__device__ __forceinline__ void put_column(TileShared& s, int c, int rg, uint2 v) { s.turned[c * 16 + (rg ^ (c / 8))] = v; }
+// Rows 16 i .. 16 i + 15 of column c.
+__device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
+  const int x = c / 8;
+  const uint4 v = reinterpret_cast<const uint4*>(s.turned)[c * 8 + (i ^ (x / 2))];
+  return x % 2 ? make_uint4(v.z, v.w, v.x, v.y) : v;
+}
+
+template <typename T, bool Vec, int Fmt>
+__global__ void __launch_bounds__(256) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
+                                                               int cols, int groups, const int* __restrict__ offsets,
+                                                               int capacity, uint8_t* __restrict__ values,
                                                                uint8_t* __restrict__ scales,
                                                                const int* __restrict__ block_offsets) {
-  __shared__ uint32_t amax[4][32];
-  __shared__ uint8_t tile[32][kBlock + 4];
+  __shared__ TileShared s;
+  __shared__ int first, last;  // this block's rows
+  const int b = blockIdx.x, tid = threadIdx.x, cg = tid % 16, rg = tid / 16;
+  const int c = blockIdx.y * kBlock + cg * 8;
+  if (tid == 0) first = last = 0;
   wait_for_previous();
-  const int b = blockIdx.x;
-  int g = 0;
-  while (g < groups && b >= block_offsets[g + 1]) ++g;
-  long long begin = 0, end = 0;
-  if (g < groups) {
-    begin = offsets ? offsets[g] : 0;
-    end = offsets ? offsets[g + 1] : rows;
-    begin += static_cast<long long>(b - block_offsets[g]) * kBlock;
-    end = min(end, static_cast<long long>(rows));
-    if (begin < 0) end = begin;
-  }
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const size_t c = static_cast<size_t>(blockIdx.y) * 32 + lane;
-  float v[32];
-  uint32_t m = 0;
-  for (int i = 0; i < 32; ++i) {
-    const long long r = begin + warp * 32 + i;
-    v[i] = c < cols && r < end ? to_float(x[r * pitch + c]) : 0.f;
-    m = max(m, finite_magnitude(v[i]));
-  }
-  amax[warp][lane] = m;
   __syncthreads();
-  for (int w = 0; w < 4; ++w) m = max(m, amax[w][lane]);
-  const int s = block_exponent(m, fmt);
-  for (int i = 0; i < 32; ++i) tile[lane][warp * 32 + i] = round8(v[i], inverse_scale(s), fmt);
-  if (warp == 0 && c < cols) scales[scale_at(c, b, cols)] = s + 127;
-  if (blockIdx.x == capacity - 1 && warp == 0 && c < cols)
-    for (size_t q = capacity; q % 4; ++q) scales[scale_at(c, q, cols)] = 127;
+  for (int g = tid; g < groups; g += 256) {
+    const int b0 = block_offsets[g];
+    if (b0 <= b && b < block_offsets[g + 1]) {
+      const long long a = (offsets ? offsets[g] : 0) + static_cast<long long>(b - b0) * kBlock;
+      const int z = offsets ? offsets[g + 1] : rows;
+      // (a group with bad starts has no blocks)
+      first = static_cast<int>(a);
+      last = static_cast<int>(min(static_cast<long long>(z), a + kBlock));
+    }
+  }
   __syncthreads();
-  for (int i = warp; i < 32; i += 4) {
-    const size_t row = static_cast<size_t>(blockIdx.y) * 32 + i;
-    if (row < cols)
-      reinterpret_cast<uint32_t*>(values + (row * capacity + b) * kBlock)[lane] =
-          *reinterpret_cast<const uint32_t*>(&tile[i][lane * 4]);
+  Raw8<T> raw[8];
+  float v[8][8];
+  const long long r0 = static_cast<long long>(first) + rg * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load8<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < last ? cols - c : 0, raw[i]);
+  if (Vec && cols % 8)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_end<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < last ? cols - c : 0, raw[i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) unpack8(raw[i], v[i]);
+  uint32_t most[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float column[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
+    most[j] = magnitude8(column);
+  }
+  uint4* to = reinterpret_cast<uint4*>(&s.amax[rg][cg * 8]);
+  to[0] = make_uint4(most[0], most[1], most[2], most[3]);
+  to[1] = make_uint4(most[4], most[5], most[6], most[7]);
+  __syncthreads();
+  if (tid < kBlock) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, s.amax[i][tid]);
+    const int e = block_exponent(m, Fmt);
+    s.inverse[tid] = inverse_scale(e);
+    const size_t row = static_cast<size_t>(blockIdx.y) * kBlock + tid;
+    if (row < static_cast<size_t>(cols)) {
+      scales[scale_at(row, b, cols)] = static_cast<uint8_t>(e + 127);
+      if (b == capacity - 1)
+        for (int q = capacity; q % 4; ++q) scales[scale_at(row, q, cols)] = 127;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float f = s.inverse[cg * 8 + j];
+    put_column(s, cg * 8 + j, rg,
+               make_uint2(round8x4<Fmt>(v[0][j], v[1][j], v[2][j], v[3][j], f),
+                          round8x4<Fmt>(v[4][j], v[5][j], v[6][j], v[7][j], f)));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int column = i * 32 + tid / 8, part = tid % 8;
+    const size_t row = static_cast<size_t>(blockIdx.y) * kBlock + column;
+    if (row < static_cast<size_t>(cols))
+      reinterpret_cast<uint4*>(values + (row * capacity + b) * kBlock)[part] = get_column(s, column, part);
   }
 }
 
-// One CTA a 128 x 128 block of a weight; the transpose goes through shared memory.
-template <typename T>
-__global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restrict__ w, size_t rows, size_t cols,
-                                                              int fmt, uint8_t* __restrict__ values,
+// One scale for the tile; its rows are written from registers, its transpose through shared memory.
+template <typename T, bool Vec, int Fmt>
+__global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restrict__ w, int rows, int cols,
+                                                              uint8_t* __restrict__ values,
                                                               uint8_t* __restrict__ scales,
                                                               uint8_t* __restrict__ values_t,
                                                               uint8_t* __restrict__ scales_t) {
-  __shared__ uint8_t tile[kBlock][kBlock + 4];
-  __shared__ uint32_t amax[8];
-  const size_t rb = ceil_div(rows, kBlock), cb = ceil_div(cols, kBlock);
-  const size_t br = blockIdx.y, bc = blockIdx.x, g = blockIdx.z;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  __shared__ TileShared s;
+  const int rb = (rows + kBlock - 1) / kBlock, cb = (cols + kBlock - 1) / kBlock;
+  const int bc = blockIdx.x, br = blockIdx.y, tid = threadIdx.x, cg = tid % 16, rg = tid / 16;
+  const size_t g = blockIdx.z;
+  const int c = bc * kBlock + cg * 8;
   w += g * rows * cols;
-  const auto load = [&](int i, int q) {
-    const size_t r = br * kBlock + i, c = bc * kBlock + q * 32 + lane;
-    return r < rows && c < cols ? to_float(w[r * cols + c]) : 0.f;
-  };
+  Raw8<T> raw[8];
+  float v[8][8];
   uint32_t m = 0;
-  for (int i = warp; i < kBlock; i += 8)
-    for (int q = 0; q < 4; ++q) m = max(m, finite_magnitude(load(i, q)));
+  const int r0 = br * kBlock + rg * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    load8<T, Vec>(w + static_cast<size_t>(r0 + i) * cols + c, r0 + i < rows ? cols - c : 0, raw[i]);
+  if (Vec && cols % 8)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      load_end<T, Vec>(w + static_cast<size_t>(r0 + i) * cols + c, r0 + i < rows ? cols - c : 0, raw[i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) unpack8(raw[i], v[i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, magnitude8(v[i]));
   m = __reduce_max_sync(~0u, m);
-  if (lane == 0) amax[warp] = m;
+  if (tid % 32 == 0) s.amax[0][tid / 32] = m;
   __syncthreads();
-  for (int i = 0; i < 8; ++i) m = max(m, amax[i]);
-  const int s = block_exponent(m, fmt);
-  uint8_t* v = values + g * rows * cb * kBlock;
-  for (int i = warp; i < kBlock; i += 8)
-    for (int q = 0; q < 4; ++q) {
-      const uint8_t byte = round8(load(i, q), inverse_scale(s), fmt);
-      tile[i][q * 32 + lane] = byte;
-      const size_t r = br * kBlock + i;
-      if (r < rows) v[(r * cb + bc) * kBlock + q * 32 + lane] = byte;
-    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, s.amax[0][i]);
+  const int e = block_exponent(m, Fmt);
+  const float f = inverse_scale(e);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = br * kBlock + rg * 8 + i;
+    if (r < rows)
+      *reinterpret_cast<uint2*>(values + ((g * rows + r) * cb + bc) * kBlock + cg * 8) =
+          make_uint2(round8x4<Fmt>(v[i][0], v[i][1], v[i][2], v[i][3], f),
+                     round8x4<Fmt>(v[i][4], v[i][5], v[i][6], v[i][7], f));
+  }
   // the block's scale for each of its rows (and, behind the last block, the word's empty bytes)
-  const auto put_scales = [&](uint8_t* to, size_t n, size_t first, size_t b, size_t blocks) {
-    to += g * ceil_div(blocks, 4) * 4 * n;
-    for (int i = threadIdx.x; i < kBlock; i += 256)
-      if (first + i < n) {
-        to[scale_at(first + i, b, n)] = s + 127;
-        if (b == blocks - 1)
-          for (size_t q = blocks; q % 4; ++q) to[scale_at(first + i, q, n)] = 127;
-      }
-  };
-  put_scales(scales, rows, br * kBlock, bc, cb);
-  if (values_t == nullptr) return;
-  put_scales(scales_t, cols, bc * kBlock, br, rb);
-  __syncthreads();
-  uint8_t* vt = values_t + g * cols * rb * kBlock;
-  for (int i = warp; i < kBlock; i += 8)
-    for (int q = 0; q < 4; ++q) {
-      const size_t c = bc * kBlock + i;
-      if (c < cols) vt[(c * rb + br) * kBlock + q * 32 + lane] = tile[q * 32 + lane][i];
+  const auto put_scales = [&](uint8_t* to, int n, int block_row, int b, int blocks) {
+    to += g * ((blocks + 3) / 4) * 4 * n;
+    const int row = block_row * kBlock + tid;
+    if (tid < kBlock && row < n) {
+      to[scale_at(row, b, n)] = static_cast<uint8_t>(e + 127);
+      if (b == blocks - 1)
+        for (int q = blocks; q % 4; ++q) to[scale_at(row, q, n)] = 127;
     }
+  };
+  put_scales(scales, rows, br, bc, cb);
+  if (values_t == nullptr) return;
+  put_scales(scales_t, cols, bc, br, rb);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    put_column(s, cg * 8 + j, rg,
+               make_uint2(round8x4<Fmt>(v[0][j], v[1][j], v[2][j], v[3][j], f),
+                          round8x4<Fmt>(v[4][j], v[5][j], v[6][j], v[7][j], f)));
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int column = i * 32 + tid / 8, part = tid % 8;
+    const int row = bc * kBlock + column;
+    if (row < cols)
+      reinterpret_cast<uint4*>(values_t + ((g * cols + row) * rb + br) * kBlock)[part] = get_column(s, column, part);
+  }
 }
 
+// The type, whether 16-byte loads reach every row, and the format, as template arguments.
 template <typename F>
-cudaError_t by_type(int type, F&& f) {
-  return type == ZC_TYPE_FP32 ? f(float{}) : type == ZC_TYPE_FP16 ? f(__half{}) : f(__nv_bfloat16{});
+cudaError_t variant(int type, bool vec, int fmt, F&& f) {
+  using std::integral_constant;
+  const auto with_fmt = [&](auto t, auto v) {
+    return fmt == ZC_FP8_E4M3 ? f(t, v, integral_constant<int, ZC_FP8_E4M3>{})
+                              : f(t, v, integral_constant<int, ZC_FP8_E5M2>{});
+  };
+  const auto with_vec = [&](auto t) {
+    return vec ? with_fmt(t, std::true_type{}) : with_fmt(t, std::false_type{});
+  };
+  return type == ZC_TYPE_FP32 ? with_vec(float{}) : type == ZC_TYPE_FP16 ? with_vec(__half{}) : with_vec(__nv_bfloat16{});
+}
+
+bool vector_rows(const void* x, size_t pitch, int type) {
+  return (reinterpret_cast<uintptr_t>(x) | pitch * type_bytes(type)) % 16 == 0;
 }
 
 }  // namespace
@@ -164,12 +347,18 @@ size_t column_blocks(size_t rows, int groups) {
 
 cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, size_t cols, int fmt, uint8_t* values,
                             uint8_t* scales, cudaStream_t stream) {
-  const size_t items = rows * ceil_div(ceil_div(cols, kBlock), 4) * 4;
-  if (items == 0) return cudaSuccess;
-  return by_type(type, [&](auto t) {
+  const size_t words = ceil_div(cols, 4 * kBlock);
+  return variant(type, vector_rows(x, pitch, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(quantize_kernel<T>, static_cast<unsigned>(ceil_div(items, 8)), 256, 0, stream, false,
-                  static_cast<const T*>(x), pitch, rows, cols, fmt, values, scales);
+    const auto go = [&](auto per_warp) {
+      constexpr int R = per_warp();
+      return launch(quantize_kernel<T, vec(), f(), R>, static_cast<unsigned>(ceil_div(rows, kRowWarps * R) * words),
+                    32 * kRowWarps, 0, stream, false, static_cast<const T*>(x), pitch, rows, static_cast<int>(cols),
+                    static_cast<unsigned>(words), values, reinterpret_cast<uint32_t*>(scales));
+    };
+    // four rows a warp once that still gives every SM a few CTAs; one row a warp below
+    return ceil_div(rows, kRowWarps * 4) * words >= 1024 ? go(std::integral_constant<int, 4>{})
+                                                         : go(std::integral_constant<int, 1>{});
   });
 }
 
@@ -177,15 +366,15 @@ cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_
                                     const int* offsets, int fmt, uint8_t* values, uint8_t* scales, int* block_offsets,
                                     int* status, cudaStream_t stream) {
   const size_t capacity = column_blocks(rows, groups);
-  cudaError_t err = launch(block_offsets_kernel, 1, 1, 0, stream, false, offsets, static_cast<int>(rows), groups,
-                           static_cast<int>(capacity), block_offsets, status);
+  const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, false, offsets, static_cast<int>(rows),
+                                 groups, block_offsets, status);
   if (err != cudaSuccess || capacity == 0) return err;
-  return by_type(type, [&](auto t) {
+  const dim3 grid(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, kBlock)));
+  return variant(type, vector_rows(x, pitch, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(quantize_columns_kernel<T>,
-                  dim3(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, 32))), 128, 0, stream,
-                  true, static_cast<const T*>(x), pitch, rows, cols, groups, offsets, fmt, capacity, values, scales,
-                  block_offsets);
+    return launch(quantize_columns_kernel<T, vec(), f()>, grid, 256, 0, stream, true, static_cast<const T*>(x), pitch,
+                  static_cast<int>(rows), static_cast<int>(cols), groups, offsets, static_cast<int>(capacity), values,
+                  scales, block_offsets);
   });
 }
 
@@ -194,10 +383,10 @@ cudaError_t launch_quantize_weight(const void* w, int type, int groups, size_t r
                                    cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(ceil_div(cols, kBlock)), static_cast<unsigned>(ceil_div(rows, kBlock)),
                   static_cast<unsigned>(groups));
-  return by_type(type, [&](auto t) {
+  return variant(type, vector_rows(w, cols, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(quantize_weight_kernel<T>, grid, 256, 0, stream, false, static_cast<const T*>(w), rows, cols, fmt,
-                  values, scales, values_t, scales_t);
+    return launch(quantize_weight_kernel<T, vec(), f()>, grid, 256, 0, stream, false, static_cast<const T*>(w),
+                  static_cast<int>(rows), static_cast<int>(cols), values, scales, values_t, scales_t);
   });
 }
 

@@ -2,7 +2,8 @@
 // gradients.  The order is a permutation known from the sort, so every kernel here is driven by
 // tokens: a token's row is read (or written) once and its k sorted rows once each, which is all
 // the traffic there is, and every sum over j runs inside one thread in slot order (no atomics).
-// Bound by HBM.
+// Bound by HBM when there are many tokens, by two dependent loads (position, then row) when there
+// are few; so a thread asks for the rows of eight slots before it uses the first.
 #include <initializer_list>
 
 #include "ex_common.cuh"
@@ -11,119 +12,238 @@ namespace zc {
 namespace ex {
 namespace {
 
-// A slot's row, or -1 when the slot has no expert (or its position is out of range, which sets
-// the error and is never used as an address).
-__device__ __forceinline__ int row_of(const int* position, size_t s, size_t slots, int kept, int* status) {
-  const int p = position[s];
-  if (p < 0 || static_cast<size_t>(p) >= slots) {
-    set_error(status, ZC_ERR_CORRUPT);
-    return -2;
-  }
-  return p < kept ? p : -1;
+constexpr int kMaxThreads = 256;
+constexpr int kBatch = 8;  // slots whose rows a thread has in flight
+
+// A position that may be used as an address; reported otherwise.
+__device__ __forceinline__ bool in_range(int p, size_t slots, int* status) {
+  if (p >= 0 && static_cast<size_t>(p) < slots) return true;
+  set_error(status, ZC_ERR_CORRUPT);
+  return false;
 }
 
-// rows[position[t, j]] = x[t].  One CTA a token.
+// How a row's vectors are shared out: `parts` CTAs a row, one vector a thread.
+struct Cut {
+  unsigned parts, threads;
+};
+Cut cut_row(size_t vecs, unsigned most) {
+  const unsigned parts = static_cast<unsigned>((vecs + most - 1) / most);
+  const unsigned each = static_cast<unsigned>((vecs + parts - 1) / parts);
+  return {parts, (each + 31) / 32 * 32};
+}
+
+// Writes this thread's vector of a token to its slots' rows.
+template <typename V>
+__device__ __forceinline__ void spread(const V& v, uint8_t* rows, size_t rows_pitch, int c, const int* position, int k,
+                                       size_t slots, int kept, int* status) {
+  for (int j = 0; j < k; ++j) {
+    const int p = position[j];
+    if (in_range(p, slots, status)) reinterpret_cast<V*>(rows + p * rows_pitch)[c] = p < kept ? v : V{};
+  }
+}
+
+// rows[position[t, j]] = x[t].
 template <int B>
-__global__ void __launch_bounds__(256) dispatch_kernel(const uint8_t* __restrict__ x, size_t x_pitch,
-                                                       uint8_t* __restrict__ rows, size_t rows_pitch, int vecs, int k,
-                                                       size_t slots, const int* __restrict__ position,
-                                                       const int* __restrict__ total, int* status) {
+__global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __restrict__ x, size_t x_pitch,
+                                                               uint8_t* __restrict__ rows, size_t rows_pitch, int vecs,
+                                                               unsigned parts, int k, size_t slots,
+                                                               const int* __restrict__ position,
+                                                               const int* __restrict__ total, int* status) {
   using V = typename Bytes<B>::type;
+  const size_t t = blockIdx.x / parts;
+  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
+  V v{};
+  if (c < vecs) v = reinterpret_cast<const V*>(x + t * x_pitch)[c];  // x does not come from the sort
   wait_for_previous();
-  const size_t t = blockIdx.x;
-  const int kept = *total;
-  for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-    const V v = reinterpret_cast<const V*>(x + t * x_pitch)[c];
+  if (c < vecs) spread(v, rows, rows_pitch, c, position + t * k, k, slots, *total, status);
+}
+
+// Sort and dispatch of few slots in one launch: every CTA counts, for the slots of its token, the
+// slots that come before them -- slots x k comparisons, shared by its threads -- so no CTA waits
+// for another.  At 64 tokens x 8 that is 16 comparisons a thread.
+constexpr size_t kSmallSlots = 1024;
+
+template <typename Id, int B>
+__global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
+    const Id* __restrict__ ids, int slots, int experts, const uint8_t* __restrict__ x, size_t x_pitch,
+    uint8_t* __restrict__ rows, size_t rows_pitch, int vecs, unsigned parts, int k, int* __restrict__ position,
+    int* __restrict__ offsets) {
+  using V = typename Bytes<B>::type;
+  __shared__ short keys[kSmallSlots];
+  __shared__ int place[ZC_MOE_MAX_K];
+  __shared__ int bins[ZC_MOE_MAX_EXPERTS + 1];
+  __shared__ int kept;
+  const int t = static_cast<int>(blockIdx.x / parts), part = static_cast<int>(blockIdx.x % parts);
+  const int c = part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x), lane = threadIdx.x % 32;
+  V v{};
+  if (c < vecs) v = reinterpret_cast<const V*>(x + t * x_pitch)[c];
+  const bool starts = blockIdx.x == 0;  // this CTA writes the offsets as well
+  if (threadIdx.x < ZC_MOE_MAX_K) place[threadIdx.x] = 0;
+  if (threadIdx.x == 0) kept = 0;
+  if (starts)
+    for (int i = threadIdx.x; i <= experts; i += blockDim.x) bins[i] = 0;
+  __syncthreads();
+  int valid = 0;
+  for (int s = threadIdx.x; s < slots; s += blockDim.x) {
+    const Id id = ids[s];
+    const int key = id >= 0 && id < experts ? static_cast<int>(id) : experts;
+    keys[s] = static_cast<short>(key);
+    valid += key < experts;
+    if (starts) atomicAdd(&bins[key], 1);
+  }
+  valid = __reduce_add_sync(~0u, valid);
+  if (lane == 0 && valid) atomicAdd(&kept, valid);
+  __syncthreads();
+  for (int j = 0; j < k; ++j) {
+    const int s = t * k + j, key = keys[s];
+    int before = 0;
+    for (int o = threadIdx.x; o < slots; o += blockDim.x) {
+      const int other = keys[o];
+      before += other < key || (other == key && o < s);
+    }
+    before = __reduce_add_sync(~0u, before);
+    if (lane == 0 && before) atomicAdd(&place[j], before);
+  }
+  __syncthreads();
+  if (part == 0 && static_cast<int>(threadIdx.x) < k) position[t * k + threadIdx.x] = place[threadIdx.x];
+  if (c < vecs)
     for (int j = 0; j < k; ++j) {
-      const int p = position[t * k + j];
-      if (p < 0 || static_cast<size_t>(p) >= slots) {
-        set_error(status, ZC_ERR_CORRUPT);
-        continue;
-      }
+      const int p = place[j];
       reinterpret_cast<V*>(rows + p * rows_pitch)[c] = p < kept ? v : V{};
     }
-  }
-}
-
-// out[t] = sum over j of weights[t, j] rows[position[t, j]].  One CTA a token.
-template <typename T, int B>
-__global__ void __launch_bounds__(256) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
-                                                      const float* __restrict__ weights, uint8_t* __restrict__ out,
-                                                      size_t out_pitch, int vecs, int k, size_t slots,
-                                                      const int* __restrict__ position, const int* __restrict__ total,
-                                                      int* status) {
-  constexpr int N = B / sizeof(T);
-  const size_t t = blockIdx.x;
-  const int kept = *total;
-  for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-    float acc[N] = {};
-    for (int j = 0; j < k; ++j) {
-      const int p = row_of(position, t * k + j, slots, kept, status);
-      if (p < 0) continue;
-      Pack<T, B> v;
-      v.raw = reinterpret_cast<const typename Bytes<B>::type*>(rows + p * rows_pitch)[c];
-      const float w = weights ? weights[t * k + j] : 1.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = fmaf(w, to_float(v.v[i]), acc[i]);
+  if (starts && threadIdx.x < 32) {
+    int before = 0;
+    for (int base = 0; base <= experts; base += 32) {
+      const int e = base + lane;
+      const int n = e <= experts ? bins[e] : 0;
+      int incl = n;
+      for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(~0u, incl, d);
+        if (lane >= d) incl += u;
+      }
+      if (e <= experts) offsets[e] = before + incl - n;
+      before += __shfl_sync(~0u, incl, 31);
     }
-    Pack<T, B> o;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_float<T>(acc[i]);
-    reinterpret_cast<typename Bytes<B>::type*>(out + t * out_pitch)[c] = o.raw;
   }
 }
 
-// d_rows[position[t, j]] = weights[t, j] d_out[t], d_weights[t, j] = <d_out[t], rows[...]>.
-// One CTA a token.
+// out[t] = sum over j of weights[t, j] rows[position[t, j]].
 template <typename T, int B>
-__global__ void __launch_bounds__(256) combine_grad_kernel(
+__global__ void __launch_bounds__(kMaxThreads) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
+                                                              const float* __restrict__ weights,
+                                                              uint8_t* __restrict__ out, size_t out_pitch, int vecs,
+                                                              unsigned parts, int k, size_t slots,
+                                                              const int* __restrict__ position,
+                                                              const int* __restrict__ total, int* status) {
+  constexpr int N = B / sizeof(T);
+  const size_t t = blockIdx.x / parts;
+  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
+  if (c >= vecs) return;
+  const int kept = *total;
+  float acc[N] = {};
+  for (int j0 = 0; j0 < k; j0 += kBatch) {
+    Pack<T, B> v[kBatch];
+    float w[kBatch];
+    int at[kBatch];
+    bool here[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const size_t s = t * k + min(j0 + i, k - 1);
+      at[i] = position[s];
+      w[i] = weights ? weights[s] : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      here[i] = j0 + i < k && in_range(at[i], slots, status) && at[i] < kept;
+      v[i].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(c) * B, here[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        acc[e] = here[i] ? fmaf(w[i], to_float(v[i].v[e]), acc[e]) : acc[e];
+  }
+  Pack<T, B> o;
+#pragma unroll
+  for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[e]);
+  reinterpret_cast<typename Bytes<B>::type*>(out + t * out_pitch)[c] = o.raw;
+}
+
+// d_rows[position[t, j]] = weights[t, j] d_out[t], d_weights[t, j] = <d_out[t], rows[...]>.  One
+// CTA a token: each thread sums its vectors' products, then lanes, then warps, in a fixed order.
+template <typename T, int B>
+__global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
     const uint8_t* __restrict__ d_out, size_t d_out_pitch, const uint8_t* __restrict__ rows, size_t rows_pitch,
     const float* __restrict__ weights, uint8_t* __restrict__ d_rows, size_t d_rows_pitch, float* __restrict__ d_weights,
     int vecs, int k, size_t slots, const int* __restrict__ position, const int* __restrict__ total, int* status) {
   constexpr int N = B / sizeof(T);
   using V = typename Bytes<B>::type;
-  __shared__ float sums[8];
+  __shared__ float sums[kBatch][kMaxThreads / 32];
   const size_t t = blockIdx.x;
-  const int kept = *total;
-  for (int j = 0; j < k; ++j) {
-    const int p = position[t * k + j];
-    const bool ok = p >= 0 && static_cast<size_t>(p) < slots, here = ok && p < kept;
-    if (!ok) set_error(status, ZC_ERR_CORRUPT);
-    const float w = here ? weights[t * k + j] : 0.f;
-    float dot = 0.f;
-    for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-      Pack<T, B> d, r, o;
-      d.raw = reinterpret_cast<const V*>(d_out + t * d_out_pitch)[c];
-      if (here) r.raw = reinterpret_cast<const V*>(rows + p * rows_pitch)[c];
+  const int kept = *total, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int j0 = 0; j0 < k; j0 += kBatch) {
+    int at[kBatch];
+    float w[kBatch], dot[kBatch];
+    bool ok[kBatch], here[kBatch];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        o.v[i] = from_float<T>(here ? w * to_float(d.v[i]) : 0.f);
-        if (here) dot = fmaf(to_float(d.v[i]), to_float(r.v[i]), dot);
-      }
-      if (ok) reinterpret_cast<V*>(d_rows + p * d_rows_pitch)[c] = o.raw;
+    for (int i = 0; i < kBatch; ++i) {
+      const size_t s = t * k + j0 + i;
+      at[i] = j0 + i < k ? position[s] : 0;
+      ok[i] = j0 + i < k && in_range(at[i], slots, status);
+      here[i] = ok[i] && at[i] < kept;
+      w[i] = here[i] ? weights[s] : 0.f;
+      dot[i] = 0.f;
     }
-    for (int m = 16; m; m /= 2) dot += __shfl_xor_sync(~0u, dot, m);
-    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = dot;
+    for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
+      Pack<T, B> d, r[kBatch];
+      d.raw = reinterpret_cast<const V*>(d_out + t * d_out_pitch)[c];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        r[i].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(c) * B, here[i]);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (!ok[i]) continue;
+        Pack<T, B> o;
+        o.raw = V{};
+        if (here[i]) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float g = to_float(d.v[e]);
+            o.v[e] = from_float<T>(w[i] * g);
+            dot[i] = fmaf(g, to_float(r[i].v[e]), dot[i]);
+          }
+        }
+        reinterpret_cast<V*>(d_rows + at[i] * d_rows_pitch)[c] = o.raw;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      for (int m = 16; m; m /= 2) dot[i] += __shfl_xor_sync(~0u, dot[i], m);
+      if (lane == 0) sums[i][warp] = dot[i];
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < k) {
       float s = 0.f;
-      for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += sums[i];
-      d_weights[t * k + j] = s;
+      for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += sums[threadIdx.x][i];
+      d_weights[t * k + j0 + threadIdx.x] = s;
     }
     __syncthreads();
   }
 }
 
 template <typename F>
+cudaError_t by_bytes(int bytes, F&& f) {
+  using std::integral_constant;
+  return bytes == 16  ? f(integral_constant<int, 16>{})
+         : bytes == 4 ? f(integral_constant<int, 4>{})
+                      : f(integral_constant<int, 2>{});
+}
+template <typename F>
 cudaError_t by_type(int type, int bytes, F&& f) {
   using std::integral_constant;
   if (type == ZC_TYPE_FP32)
     return bytes == 16 ? f(float{}, integral_constant<int, 16>{}) : f(float{}, integral_constant<int, 4>{});
-  const auto half = [&](auto t) {
-    return bytes == 16  ? f(t, integral_constant<int, 16>{})
-           : bytes == 4 ? f(t, integral_constant<int, 4>{})
-                        : f(t, integral_constant<int, 2>{});
-  };
+  const auto half = [&](auto t) { return by_bytes(bytes, [&](auto b) { return f(t, b); }); };
   return type == ZC_TYPE_FP16 ? half(__half{}) : half(__nv_bfloat16{});
 }
 
@@ -133,12 +253,34 @@ cudaError_t launch_dispatch(const RowShape& s, const void* x, size_t x_pitch, vo
                             const int* position, const int* offsets, int* status, cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
   const int v = vector_bytes(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
-  const auto run = [&](auto kernel) {
-    return launch(kernel, static_cast<unsigned>(s.tokens), 256, 0, stream, true, static_cast<const uint8_t*>(x),
-                  x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(s.hidden * b / v), s.k,
-                  s.tokens * s.k, position, offsets + s.experts, status);
-  };
-  return v == 16 ? run(dispatch_kernel<16>) : v == 4 ? run(dispatch_kernel<4>) : run(dispatch_kernel<2>);
+  const size_t vecs = s.hidden * b / v;
+  const Cut cut = cut_row(vecs, kMaxThreads);
+  return by_bytes(v, [&](auto bytes) {
+    return launch(dispatch_kernel<bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, cut.threads, 0, stream, true,
+                  static_cast<const uint8_t*>(x), x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b,
+                  static_cast<int>(vecs), cut.parts, s.k, s.tokens * s.k, position, offsets + s.experts, status);
+  });
+}
+
+bool small_dispatch(size_t slots) { return slots > 0 && slots <= kSmallSlots; }
+
+cudaError_t launch_small_dispatch(const RowShape& s, const void* ids, int id_bytes, const void* x, size_t x_pitch,
+                                  void* rows, size_t rows_pitch, int* position, int* offsets, cudaStream_t stream) {
+  const size_t b = type_bytes(s.type);
+  const int v = vector_bytes(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
+  const size_t vecs = s.hidden * b / v;
+  const Cut cut = cut_row(vecs, kMaxThreads);
+  const unsigned threads = cut.threads < 64 ? 64 : cut.threads;  // at least ZC_MOE_MAX_K
+  return by_bytes(v, [&](auto bytes) {
+    const auto go = [&](auto* p) {
+      using Id = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+      return launch(small_dispatch_kernel<Id, bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, threads, 0,
+                    stream, false, p, static_cast<int>(s.tokens * s.k), s.experts, static_cast<const uint8_t*>(x),
+                    x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(vecs), cut.parts, s.k,
+                    position, offsets);
+    };
+    return id_bytes == 8 ? go(static_cast<const long long*>(ids)) : go(static_cast<const int*>(ids));
+  });
 }
 
 cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitch, const float* weights,
@@ -146,11 +288,13 @@ cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitc
                            cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
   const int v = vector_bytes(b, s.hidden, {rows, out}, {rows_pitch, out_pitch});
+  const size_t vecs = s.hidden * b / v;
+  const Cut cut = cut_row(vecs, kMaxThreads);
   return by_type(s.type, v, [&](auto type, auto bytes) {
-    return launch(combine_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens), 256, 0, stream, false,
-                  static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(out),
-                  out_pitch * b, static_cast<int>(s.hidden * b / v), s.k, s.tokens * s.k, position,
-                  offsets + s.experts, status);
+    return launch(combine_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, cut.threads, 0,
+                  stream, false, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
+                  static_cast<uint8_t*>(out), out_pitch * b, static_cast<int>(vecs), cut.parts, s.k, s.tokens * s.k,
+                  position, offsets + s.experts, status);
   });
 }
 
@@ -160,11 +304,13 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
                                 cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
   const int v = vector_bytes(b, s.hidden, {d_out, rows, d_rows}, {d_out_pitch, rows_pitch, d_rows_pitch});
+  const size_t vecs = s.hidden * b / v;
   return by_type(s.type, v, [&](auto type, auto bytes) {
-    return launch(combine_grad_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens), 256, 0, stream, false,
-                  static_cast<const uint8_t*>(d_out), d_out_pitch * b, static_cast<const uint8_t*>(rows),
-                  rows_pitch * b, weights, static_cast<uint8_t*>(d_rows), d_rows_pitch * b, d_weights,
-                  static_cast<int>(s.hidden * b / v), s.k, s.tokens * s.k, position, offsets + s.experts, status);
+    return launch(combine_grad_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens),
+                  cut_row(vecs, kMaxThreads).threads, 0, stream, false, static_cast<const uint8_t*>(d_out),
+                  d_out_pitch * b, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
+                  static_cast<uint8_t*>(d_rows), d_rows_pitch * b, d_weights, static_cast<int>(vecs), s.k,
+                  s.tokens * s.k, position, offsets + s.experts, status);
   });
 }
 

@@ -1,10 +1,12 @@
 // ex_sort.cu -- the place of each slot in the order by expert (a stable counting sort).
 //
 // position[s] = #{s' : key(s') < key(s)} + #{s' < s : key(s') = key(s)}, with key(s) the slot's
-// expert, or `experts` for a slot without one.  One CTA: each warp counts the keys of its own
-// contiguous run of slots, a scan over (key, warp) turns the counts into starts, and each warp
-// walks its run again, 32 slots at a time, giving a slot its key's start plus the number of
-// equal keys before it in the warp.
+// expert, or `experts` for a slot without one.  Each CTA takes a contiguous run of slots: a first
+// kernel counts the keys of every run, a second turns the counts into starts (a run's key starts
+// after all smaller keys and after the same key in the runs before it) and walks the run again,
+// 32 slots of a warp at a time, giving a slot its key's start plus the number of equal keys before it
+// in the warp.  A call of one run needs only the second kernel.  Bound by latency: two launches
+// and a few dependent loads.
 #include "ex_common.cuh"
 
 namespace zc {
@@ -13,6 +15,13 @@ namespace {
 
 constexpr int kSortWarps = 16;
 constexpr int kSortThreads = 32 * kSortWarps;
+constexpr size_t kRunSlots = 1024;  // slots of a run, while there are at most kMaxRuns
+constexpr size_t kMaxRuns = 128;    // every CTA of the second kernel reads every run's counts
+
+size_t runs_of(size_t slots) {
+  const size_t r = (slots + kRunSlots - 1) / kRunSlots;
+  return r < 1 ? 1 : r > kMaxRuns ? kMaxRuns : r;
+}
 
 template <typename Id>
 __device__ __forceinline__ int key_of(const Id* ids, size_t s, int experts) {
@@ -21,26 +30,52 @@ __device__ __forceinline__ int key_of(const Id* ids, size_t s, int experts) {
 }
 
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const Id* __restrict__ ids, int slots, int experts,
-                                                            int* __restrict__ position, int* __restrict__ offsets) {
-  extern __shared__ int counts[];  // [kSortWarps][experts + 1]
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const Id* __restrict__ ids, int slots, int run,
+                                                             int experts, int* __restrict__ counts) {
+  extern __shared__ int bins[];
+  const int keys = experts + 1;
+  const int begin = min(slots, static_cast<int>(blockIdx.x) * run), end = min(slots, begin + run);
+  for (int i = threadIdx.x; i < keys; i += kSortThreads) bins[i] = 0;
+  __syncthreads();
+  for (int s = begin + threadIdx.x; s < end; s += kSortThreads) atomicAdd(&bins[key_of(ids, s, experts)], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < keys; i += kSortThreads) counts[static_cast<size_t>(blockIdx.x) * keys + i] = bins[i];
+  let_next_start();
+}
+
+// counts: [runs][experts + 1] from count_kernel; not read when there is one run.
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const Id* __restrict__ ids, int slots, int run, int runs,
+                                                             int experts, const int* __restrict__ counts,
+                                                             int* __restrict__ position, int* __restrict__ offsets) {
+  extern __shared__ int bins[];  // [kSortWarps][experts + 1]
   __shared__ int warp_sums[kSortWarps];
   __shared__ int carry;
   const int keys = experts + 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int run = (slots + kSortWarps - 1) / kSortWarps;
-  const int begin = min(slots, warp * run), end = min(slots, begin + run);
-  int* mine = counts + warp * keys;
-  for (int i = threadIdx.x; i < kSortWarps * keys; i += kSortThreads) counts[i] = 0;
+  const int first = min(slots, static_cast<int>(blockIdx.x) * run), last = min(slots, first + run);
+  const int part = (last - first + kSortWarps - 1) / kSortWarps;
+  const int begin = min(last, first + warp * part), end = min(last, begin + part);
+  int* mine = bins + warp * keys;
+  for (int i = threadIdx.x; i < kSortWarps * keys; i += kSortThreads) bins[i] = 0;
   if (threadIdx.x == 0) carry = 0;
   __syncthreads();
   for (int s = begin + lane; s < end; s += 32) atomicAdd(&mine[key_of(ids, s, experts)], 1);
+  if (runs > 1) wait_for_previous();
   __syncthreads();
-  // exclusive scan over the keys, and over the warps within a key
   for (int base = 0; base < keys; base += kSortThreads) {
     const int e = base + threadIdx.x;
-    int total = 0;
-    if (e < keys)
-      for (int w = 0; w < kSortWarps; ++w) total += counts[w * keys + e];
+    int total = 0, before = 0;  // of this key: in all the runs, and in the runs before this one
+    if (e < keys) {
+      if (runs > 1) {
+        for (int r = 0; r < runs; ++r) {
+          const int c = counts[static_cast<size_t>(r) * keys + e];
+          total += c;
+          if (r < static_cast<int>(blockIdx.x)) before += c;
+        }
+      } else {
+        for (int w = 0; w < kSortWarps; ++w) total += bins[w * keys + e];
+      }
+    }
     int incl = total;
     for (int d = 1; d < 32; d *= 2) {
       const int v = __shfl_up_sync(~0u, incl, d);
@@ -53,10 +88,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const Id* __restrict
     __syncthreads();
     if (threadIdx.x == kSortThreads - 1) carry = start + total;
     if (e < keys) {
-      offsets[e] = start;
+      if (blockIdx.x == 0) offsets[e] = start;
+      start += before;
       for (int w = 0; w < kSortWarps; ++w) {
-        const int c = counts[w * keys + e];
-        counts[w * keys + e] = start;
+        const int c = bins[w * keys + e];
+        bins[w * keys + e] = start;
         start += c;
       }
     }
@@ -69,31 +105,44 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const Id* __restrict
     if (in) {
       const int key = key_of(ids, s, experts);
       const unsigned same = __match_any_sync(live, key);
-      const int before = __popc(same & ((1u << lane) - 1));
+      const int ahead = __popc(same & ((1u << lane) - 1));
       const int start = mine[key];
       __syncwarp(live);
-      if (before == 0) mine[key] = start + __popc(same);
-      position[s] = start + before;
+      if (ahead == 0) mine[key] = start + __popc(same);
+      position[s] = start + ahead;
     }
     __syncwarp();
   }
+  let_next_start();
 }
 
 }  // namespace
 
-size_t sort_workspace(size_t, int) { return 16; }
+size_t sort_workspace(size_t slots, int experts) {
+  const size_t r = runs_of(slots);
+  return r > 1 ? 4 * r * (static_cast<size_t>(experts) + 1) : 0;
+}
 
-cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts, int* position, int* offsets, void*,
-                        cudaStream_t stream) {
-  const size_t smem = sizeof(int) * kSortWarps * (experts + 1);
-  const auto run = [&](auto kernel, auto* p) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 sizeof(int) * kSortWarps * (ZC_MOE_MAX_EXPERTS + 1));
-    if (err != cudaSuccess) return err;
-    return launch(kernel, 1, kSortThreads, smem, stream, false, p, static_cast<int>(slots), experts, position, offsets);
+cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts, int* position, int* offsets,
+                        void* workspace, cudaStream_t stream) {
+  const int runs = static_cast<int>(runs_of(slots)), run = static_cast<int>((slots + runs - 1) / runs);
+  const int n = static_cast<int>(slots);
+  int* counts = static_cast<int*>(workspace);
+  const size_t row = sizeof(int) * (experts + 1);
+  const auto go = [&](auto* p) {
+    using Id = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+    cudaError_t err = cudaSuccess;
+    if (kSortWarps * row > 48 * 1024)
+      err = cudaFuncSetAttribute(place_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSortWarps * row));
+    if (err == cudaSuccess && runs > 1)
+      err = launch(count_kernel<Id>, runs, kSortThreads, row, stream, false, p, n, run, experts, counts);
+    if (err == cudaSuccess)
+      err = launch(place_kernel<Id>, runs, kSortThreads, kSortWarps * row, stream, runs > 1, p, n, run, runs, experts,
+                   counts, position, offsets);
+    return err;
   };
-  return id_bytes == 8 ? run(sort_kernel<long long>, static_cast<const long long*>(ids))
-                       : run(sort_kernel<int>, static_cast<const int*>(ids));
+  return id_bytes == 8 ? go(static_cast<const long long*>(ids)) : go(static_cast<const int*>(ids));
 }
 
 }  // namespace ex

@@ -68,6 +68,17 @@ class Matrix:
         return self.scales.view(torch.float8_e8m0fnu).float()
 
 
+_ROW_TYPES = tuple(TYPES)
+_INT32 = (torch.int32,)
+
+
+def _made(data, scales, cols, fmt, offsets=None):
+    """A Matrix of this module's own making: its parts fit and are not looked at again."""
+    m = object.__new__(Matrix)
+    m.__dict__.update(data=data, scales=scales, cols=cols, fmt=fmt, offsets=offsets)
+    return m
+
+
 def _pitch(cols):
     return -(-cols // BLOCK) * BLOCK
 
@@ -84,30 +95,34 @@ def _format(fmt):
 
 
 def _input(name, x):
-    on_device(name, x, tuple(TYPES), 2)
-    check(x.shape[1] >= 1, f"{name} must have at least one column")
+    device = on_device(name, x, None, _ROW_TYPES, 2)
+    if x.shape[1] < 1:
+        raise ValueError(f"{name} must have at least one column")
+    return device
 
 
-def _offsets(offsets):
+def _offsets(offsets, device):
     if offsets is None:
         return 1, None
-    on_device("offsets", offsets, (torch.int32,), 1)
-    check(2 <= offsets.numel() <= MAX_EXPERTS + 1, f"offsets must have 2 to {MAX_EXPERTS + 1} entries")
-    check(offsets.is_contiguous(), "offsets must be contiguous")
-    return offsets.numel() - 1, offsets.data_ptr()
+    on_device("offsets", offsets, device, _INT32, 1)
+    if not 2 <= offsets.shape[0] <= MAX_EXPERTS + 1:
+        raise ValueError(f"offsets must have 2 to {MAX_EXPERTS + 1} entries")
+    if not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous")
+    return offsets.shape[0] - 1, offsets.data_ptr()
 
 
 def quantize(x, fmt: str = "e4m3", stream=None) -> Matrix:
     """x [rows, cols] (bfloat16, float16 or float32, any row stride) in blocks of 128 along its rows."""
     f = _format(fmt)
-    _input("x", x)
+    device = _input("x", x)
     rows, cols = x.shape
     with on(stream, x):
         x, pitch = rows_of(x)
         data, scales = _empty((), rows, cols, x.device)
         call("zc_fp8_quantize", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, f, data.data_ptr(), scales.data_ptr(),
-             current())
-    return Matrix(data, scales, cols, fmt)
+             current(device))
+    return _made(data, scales, cols, fmt)
 
 
 def quantize_columns(x, offsets=None, fmt: str = "e4m3", stream=None) -> Matrix:
@@ -116,8 +131,8 @@ def quantize_columns(x, offsets=None, fmt: str = "e4m3", stream=None) -> Matrix:
     The result has `cols` rows; its ``offsets`` hold the first block of each group.  Blocks behind the last group's
     are zeros."""
     f = _format(fmt)
-    groups, at = _offsets(offsets)
-    _input("x", x)
+    device = _input("x", x)
+    groups, at = _offsets(offsets, device)
     rows, cols = x.shape
     with on(stream, x, offsets):
         x, pitch = rows_of(x)
@@ -125,16 +140,16 @@ def quantize_columns(x, offsets=None, fmt: str = "e4m3", stream=None) -> Matrix:
         data, scales = _empty((), cols, wide, x.device)
         starts = torch.empty(groups + 1, dtype=torch.int32, device=x.device)
         call("zc_fp8_quantize_columns", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, groups, at, f,
-             data.data_ptr(), scales.data_ptr(), starts.data_ptr(), current())
-    return Matrix(data, scales, wide, fmt, starts)
+             data.data_ptr(), scales.data_ptr(), starts.data_ptr(), current(device))
+    return _made(data, scales, wide, fmt, starts)
 
 
 def quantize_weight(w, fmt: str = "e4m3", transposed: bool = True, stream=None) -> tuple[Matrix, Matrix | None]:
     """Weights [n, k] or [experts, n, k] in blocks of 128 x 128, and (with `transposed`) the same values transposed."""
     f = _format(fmt)
-    on_device("w", w, tuple(TYPES))
+    device = on_device("w", w, None, _ROW_TYPES)
     check(w.dim() in (2, 3) and min(w.shape) >= 1, f"w must be [n, k] or [experts, n, k], got {tuple(w.shape)}")
-    lead, n, k = w.shape[:-2], *w.shape[-2:]
+    lead, n, k = tuple(w.shape[:-2]), *w.shape[-2:]
     groups = lead[0] if lead else 1
     check(groups <= MAX_EXPERTS, f"at most {MAX_EXPERTS} experts")
     with on(stream, w):
@@ -143,8 +158,8 @@ def quantize_weight(w, fmt: str = "e4m3", transposed: bool = True, stream=None) 
         data_t, scales_t = _empty(lead, k, n, w.device) if transposed else (None, None)
         call("zc_fp8_quantize_weight", w.data_ptr(), TYPES[w.dtype], groups, n, k, f, data.data_ptr(),
              scales.data_ptr(), data_t.data_ptr() if transposed else None, scales_t.data_ptr() if transposed else None,
-             current())
-    return Matrix(data, scales, k, fmt), Matrix(data_t, scales_t, n, fmt) if transposed else None
+             current(device))
+    return _made(data, scales, k, fmt), _made(data_t, scales_t, n, fmt) if transposed else None
 
 
 def _out_type(dtype):
@@ -153,21 +168,31 @@ def _out_type(dtype):
     return TYPES[dtype]
 
 
+def _operand(name, m, device, dim=None):
+    if not isinstance(m, Matrix):
+        raise TypeError(f"{name} must be a Matrix")
+    return on_device(name, m.data, device, None, dim)
+
+
 def matmul(a: Matrix, b: Matrix, offsets=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """a [rows, k] times the transpose of its group's b [n, k]: [rows, n], zeros for rows behind the last group.
 
     b holds one matrix for each group (data [groups, n, pitch]), or a single one without offsets."""
     t = _out_type(out_dtype)
-    groups, at = _offsets(offsets)
-    on_device("a", a.data, None, 2)
-    on_device("b", b.data)
-    check(a.cols == b.cols and a.cols >= 1, f"a has rows of {a.cols} values, b of {b.cols}")
-    check((b.data.shape[0] if b.data.dim() == 3 else 1) == groups, f"b must hold {groups} matrices, got {tuple(b.data.shape)}")
-    rows, n = a.rows, b.rows
+    device = _operand("a", a, None, 2)
+    _operand("b", b, device)
+    groups, at = _offsets(offsets, device)
+    k = a.cols
+    if k != b.cols or k < 1:
+        raise ValueError(f"a has rows of {k} values, b of {b.cols}")
+    held = b.data.shape
+    if (held[0] if len(held) == 3 else 1) != groups:
+        raise ValueError(f"b must hold {groups} matrices, got {tuple(held)}")
+    rows, n = a.data.shape[0], held[-2]
     with on(stream, a.data, a.scales, b.data, b.scales, offsets):
         out = torch.empty((rows, n), dtype=out_dtype, device=a.data.device)
         call("zc_fp8_matmul", a.data.data_ptr(), a.scales.data_ptr(), FORMATS[a.fmt], rows, b.data.data_ptr(),
-             b.scales.data_ptr(), FORMATS[b.fmt], groups, n, a.cols, at, out.data_ptr(), n, t, current())
+             b.scales.data_ptr(), FORMATS[b.fmt], groups, n, k, at, out.data_ptr(), n, t, current(device))
     return out
 
 
@@ -175,14 +200,14 @@ def weight_grad(dy: Matrix, x: Matrix, out_dtype=torch.bfloat16, stream=None) ->
     """The gradient of matmul's weights, [groups, n, k], from quantize_columns of dy [rows, n] and x [rows, k]
     (with the same offsets); zeros for a group without rows."""
     t = _out_type(out_dtype)
+    device = _operand("dy", dy, None, 2)
+    _operand("x", x, device, 2)
     check(dy.offsets is not None and x.offsets is not None, "dy and x must come from quantize_columns")
-    on_device("dy", dy.data, None, 2)
-    on_device("x", x.data, None, 2)
-    check(dy.cols == x.cols and dy.offsets.numel() == x.offsets.numel(), "dy and x must have the same groups")
-    groups = x.offsets.numel() - 1
+    check(dy.cols == x.cols and dy.offsets.shape == x.offsets.shape, "dy and x must have the same groups")
+    groups, at = _offsets(x.offsets, device)
     with on(stream, dy.data, dy.scales, x.data, x.scales, x.offsets):
         out = torch.empty((groups, dy.rows, x.rows), dtype=out_dtype, device=x.data.device)
         call("zc_fp8_weight_grad", dy.data.data_ptr(), dy.scales.data_ptr(), FORMATS[dy.fmt], x.data.data_ptr(),
-             x.scales.data_ptr(), FORMATS[x.fmt], x.cols // BLOCK, groups, dy.rows, x.rows, x.offsets.data_ptr(),
-             out.data_ptr(), t, current())
+             x.scales.data_ptr(), FORMATS[x.fmt], x.cols // BLOCK, groups, dy.rows, x.rows, at, out.data_ptr(), t,
+             current(device))
     return out

@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._tensors import MAX_EXPERTS, MAX_K, TYPES, call, check, current, fn, on, on_device, rows_of
+from ._tensors import MAX_EXPERTS, MAX_K, TYPES, call, current, fn, on, on_device, rows_of
 
 
 class Plan(NamedTuple):
@@ -31,78 +31,95 @@ class Plan(NamedTuple):
         return self.offsets.numel() - 1
 
 
+_ID_TYPES = (torch.int32, torch.int64)
+_INT32 = (torch.int32,)
+_FLOAT32 = (torch.float32,)
+_ROW_TYPES = tuple(TYPES)
+
+
 def _ids(experts_of, num_experts):
-    on_device("experts_of", experts_of, (torch.int32, torch.int64), 2)
-    check(1 <= num_experts <= MAX_EXPERTS, f"num_experts must be 1 to {MAX_EXPERTS}, got {num_experts}")
-    check(1 <= experts_of.shape[1] <= MAX_K, f"experts_of must have 1 to {MAX_K} columns, got {experts_of.shape[1]}")
+    device = on_device("experts_of", experts_of, None, _ID_TYPES, 2)
+    if not 1 <= num_experts <= MAX_EXPERTS:
+        raise ValueError(f"num_experts must be 1 to {MAX_EXPERTS}, got {num_experts}")
+    if not 1 <= experts_of.shape[1] <= MAX_K:
+        raise ValueError(f"experts_of must have 1 to {MAX_K} columns, got {experts_of.shape[1]}")
+    return device
 
 
 def _new_plan(ids, num_experts):
-    slots, d = ids.numel(), ids.device
-    workspace = torch.empty(fn("zc_moe_sort_workspace")(slots, num_experts), dtype=torch.uint8, device=d)
-    return (Plan(torch.empty(ids.shape, dtype=torch.int32, device=d),
-                 torch.empty(num_experts + 1, dtype=torch.int32, device=d)), workspace)
+    need = fn("zc_moe_sort_workspace")(ids.numel(), num_experts)
+    workspace = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    position = torch.empty_like(ids, dtype=torch.int32)
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
+    return Plan(position, offsets), None if workspace is None else workspace.data_ptr(), workspace
 
 
 def _plan(plan):
-    on_device("plan.position", plan.position, (torch.int32,), 2)
-    on_device("plan.offsets", plan.offsets, (torch.int32,), 1)
-    check(plan.position.is_contiguous() and plan.offsets.is_contiguous(), "a plan's tensors must be contiguous")
-    check(2 <= plan.offsets.numel() <= MAX_EXPERTS + 1, f"a plan has 1 to {MAX_EXPERTS} experts")
-    check(1 <= plan.position.shape[1] <= MAX_K, f"a plan has 1 to {MAX_K} slots a token")
-    return plan.position.shape
+    position, offsets = plan
+    device = on_device("plan.position", position, None, _INT32, 2)
+    on_device("plan.offsets", offsets, device, _INT32, 1)
+    if not (position.is_contiguous() and offsets.is_contiguous()):
+        raise ValueError("a plan's tensors must be contiguous")
+    tokens, k = position.shape
+    experts = offsets.shape[0] - 1
+    if not (1 <= experts <= MAX_EXPERTS and 1 <= k <= MAX_K):
+        raise ValueError(f"a plan has 1 to {MAX_EXPERTS} experts and 1 to {MAX_K} slots a token, got {experts} and {k}")
+    return device, tokens, k, experts
 
 
-def _rows(name, t, rows, like=None):
-    on_device(name, t, tuple(TYPES) if like is None else (like.dtype,), 2)
-    check(t.shape[0] == rows, f"{name} must have {rows} rows, got {t.shape[0]}")
-    check(t.shape[1] >= 1 and (like is None or t.shape[1] == like.shape[1]), f"{name} has {t.shape[1]} columns")
+def _rows(name, t, device, rows, dtypes=_ROW_TYPES, hidden=None):
+    on_device(name, t, device, dtypes, 2)
+    if t.shape[0] != rows or t.shape[1] < 1 or (hidden is not None and t.shape[1] != hidden):
+        raise ValueError(f"{name} must be [{rows}, {'hidden' if hidden is None else hidden}], got {tuple(t.shape)}")
 
 
-def _weights(weights, plan):
-    on_device("weights", weights, (torch.float32,), 2)
-    check(weights.shape == plan.position.shape, f"weights must have the shape {tuple(plan.position.shape)}")
+def _weights(weights, device, plan):
+    on_device("weights", weights, device, _FLOAT32, 2)
+    if weights.shape != plan.position.shape:
+        raise ValueError(f"weights must have the shape {tuple(plan.position.shape)}, got {tuple(weights.shape)}")
 
 
 def sort(experts_of, num_experts: int, stream=None) -> Plan:
     """The plan of a routing: the place of each slot in the order by expert, ties in slot order."""
-    _ids(experts_of, num_experts)
+    device = _ids(experts_of, num_experts)
     with on(stream, experts_of):
         ids = experts_of.contiguous()
-        plan, workspace = _new_plan(ids, num_experts)
+        plan, scratch, _keep = _new_plan(ids, num_experts)
         call("zc_moe_sort", ids.data_ptr(), ids.element_size(), ids.shape[0], ids.shape[1], num_experts,
-             plan.position.data_ptr(), plan.offsets.data_ptr(), workspace.data_ptr(), current())
+             plan.position.data_ptr(), plan.offsets.data_ptr(), scratch, current(device))
     return plan
 
 
 def dispatch(x, experts_of, num_experts: int, stream=None) -> tuple[torch.Tensor, Plan]:
     """x [tokens, hidden] as rows [tokens * k, hidden] sorted by expert, and the plan."""
-    _ids(experts_of, num_experts)
+    device = _ids(experts_of, num_experts)
     tokens, k = experts_of.shape
-    _rows("x", x, tokens)
+    _rows("x", x, device, tokens)
     hidden = x.shape[1]
     with on(stream, experts_of, x):
         ids = experts_of.contiguous()
         x, pitch = rows_of(x)
-        plan, workspace = _new_plan(ids, num_experts)
-        rows = torch.empty((tokens * k, hidden), dtype=x.dtype, device=x.device)
+        plan, scratch, _keep = _new_plan(ids, num_experts)
+        rows = x.new_empty((tokens * k, hidden))
         call("zc_moe_dispatch", x.data_ptr(), pitch, TYPES[x.dtype], ids.data_ptr(), ids.element_size(), tokens, k,
              num_experts, hidden, rows.data_ptr(), hidden, plan.position.data_ptr(), plan.offsets.data_ptr(),
-             workspace.data_ptr(), current())
+             scratch, current(device))
     return rows, plan
 
 
 def _combine(rows, weights, plan, stream):
-    tokens, k = _plan(plan)
-    _rows("rows", rows, tokens * k)
+    device, tokens, k, experts = _plan(plan)
+    _rows("rows", rows, device, tokens * k)
+    if weights is not None:
+        _weights(weights, device, plan)
     hidden = rows.shape[1]
     with on(stream, rows, weights, *plan):
         rows, pitch = rows_of(rows)
         weights = None if weights is None else weights.contiguous()
-        out = torch.empty((tokens, hidden), dtype=rows.dtype, device=rows.device)
+        out = rows.new_empty((tokens, hidden))
         call("zc_moe_combine", rows.data_ptr(), pitch, TYPES[rows.dtype], None if weights is None else weights.data_ptr(),
-             plan.position.data_ptr(), plan.offsets.data_ptr(), tokens, k, plan.num_experts, hidden, out.data_ptr(),
-             hidden, current())
+             plan.position.data_ptr(), plan.offsets.data_ptr(), tokens, k, experts, hidden, out.data_ptr(), hidden,
+             current(device))
     return out
 
 
@@ -113,25 +130,25 @@ def dispatch_grad(d_rows, plan: Plan, stream=None) -> torch.Tensor:
 
 def combine(rows, weights, plan: Plan, stream=None) -> torch.Tensor:
     """Each token's rows [tokens * k, hidden] brought back and added with weights [tokens, k] (float32)."""
-    _plan(plan)
-    _weights(weights, plan)
+    if weights is None:
+        raise TypeError("weights must be a CUDA tensor")
     return _combine(rows, weights, plan, stream)
 
 
 def combine_grad(d_out, rows, weights, plan: Plan, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The gradients of combine with respect to rows and weights."""
-    tokens, k = _plan(plan)
-    _weights(weights, plan)
-    _rows("rows", rows, tokens * k)
-    _rows("d_out", d_out, tokens, rows)
+    device, tokens, k, experts = _plan(plan)
+    _weights(weights, device, plan)
+    _rows("rows", rows, device, tokens * k)
     hidden = rows.shape[1]
+    _rows("d_out", d_out, device, tokens, (rows.dtype,), hidden)
     with on(stream, rows, d_out, weights, *plan):
         rows, pitch = rows_of(rows)
         d_out, d_pitch = rows_of(d_out)
         weights = weights.contiguous()
-        d_rows = torch.empty((tokens * k, hidden), dtype=rows.dtype, device=rows.device)
-        d_weights = torch.empty((tokens, k), dtype=torch.float32, device=rows.device)
+        d_rows = rows.new_empty((tokens * k, hidden))
+        d_weights = torch.empty_like(weights)
         call("zc_moe_combine_grad", d_out.data_ptr(), d_pitch, rows.data_ptr(), pitch, TYPES[rows.dtype],
-             weights.data_ptr(), plan.position.data_ptr(), plan.offsets.data_ptr(), tokens, k, plan.num_experts,
-             hidden, d_rows.data_ptr(), hidden, d_weights.data_ptr(), current())
+             weights.data_ptr(), plan.position.data_ptr(), plan.offsets.data_ptr(), tokens, k, experts, hidden,
+             d_rows.data_ptr(), hidden, d_weights.data_ptr(), current(device))
     return d_rows, d_weights

@@ -47,7 +47,8 @@ def test_sizes():
     assert f("zc_fp8_column_blocks")(3, 10) == 3
     assert f("zc_fp8_column_blocks")(0, 10) == 0
     assert f("zc_fp8_column_blocks")(100, 0) == 0 == f("zc_fp8_column_blocks")(100, 1025)
-    assert f("zc_moe_sort_workspace")(100, 8) >= 16
+    assert f("zc_moe_sort_workspace")(100, 8) == 0  # small calls need none
+    assert f("zc_moe_sort_workspace")(100000, 8) >= 9 * 4
     assert f("zc_moe_sort_workspace")((1 << 30) + 1, 8) == 0 == f("zc_moe_sort_workspace")(10, 0)
 
 
@@ -65,11 +66,13 @@ INV, MIS = zc.ZC_ERR_INVALID_ARG, zc.ZC_ERR_MISALIGNED
 def test_sort_and_dispatch_refuse():
     refused("zc_moe_sort", [A, 4, 10, 2, 4, B, C, D, 0],
             [(0, 0, INV), (1, 2, INV), (3, 0, INV), (3, 65, INV), (4, 0, INV), (4, 1025, INV), (5, 0, INV), (6, 0, INV),
-             (7, 0, INV), (0, A + 2, MIS), (5, B + 2, MIS), (6, C + 1, MIS), (7, D + 8, MIS), (5, A + 4, INV),
+             (0, A + 2, MIS), (5, B + 2, MIS), (6, C + 1, MIS), (7, D + 8, MIS), (5, A + 4, INV),
              (6, B + 8, INV), (2, 1 << 30, INV)])
+    refused("zc_moe_sort", [A, 4, 10000, 2, 4, B, C, D, 0], [(7, 0, INV)])  # many slots: a workspace
+    refused("zc_moe_dispatch", [A, 64, 0, B, 4, 10000, 2, 4, 64, C, 64, D, E, F, 0], [(13, 0, INV)])
     refused("zc_moe_dispatch", [A, 64, 0, B, 4, 10, 2, 4, 64, C, 64, D, E, F, 0],
             [(0, 0, INV), (1, 63, INV), (2, 3, INV), (2, -1, INV), (3, 0, INV), (4, 3, INV), (6, 0, INV), (7, 0, INV),
-             (8, 0, INV), (9, 0, INV), (10, 63, INV), (11, 0, INV), (12, 0, INV), (13, 0, INV), (0, A + 1, MIS),
+             (8, 0, INV), (9, 0, INV), (10, 63, INV), (11, 0, INV), (12, 0, INV), (0, A + 1, MIS),
              (9, C + 1, MIS), (9, A + 128, INV), (9, B, INV), (9, D, INV)])
 
 
