@@ -34,6 +34,10 @@ constexpr int kMaxStages = 12;
 constexpr int kScaleSlots = 2;
 constexpr int kSlotBytes = 512 * 3;  // P's scales, and up to two chunks of 128 rows of Q
 constexpr int kColumns = 512;        // tensor memory: all of it (one CTA an SM)
+constexpr int kChunk = 32;           // accumulator columns a warp reads at once
+// Two accumulators of 256 columns and the scales do not fit in 512 columns: with tiles of 256 the
+// second accumulator starts at column 224, and the epilogue reads the 32 columns they share first.
+constexpr int kSecond = 224;
 
 struct TileParams {
   const uint32_t *p_scales, *q_scales;  // words
@@ -42,7 +46,7 @@ struct TileParams {
   int blocks;                 // by_blocks: the capacity; else the blocks of a row
   int words;                  // scale words of a row
   bool by_blocks;             // the groups are runs of blocks, and out has a matrix for each
-  int tile_q, stages, accumulators;
+  int tile_q, stages;
   const int* offsets;         // rows (or blocks) of each group; null: one group
   void* out;
   size_t out_pitch;
@@ -156,6 +160,78 @@ __device__ __forceinline__ uint4 scale_words(const uint32_t* words, int row0, in
   return v;
 }
 
+__device__ __forceinline__ void put(float* to, uint32_t v) { *to = __uint_as_float(v); }
+__device__ __forceinline__ void put(__nv_bfloat16* to, uint32_t v) { *to = __float2bfloat16_rn(__uint_as_float(v)); }
+
+// The epilogue: warps 4-7, each its 32 lanes (rows of P) of every finished tile.
+template <typename Out>
+__device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint32_t tmem, uint32_t accumulator) {
+  const int quarter = threadIdx.x / 32 % 4, lane = threadIdx.x % 32;
+  volatile unsigned* failed = &s.failed;
+  const bool shared_columns = p.tile_q > kSecond;
+  Walk walk(p, s);
+  Tile tile;
+  unsigned sums = 0;
+  while (walk.next(&tile)) {
+    const int pr = tile.p0 + 32 * quarter + lane, columns = tile.q1 - tile.q0;
+    const size_t base = (p.by_blocks ? static_cast<size_t>(tile.group) * p.q_rows : 0) + tile.q0;
+    Out* out = static_cast<Out*>(p.out) + base * p.out_pitch + pr;
+    const int chunks = (columns + kChunk - 1) / kChunk;
+    if (tile.b0 == tile.b1) {
+      if (pr < p.p_rows)
+        for (int c = 0; c < columns; ++c) put(out + c * p.out_pitch, 0u);
+      continue;
+    }
+    if (!__all_sync(~0u, wait_phase(&s.sum_full[sums % 2], sums / 2 % 2, failed))) break;
+    tcgen05_fence_after();
+    const uint32_t from = tmem + (static_cast<uint32_t>(quarter) << 21) + sums % 2 * accumulator;
+    // the first accumulator's shared columns are its last ones, the second's its first
+    const int all = p.tile_q / kChunk, turn = shared_columns && sums % 2 == 0 ? all - 1 : 0;
+    const auto chunk_at = [&](int i) { return i + turn < all ? i + turn : i + turn - all; };
+    const auto store = [&](const uint32_t(&v)[kChunk], int chunk) {
+      Out* to = out + static_cast<size_t>(chunk) * kChunk * p.out_pitch;
+      const int n = columns - chunk * kChunk;
+      if (pr >= p.p_rows) return;
+      if (n >= kChunk) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) put(to + i * p.out_pitch, v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          if (i < n) put(to + i * p.out_pitch, v[i]);
+      }
+    };
+    const auto release = [&] {
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.sum_empty[sums % 2]);
+    };
+    if (p.tile_q < kChunk) {  // 16 columns
+      uint32_t v[16];
+      tmem_load(from, v);
+      tmem_load_wait(v);
+      release();
+      if (pr < p.p_rows)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < columns) put(out + i * p.out_pitch, v[i]);
+    } else {
+      // one chunk is stored while the next one is read
+      uint32_t v[2][kChunk];
+      tmem_load(from + chunk_at(0) * kChunk, v[0]);
+#pragma unroll 2
+      for (int i = 0; i < all; ++i) {
+        tmem_load_wait(v[i % 2]);
+        if (i == (shared_columns ? 0 : all - 1)) release();
+        if (i + 1 < all) tmem_load(from + chunk_at(i + 1) * kChunk, v[(i + 1) % 2]);
+        if (chunk_at(i) < chunks) store(v[i % 2], chunk_at(i));
+        __syncwarp();
+      }
+    }
+    ++sums;
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ TileParams p,
                                                              const __grid_constant__ CUtensorMap p_map,
                                                              const __grid_constant__ CUtensorMap q_map) {
@@ -173,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         mbar_init(&s.empty[i], 1);
       }
       for (int i = 0; i < kScaleSlots; ++i) {
-        mbar_init(&s.scales_full[i], 1);
+        mbar_init(&s.scales_full[i], 2);
         mbar_init(&s.scales_empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -194,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   tcgen05_fence_after();
   const uint32_t tmem = s.tmem;
   const uint32_t scale_columns = tmem + kColumns - 16 * kScaleSlots;
+  const uint32_t accumulator = min(p.tile_q, kSecond);  // columns from one accumulator to the next
   volatile unsigned* failed = &s.failed;
 
   Walk walk(p, s);
@@ -225,14 +302,20 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t desc = product_desc(p.p_fmt, p.q_fmt, p.tile_q);
-      int stage = 0, slot = 0, acc = 0;
-      unsigned phase = 0, slot_phase = 0, acc_phase = 0;
+      int stage = 0, slot = 0;
+      unsigned phase = 0, slot_phase = 0, sums = 0;
+      // Tile j needs its accumulator read out: that of tile j - 2, and, where the accumulators
+      // share columns, those of tile j - 1 (the epilogue reads in order, so that implies the rest).
+      const unsigned lag = p.tile_q > kSecond ? 1 : 2;
       bool ok = true;
       while (ok && walk.next(&tile)) {
         if (tile.b0 == tile.b1) continue;
-        if (!(ok = wait_phase(&s.sum_empty[acc], acc_phase ^ 1, failed))) break;
-        tcgen05_fence_after();
-        const uint32_t d = tmem + acc * p.tile_q;
+        if (sums >= lag) {
+          const unsigned j = sums - lag;
+          if (!(ok = wait_phase(&s.sum_empty[j % 2], j / 2 % 2, failed))) break;
+          tcgen05_fence_after();
+        }
+        const uint32_t d = tmem + sums % 2 * accumulator;
         for (int b = tile.b0; b < tile.b1; ++b) {
           const uint32_t sp = scale_columns + slot * 16, sq = sp + 4;
           if (b == tile.b0 || b % 4 == 0) {
@@ -259,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           if (++stage == p.stages) stage = 0, phase ^= 1;
         }
         if (!ok) break;
-        commit_to(&s.sum_full[acc]);
-        if (++acc == p.accumulators) acc = 0, acc_phase ^= 1;
+        commit_to(&s.sum_full[sums % 2]);
+        ++sums;
       }
       if (!ok) {  // given up: the products in flight end before tensor memory is freed
         commit_to(&s.drained);
@@ -268,66 +351,51 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         while (!mbar_try_wait(&s.drained, 0) && now_ns() - start < kWaitLimitNs) {}
       }
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
+    // warp 2 brings P's scales, warp 3 Q's; each has its next words' loads in flight while it
+    // waits for a slot
+    const bool is_p = warp == 2;
+    const int chunks = is_p || p.tile_q <= 128 ? 1 : 2;
+    uint4 next[2];
+    int b = 0;
+    bool more = walk.next(&tile);
+    const auto fetch = [&] {  // the words of the blocks from b on
+      while (more && b >= tile.b1) {
+        more = walk.next(&tile);
+        b = tile.b0;
+      }
+      if (!more) return;
+      const size_t w = b / 4;
+      if (is_p) {
+        const uint32_t* at = p.p_scales + (p.by_blocks ? 0 : static_cast<size_t>(tile.group) * p.words * p.p_rows);
+        next[0] = scale_words(at + w * p.p_rows, tile.p0, p.p_rows);
+      } else {
+        const uint32_t* at = p.q_scales + w * p.q_rows;
+        next[0] = scale_words(at, tile.q0, tile.q1);
+        if (chunks > 1) next[1] = scale_words(at, tile.q0 + 128, tile.q1);
+      }
+      b = (b / 4 + 1) * 4;
+    };
+    b = more ? tile.b0 : 0;
+    fetch();
     int slot = 0;
     unsigned phase = 0;
-    bool ok = true;
-    while (ok && walk.next(&tile)) {
-      const uint32_t* pw = p.p_scales + (p.by_blocks ? 0 : static_cast<size_t>(tile.group) * p.words * p.p_rows);
-      for (int b = tile.b0; b < tile.b1; b = (b / 4 + 1) * 4) {
-        const size_t w = b / 4;
-        const uint4 vp = scale_words(pw + w * p.p_rows, tile.p0, p.p_rows);
-        const uint4 v0 = scale_words(p.q_scales + w * p.q_rows, tile.q0, tile.q1);
-        uint4 v1 = make_uint4(0, 0, 0, 0);
-        if (p.tile_q > 128) v1 = scale_words(p.q_scales + w * p.q_rows, tile.q0 + 128, tile.q1);
-        if (!(ok = __all_sync(~0u, wait_phase(&s.scales_empty[slot], phase ^ 1, failed)))) break;
-        uint4* to = reinterpret_cast<uint4*>(slots + slot * kSlotBytes) + lane;
-        to[0] = vp;
-        to[32] = v0;
-        if (p.tile_q > 128) to[64] = v1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.scales_full[slot]);
-        if (++slot == kScaleSlots) slot = 0, phase ^= 1;
-      }
+    for (bool one = more; one; ) {
+      const uint4 now[2] = {next[0], next[1]};
+      fetch();
+      one = more;
+      if (!__all_sync(~0u, wait_phase(&s.scales_empty[slot], phase ^ 1, failed))) break;
+      uint4* to = reinterpret_cast<uint4*>(slots + slot * kSlotBytes) + lane + (is_p ? 0 : 32);
+      to[0] = now[0];
+      if (chunks > 1) to[32] = now[1];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.scales_full[slot]);
+      if (++slot == kScaleSlots) slot = 0, phase ^= 1;
     }
-  } else if (warp >= 4) {
-    const uint32_t quarter = static_cast<uint32_t>(warp % 4) << 21;  // lane 32 (warp % 4)
-    int acc = 0;
-    unsigned acc_phase = 0;
-    while (walk.next(&tile)) {
-      const bool any = tile.b0 != tile.b1;
-      if (any) {
-        if (!__all_sync(~0u, wait_phase(&s.sum_full[acc], acc_phase, failed))) break;
-        tcgen05_fence_after();
-      }
-      const int pr = tile.p0 + 32 * (warp % 4) + lane;
-      const size_t base = p.by_blocks ? static_cast<size_t>(tile.group) * p.q_rows : 0;
-      const int columns = tile.q1 - tile.q0;
-      for (int c = 0; c < columns; c += 16) {
-        uint32_t v[16] = {};
-        if (any) {
-          tmem_load16(tmem + quarter + acc * p.tile_q + c, v);
-          tmem_load_wait();
-        }
-        if (pr < p.p_rows) {
-          const size_t at = (base + tile.q0 + c) * p.out_pitch + pr;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < columns) {
-              if (p.out_fp32) static_cast<uint32_t*>(p.out)[at + i * p.out_pitch] = v[i];
-              else static_cast<__nv_bfloat16*>(p.out)[at + i * p.out_pitch] = __float2bfloat16_rn(__uint_as_float(v[i]));
-            }
-        }
-        __syncwarp();
-      }
-      if (any) {
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.sum_empty[acc]);
-        if (++acc == p.accumulators) acc = 0, acc_phase ^= 1;
-      }
-    }
+  } else {
+    if (p.out_fp32) write_sums<float>(p, s, tmem, accumulator);
+    else write_sums<__nv_bfloat16>(p, s, tmem, accumulator);
   }
   tcgen05_fence_before();
   __syncthreads();
@@ -379,7 +447,6 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
                          size_t q_pitch, const DeviceInfo& dev, cudaStream_t stream) {
   t.stages = 2;
   while (t.stages < kMaxStages && smem_bytes(t.tile_q, t.stages + 1) <= kSmemLimit) ++t.stages;
-  t.accumulators = t.tile_q > 128 ? 1 : 2;
   t.status = dev.status;
   CUtensorMap p_map, q_map;
   cudaError_t err = tile_map(pv, p_pitch, t.p_rows, p_matrices, 3, kTileP, &p_map);
