@@ -21,7 +21,8 @@ SIGNATURES = {
     "zc_fp8_column_blocks": (_N, [_N, _I]),
     "zc_fp8_quantize_columns": (_I, [_P, _N, _I, _N, _N, _I, _P, _I, _P, _P, _P, _P]),
     "zc_fp8_quantize_weight": (_I, [_P, _I, _I, _N, _N, _I, _P, _P, _P, _P, _P]),
-    "zc_fp8_matmul": (_I, [_P, _P, _I, _N, _P, _P, _I, _I, _N, _N, _P, _P, _N, _I, _P]),
+    "zc_fp8_matmul_workspace": (_N, [_N, _I, _N, _N]),
+    "zc_fp8_matmul": (_I, [_P, _P, _I, _N, _P, _P, _I, _I, _N, _N, _P, _P, _N, _I, _P, _P]),
     "zc_fp8_weight_grad": (_I, [_P, _P, _I, _P, _P, _I, _N, _I, _N, _N, _P, _P, _I, _P]),
 }
 

@@ -220,19 +220,26 @@ int zc_fp8_quantize_weight(const void* w, int type, int groups, size_t rows, siz
                                            static_cast<uint8_t*>(scales_t), stream));
 }
 
+size_t zc_fp8_matmul_workspace(size_t rows, int groups, size_t n, size_t k) {
+  if (!groups_ok(groups) || !matrix_ok(rows, k) || rows == 0 || n < 1 || n > kMaxCols) return 0;
+  return ex::matmul_workspace(rows, groups, n, k);
+}
+
 int zc_fp8_matmul(const void* a, const void* a_scales, int a_fmt, size_t rows, const void* b, const void* b_scales,
                   int b_fmt, int groups, size_t n, size_t k, const int* offsets, void* out, size_t out_pitch,
-                  int out_type, cudaStream_t stream) {
+                  int out_type, void* workspace, cudaStream_t stream) {
   if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || !matrix_ok(rows, k) || n < 1 || n > kMaxCols ||
       out_pitch < n || (out_type != ZC_TYPE_BF16 && out_type != ZC_TYPE_FP32) || (!offsets && groups != 1))
     return ZC_ERR_INVALID_ARG;
   if (rows == 0) return ZC_OK;
-  if (!a || !a_scales || !b || !b_scales || !out) return ZC_ERR_INVALID_ARG;
+  const size_t scratch = ex::matmul_workspace(rows, groups, n, k);
+  if (!a || !a_scales || !b || !b_scales || !out || (scratch && !workspace)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16)) return ZC_ERR_MISALIGNED;
   if (!aligned(a, 128) || !aligned(b, 128) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
       !aligned(offsets, 4) || !aligned(out, ex::type_bytes(out_type)))
     return ZC_ERR_MISALIGNED;
   const size_t g = groups;
-  if (clash({{out, rows_bytes(rows, out_pitch, n, out_type)}},
+  if (clash({{out, rows_bytes(rows, out_pitch, n, out_type)}, {workspace, scratch}},
             {{a, values_bytes(rows, k)},
              {a_scales, scales_bytes(rows, k)},
              {b, g * values_bytes(n, k)},
@@ -243,7 +250,7 @@ int zc_fp8_matmul(const void* a, const void* a_scales, int a_fmt, size_t rows, c
   if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
   const ex::Product p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
                       static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
-                      a_fmt, b_fmt, groups, out_type, rows, n, k, out_pitch, offsets, out};
+                      a_fmt, b_fmt, groups, out_type, rows, n, k, out_pitch, offsets, out, workspace};
   return finish(ex::launch_matmul(p, dev, stream));
 }
 
@@ -269,7 +276,7 @@ int zc_fp8_weight_grad(const void* a, const void* a_scales, int a_fmt, const voi
   if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
   const ex::Product p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
                       static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
-                      a_fmt, b_fmt, groups, out_type, capacity, n, k, k, block_offsets, out};
+                      a_fmt, b_fmt, groups, out_type, capacity, n, k, k, block_offsets, out, nullptr};
   return finish(ex::launch_weight_grad(p, dev, stream));
 }
 

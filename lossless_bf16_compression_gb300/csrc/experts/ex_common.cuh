@@ -80,10 +80,10 @@ inline int vector_bytes(size_t element, size_t row_values, std::initializer_list
 
 inline size_t type_bytes(int type) { return type == ZC_TYPE_FP32 ? 4 : 2; }
 
-// A launch that may start while the kernel before it (of the same call) still runs; it waits
-// for that kernel's writes with griddepcontrol.wait.
+// A launch; early: it may start while the kernel before it in the stream still runs (whoever
+// launched that one), so the kernel calls wait_for_previous before it touches memory.
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool after_own,
+cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool early,
                    A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -94,7 +94,7 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cud
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = after_own ? 1 : 0;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
@@ -139,9 +139,10 @@ struct Product {
   int a_fmt, b_fmt, groups, out_type;
   size_t rows, n, k, out_pitch;
   const int* offsets;
-  void* out;
+  void *out, *workspace;
 };
 // rows: the capacity in blocks for weight_grad.
+size_t matmul_workspace(size_t rows, int groups, size_t n, size_t k);
 cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_weight_grad(const Product& p, const DeviceInfo& dev, cudaStream_t stream);
 

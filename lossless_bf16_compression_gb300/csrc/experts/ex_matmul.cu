@@ -13,13 +13,15 @@
 // consecutive outputs: the epilogue stores whole 64-byte (bf16) or 128-byte (fp32) segments
 // straight from registers, with no transposition, and a ragged group's last tile only skips
 // columns.  Tiles of 256 rows of Q are shared by a pair of CTAs, 256 rows of P by 256 of Q with
-// each CTA loading half of both, which takes a third off what the SMs read from the L2.  Roles: warp 0 issues the TMA loads (128 columns a stage), warp 1 the products,
-// warps 2, 3, 8 and 9 bring the scales, warps 4-7 write the results while the next tile's products
-// run.
+// each CTA loading half of both, which takes a third off what the SMs read from the L2
+// and off the shared-memory traffic that a CTA alone is bound by (8192^3: 304 us against 347).
+// Roles: warp 0 issues the TMA loads (128 columns a stage), warp 1 the products, warps 2, 3, 8 and 9
+// bring the scales, warps 4-7 write the results while the next tile's products run.
 //
 // Scales are kept four blocks to a word, [word][row].  A product's scales lie in tensor memory, row
 // r at lane r % 32 (in each quarter of the lanes) and column r / 32, so a warp reads 32 rows' words
 // as one coalesced load and stores them as one column; byte b % 4 is picked by the instruction.
+#include <cmath>
 #include <mutex>
 
 #include "ex_fp8.cuh"
@@ -32,7 +34,6 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kBand = 2048;  // rows of P: 152 SMs hold 16 x 9.5 tiles of 128 x 256
 constexpr int kTileP = 128;
-constexpr int kMaxTileQ = 256;
 constexpr int kMaxStages = 12;
 constexpr int kMaxTurns = 4;   // words of scales in tensor memory; two where accumulators leave no more room
 constexpr int kWordsAhead = 4;
@@ -51,7 +52,14 @@ struct TileParams {
   int words;                  // scale words of a row
   bool by_blocks;             // the groups are runs of blocks, and out has a matrix for each
   int tile_q, stages;
+  bool out_words;             // rows of out may be stored two 16-bit values at a time
   const int* offsets;         // rows (or blocks) of each group; null: one group
+  // Where tiles are few or uneven: the blocks of all tiles are shared out evenly, so that a CTA
+  // begins and ends inside tiles.  Its sums of a part of a tile go to `parts` (two a CTA, [column][128
+  // rows]), and whichever warp comes last to a tile's quarter of rows, by `arrivals` (four a
+  // tile, zero at the start), adds the parts in their order.  Null: whole tiles.
+  float* parts;
+  unsigned* arrivals;
   void* out;
   size_t out_pitch;
   int* status;
@@ -70,6 +78,7 @@ struct Shared {
 struct Tile {
   int group, p0, q0, q1;  // rows p0 .. of P, rows q0 .. q1 - 1 of Q
   int b0, b1;             // blocks
+  long long index;        // tiles before it
 };
 
 // Walks the tiles of this CTA (or pair); every role walks them alike.
@@ -79,22 +88,67 @@ struct Walk {
   const Shared& s;
   long long t;
   int g = 0;
-  __device__ Walk(const TileParams& p_, const Shared& s_) : p(p_), s(s_), t(blockIdx.x / G) {}
+  long long end = 0;              // of this CTA's blocks
+  long long whole = 0, all = 0;   // tiles that have blocks, and their blocks
+  long long ctas = 1;             // that share them: each gets a word of scales, four blocks, at least
+  __device__ Walk(const TileParams& p_, const Shared& s_) : p(p_), s(s_), t(blockIdx.x / G) {
+    if (p.parts) {
+      whole = s.tiles[p.groups];
+      all = whole * p.blocks;
+      ctas = min(static_cast<long long>(gridDim.x), max(all / 4, 1ll));
+      t = begin_of(blockIdx.x);
+      end = begin_of(blockIdx.x + 1);
+    }
+  }
+  // The first block of a CTA, all tiles' blocks in a row, and the CTA that has a block.
+  __device__ long long begin_of(long long cta) const { return min(cta, ctas) * all / ctas; }
+  __device__ long long cta_of(long long block) const { return ((block + 1) * ctas - 1) / all; }
+
   __device__ bool next(Tile* out) {
     const int last = p.by_blocks ? p.groups : p.groups + 1;
+    if (p.parts) {
+      if (t >= end) {  // then the tiles without blocks, one after the other
+        const long long zero = whole + blockIdx.x + (t - end) * gridDim.x;
+        if (zero >= s.tiles[last]) return false;
+        ++t;
+        locate(zero, out);
+        return true;
+      }
+      const long long tile = t / p.blocks;
+      locate(tile, out);
+      out->b0 = static_cast<int>(t - tile * p.blocks);
+      out->b1 = static_cast<int>(min(static_cast<long long>(p.blocks), out->b0 + (end - t)));
+      t += out->b1 - out->b0;
+      return true;
+    }
     if (t >= s.tiles[last]) return false;
-    while (s.tiles[g + 1] <= t) ++g;
+    locate(t, out);
+    t += gridDim.x / G;
+    return true;
+  }
+
+  __device__ void locate(long long tile, Tile* out) {
+    while (s.tiles[g + 1] <= tile) ++g;
     const int p_tiles = (p.p_rows + kTileP * G - 1) / (kTileP * G);
+    const long long local = tile - s.tiles[g], q_tiles = (s.tiles[g + 1] - s.tiles[g]) / p_tiles;
     // Within a group: bands of kBand rows of P, and in a band all of P's tiles for each of Q's, so
-    // that the tiles in flight at a time cover about as many rows of P as of Q.
-    const long long local = t - s.tiles[g], q_tiles = (s.tiles[g + 1] - s.tiles[g]) / p_tiles;
-    constexpr int width = kBand / (kTileP * G);
-    const int band = static_cast<int>(local / (width * q_tiles));
-    const int inside = static_cast<int>(local - band * width * q_tiles);
-    const int here = min(width, p_tiles - band * width);
-    const int q = inside / here;
+    // that the tiles in flight at a time cover about as many rows of P as of Q.  Shared-out tiles
+    // follow one another in a CTA: there Q's tiles for each of P's, whose rows are then in the L2.
+    int q, pt;
+    if (p.parts) {
+      q = static_cast<int>(local % q_tiles);
+      pt = static_cast<int>(local / q_tiles);
+    } else {
+      constexpr int width = kBand / (kTileP * G);
+      const int band = static_cast<int>(local / (width * q_tiles));
+      const int inside = static_cast<int>(local - band * width * q_tiles);
+      const int here = min(width, p_tiles - band * width);
+      q = inside / here;
+      pt = band * width + inside % here;
+    }
+    out->index = tile;
     out->group = g;
-    out->p0 = (band * width + inside % here) * kTileP * G;
+    out->p0 = pt * kTileP * G;
     if (p.by_blocks) {
       out->q0 = q * p.tile_q;
       out->q1 = min(p.q_rows, out->q0 + p.tile_q);
@@ -106,8 +160,6 @@ struct Walk {
       out->b0 = 0;
       out->b1 = g == p.groups ? 0 : p.blocks;  // rows without a group: zeros
     }
-    t += gridDim.x / G;
-    return true;
   }
 };
 
@@ -169,7 +221,73 @@ __device__ __forceinline__ uint4 scale_words(const uint32_t* words, int row0, in
 __device__ __forceinline__ void put(float* to, uint32_t v) { *to = __uint_as_float(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* to, uint32_t v) { *to = __float2bfloat16_rn(__uint_as_float(v)); }
 
+// Columns c and c + 1 of 32 neighbouring outputs each, as 16 words of column c from the even lanes
+// and 16 of column c + 1 from the odd ones: a lane gives its neighbour the value that belongs to
+// its word.
+__device__ __forceinline__ uint32_t pair_up(uint32_t v0, uint32_t v1) {
+  uint32_t own, r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(own) : "f"(__uint_as_float(v1)), "f"(__uint_as_float(v0)));
+  const uint32_t other = __shfl_xor_sync(~0u, own, 1);
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(own), "r"(other), "r"(threadIdx.x % 2 ? 0x3276u : 0x5410u));
+  return r;
+}
+
 // The epilogue: warps 4-7, each its 32 lanes (rows of P) of every finished tile.
+// A warp's quarter of a part of a tile: to its place among the parts, and the whole if it is the last.
+template <typename Out>
+__device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const Walk<1>& walk, const Tile& tile,
+                                           uint32_t from, unsigned acc, int quarter) {
+  const int lane = threadIdx.x % 32, row = 32 * quarter + lane;
+  const long long tile_begin = tile.index * p.blocks;
+  const size_t part = static_cast<size_t>(kTileP) * p.tile_q;
+  // a CTA's first place is for the tile that it begins inside, its second for one that it begins
+  const auto place = [&](long long cta) {
+    return p.parts + (2 * cta + (walk.begin_of(cta) > tile_begin ? 0 : 1)) * part + row;
+  };
+  float* mine = place(blockIdx.x);
+  for (int c = 0; c < p.tile_q; c += 16) {
+    uint32_t v[16];
+    tmem_load(from + c, v);
+    tmem_load_wait(v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kTileP, __uint_as_float(v[i]));
+  }
+  tcgen05_fence_before();
+  __threadfence();
+  __syncwarp();
+  unsigned before = 0;
+  if (lane == 0) {
+    mbar_arrive(&s.sum_empty[acc]);
+    before = atomicAdd(&p.arrivals[tile.index * 4 + quarter], 1u);
+  }
+  before = __shfl_sync(~0u, before, 0);
+  const long long first = walk.cta_of(tile_begin), last = walk.cta_of(tile_begin + p.blocks - 1);
+  if (before != last - first) return;
+  __threadfence();
+  const int pr = tile.p0 + row;
+  Out* out = static_cast<Out*>(p.out) + static_cast<size_t>(tile.q0) * p.out_pitch + pr;
+  for (int c = 0; c < tile.q1 - tile.q0; c += 16) {
+    float sum[16] = {};
+    for (long long cta = first; cta <= last; cta += 4) {  // four parts' loads in flight
+      float v[4][16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float* from_part = place(min(cta + k, last)) + c * kTileP;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[k][i] = __ldcg(from_part + i * kTileP);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] += cta + k <= last ? v[k][i] : 0.f;
+    }
+    if (pr < p.p_rows)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < tile.q1 - tile.q0) put(out + (c + i) * p.out_pitch, __float_as_uint(sum[i]));
+  }
+}
+
 template <int G, typename Out>
 __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint32_t tmem, uint32_t accumulator,
                                            int first_row) {
@@ -192,12 +310,32 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
     if (!__all_sync(~0u, wait_phase(&s.sum_full[sums % 2], sums / 2 % 2, failed))) break;
     tcgen05_fence_after();
     const uint32_t from = tmem + (static_cast<uint32_t>(quarter) << 21) + sums % 2 * accumulator;
+    if constexpr (G == 1) {
+      if (p.parts && tile.b1 - tile.b0 != p.blocks) {
+        write_part<Out>(p, s, walk, tile, from, sums % 2, quarter);
+        ++sums;
+        continue;
+      }
+    }
     // the first accumulator's shared columns are its last ones, the second's its first
     const int all = p.tile_q / kChunk, turn = shared_columns && sums % 2 == 0 ? all - 1 : 0;
     const auto chunk_at = [&](int i) { return i + turn < all ? i + turn : i + turn - all; };
     const auto store = [&](const uint32_t(&v)[kChunk], int chunk) {
       Out* to = out + static_cast<size_t>(chunk) * kChunk * p.out_pitch;
       const int n = columns - chunk * kChunk;
+      if (sizeof(Out) == 2 && p.out_words && n >= kChunk) {
+        // two columns a store, half as many stores (weights' gradient of 16384 x 7168 x 2048, whose
+        // tiles sum only 8 blocks: 232 -> 218 us; whole rows by way of shared memory: 317 us, the
+        // operands' traffic leaves it no bandwidth)
+        uint32_t w[kChunk / 2];
+#pragma unroll
+        for (int i = 0; i < kChunk / 2; ++i) w[i] = pair_up(v[2 * i], v[2 * i + 1]);
+        if (pr >= p.p_rows) return;
+        to += lane % 2 ? static_cast<ptrdiff_t>(p.out_pitch) - 1 : 0;
+#pragma unroll
+        for (int i = 0; i < kChunk / 2; ++i) *reinterpret_cast<uint32_t*>(to + 2 * i * p.out_pitch) = w[i];
+        return;
+      }
       if (pr >= p.p_rows) return;
       if (n >= kChunk) {
 #pragma unroll
@@ -249,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   const uint32_t stage_bytes = (kTileP + load_q) * kBlock;
   Shared& s = *reinterpret_cast<Shared*>(tiles + p.stages * stage_bytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  let_next_start();
   const int rank = G == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int first_row = rank * kTileP;  // of a tile's rows of P
 
@@ -269,12 +408,18 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       mbar_init(&s.drained, 1);
       s.failed = 0;
       fence_mbar_init();
+      prefetch_map(&p_map);
+      prefetch_map(&q_map);
     }
   } else if (warp == 1) {
     tmem_alloc<G>(&s.tmem, kColumns);
   } else if (warp == 2) {
+    wait_for_previous();
     plan_tiles<G>(p, s);
   }
+  // Everything above this line touches only this CTA, so it may run while the kernel before it
+  // in the stream ends.
+  wait_for_previous();
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
@@ -424,6 +569,8 @@ size_t smem_bytes(int load_q, int stages) {
   return 1024 + static_cast<size_t>(stages) * (kTileP + load_q) * kBlock + sizeof(Shared);
 }
 constexpr size_t kSmemLimit = 227 * 1024;
+constexpr size_t kMaxCtas = 160;  // CTAs of a launch, for the size of a workspace
+size_t sm_count(const DeviceInfo& dev) { return dev.sm_count < static_cast<int>(kMaxCtas) ? dev.sm_count : kMaxCtas; }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
@@ -463,6 +610,7 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
   t.stages = 2;
   while (t.stages < kMaxStages && smem_bytes(load_q, t.stages + 1) <= kSmemLimit) ++t.stages;
   t.status = dev.status;
+  t.out_words = reinterpret_cast<uintptr_t>(t.out) % 4 == 0 && t.out_pitch % 2 == 0 && t.p_rows % 2 == 0;
   CUtensorMap p_map, q_map;
   cudaError_t err = tile_map(pv, p_pitch, t.p_rows, p_matrices, 3, kTileP, &p_map);
   if (err == cudaSuccess) err = tile_map(qv, q_pitch, t.q_rows, 1, 2, load_q, &q_map);
@@ -472,40 +620,89 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
   if (err != cudaSuccess) return err;
   const size_t most = ceil_div(t.p_rows, kTileP * G) *
                       (t.by_blocks ? ceil_div(t.q_rows, t.tile_q) * t.groups : t.q_rows / t.tile_q + t.groups + 1);
-  const size_t room = dev.sm_count / G;
+  const size_t room = sm_count(dev) / G;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(G * (most < room ? most : room)));
+  cfg.gridDim = dim3(static_cast<unsigned>(t.parts ? room : G * (most < room ? most : room)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes(load_q, t.stages);
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = G;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = G;
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, matmul_kernel<G>, t, p_map, q_map);
 }
 
-cudaError_t launch_any(TileParams& t, const uint8_t* pv, size_t p_pitch, size_t p_matrices, const uint8_t* qv,
-                       size_t q_pitch, const DeviceInfo& dev, cudaStream_t stream) {
-  return t.tile_q == kMaxTileQ && t.p_rows > kTileP
-             ? launch_tiles<2>(t, pv, p_pitch, p_matrices, qv, q_pitch, dev, stream)
-             : launch_tiles<1>(t, pv, p_pitch, p_matrices, qv, q_pitch, dev, stream);
+__global__ void __launch_bounds__(256) clear_kernel(uint4* to, size_t n) {
+  let_next_start();
+  wait_for_previous();
+  for (size_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) to[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Rows of Q a tile takes: the smallest that holds an average group.
-int tile_rows(size_t average) {
-  int t = 16;
-  while (t < kMaxTileQ && static_cast<size_t>(t) < average) t *= 2;
-  return t;
+// How a product is cut, from sizes alone (the groups' own sizes are on the device).
+struct Shape {
+  int tile_q;
+  bool pair, share;  // share: the blocks of all tiles shared out evenly
+};
+
+// Groups of up to 64 rows on average are bound by the weights' bytes: one tile for all of a group's
+// rows where it is no more than half again the average, and the blocks shared out, so that every
+// SM streams the same amount (8 rows x 7168 x 4096: 24.6 us by whole tiles, %SHARE8% shared out; 32
+// rows over 16 such experts: 86 and %SHARE32%).  Larger groups are bound by the products: the
+// cut with the least time by the measured cycles of a block, given its waves.
+Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool by_blocks) {
+  const size_t active = by_blocks ? groups : q_rows < groups ? q_rows : groups;
+  const size_t average = by_blocks ? q_rows : ceil_div(q_rows, active);
+  if (!by_blocks && average <= 64) {
+    int t = 16;
+    while (2 * static_cast<size_t>(t) < 3 * average) t *= 2;
+    return {t, false, true};
+  }
+  struct {
+    Shape shape;
+    double cycles;  // of a block of a tile
+  } const cuts[] = {{{256, true, false}, 545}, {{256, false, false}, 722}, {{128, false, false}, 563}};
+  const Shape* best = nullptr;
+  double least = 0;
+  for (const auto& c : cuts) {
+    const size_t g = c.shape.pair ? 2 : 1;
+    const double tiles = static_cast<double>(active) * ceil_div(average, c.shape.tile_q) * ceil_div(p_rows, kTileP * g);
+    const double waves = std::ceil(tiles / (152 / g));
+    const double time = waves * c.cycles;
+    if (best == nullptr || time < least) best = &c.shape, least = time;
+  }
+  return *best;
+}
+
+size_t parts_bytes(const Shape& shape, size_t tiles) {
+  return shape.share ? 2 * kMaxCtas * kTileP * shape.tile_q * sizeof(float) + 4 * tiles * sizeof(unsigned) : 0;
+}
+// Tiles of a row-grouped product, at most.
+size_t most_tiles(const Shape& shape, size_t q_rows, size_t groups, size_t p_rows) {
+  return ceil_div(p_rows, kTileP) * (q_rows / shape.tile_q + groups + 1);
+}
+
+cudaError_t launch_any(TileParams& t, const Shape& shape, const uint8_t* pv, size_t p_pitch, size_t p_matrices,
+                       const uint8_t* qv, size_t q_pitch, const DeviceInfo& dev, cudaStream_t stream) {
+  t.tile_q = shape.tile_q;
+  return shape.pair ? launch_tiles<2>(t, pv, p_pitch, p_matrices, qv, q_pitch, dev, stream)
+                    : launch_tiles<1>(t, pv, p_pitch, p_matrices, qv, q_pitch, dev, stream);
 }
 
 }  // namespace
 
+size_t matmul_workspace(size_t rows, int groups, size_t n, size_t k) {
+  const Shape shape = shape_of(rows, groups, n, ceil_div(k, kBlock), false);
+  return parts_bytes(shape, most_tiles(shape, rows, groups, n));
+}
+
 cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
-  const size_t blocks = ceil_div(p.k, kBlock), active = p.rows < static_cast<size_t>(p.groups) ? p.rows : p.groups;
+  const size_t blocks = ceil_div(p.k, kBlock);
   TileParams t{};
   t.p_scales = reinterpret_cast<const uint32_t*>(p.b_scales);
   t.q_scales = reinterpret_cast<const uint32_t*>(p.a_scales);
@@ -518,11 +715,19 @@ cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t 
   t.blocks = static_cast<int>(blocks);
   t.words = static_cast<int>(ceil_div(blocks, 4));
   t.by_blocks = false;
-  t.tile_q = tile_rows(ceil_div(p.rows, active));
   t.offsets = p.offsets;
   t.out = p.out;
   t.out_pitch = p.out_pitch;
-  return launch_any(t, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, dev, stream);
+  const Shape shape = shape_of(p.rows, p.groups, p.n, blocks, false);
+  if (shape.share) {
+    const size_t tiles = most_tiles(shape, p.rows, p.groups, p.n);
+    t.arrivals = static_cast<unsigned*>(p.workspace);
+    t.parts = reinterpret_cast<float*>(t.arrivals + 4 * tiles);
+    const cudaError_t err = launch(clear_kernel, static_cast<unsigned>(tiles < 8192 ? ceil_div(tiles, 256) : 32), 256,
+                                   0, stream, true, static_cast<uint4*>(p.workspace), tiles);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_any(t, shape, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, dev, stream);
 }
 
 cudaError_t launch_weight_grad(const Product& p, const DeviceInfo& dev, cudaStream_t stream) {
@@ -541,11 +746,11 @@ cudaError_t launch_weight_grad(const Product& p, const DeviceInfo& dev, cudaStre
   t.blocks = static_cast<int>(capacity);
   t.words = static_cast<int>(ceil_div(capacity, 4));
   t.by_blocks = true;
-  t.tile_q = tile_rows(p.n);
   t.offsets = p.offsets;
   t.out = p.out;
   t.out_pitch = p.k;
-  return launch_any(t, p.b, capacity * kBlock, 1, p.a, capacity * kBlock, dev, stream);
+  const Shape shape = shape_of(p.n, p.groups, p.k, capacity, true);
+  return launch_any(t, shape, p.b, capacity * kBlock, 1, p.a, capacity * kBlock, dev, stream);
 }
 
 }  // namespace ex

@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
                                                                   int cols, unsigned words,
                                                                   uint8_t* __restrict__ values,
                                                                   uint32_t* __restrict__ scales) {
+  let_next_start();
+  wait_for_previous();
   const int lane = threadIdx.x % 32;
   const unsigned word = blockIdx.x % words;
   const size_t r0 = (static_cast<size_t>(blockIdx.x / words) * kRowWarps + threadIdx.x / 32) * R;
@@ -132,6 +134,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
 __global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restrict__ offsets, int rows, int groups,
                                                              int* __restrict__ block_offsets, int* status) {
   __shared__ int sums[32];
+  let_next_start();
+  wait_for_previous();
   const int g = threadIdx.x, lane = g % 32, warp = g / 32;
   int n = 0;
   if (g < groups) {
@@ -150,7 +154,6 @@ __global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restri
   for (int w = 0; w < warp; ++w) before += sums[w];
   if (g < groups) block_offsets[g] = before;
   if (g == groups - 1) block_offsets[groups] = before + n;
-  let_next_start();
 }
 
 // ------------------------------------------------------------------ 128 x 128 tiles
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const T* __restri
   const int b = blockIdx.x, tid = threadIdx.x, cg = tid % 16, rg = tid / 16;
   const int c = blockIdx.y * kBlock + cg * 8;
   if (tid == 0) first = last = 0;
+  let_next_start();
   wait_for_previous();
   __syncthreads();
   for (int g = tid; g < groups; g += 256) {
@@ -258,6 +262,8 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restric
                                                               uint8_t* __restrict__ values_t,
                                                               uint8_t* __restrict__ scales_t) {
   __shared__ TileShared s;
+  let_next_start();
+  wait_for_previous();
   const int rb = (rows + kBlock - 1) / kBlock, cb = (cols + kBlock - 1) / kBlock;
   const int bc = blockIdx.x, br = blockIdx.y, tid = threadIdx.x, cg = tid % 16, rg = tid / 16;
   const size_t g = blockIdx.z;
@@ -353,7 +359,7 @@ cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, 
     const auto go = [&](auto per_warp) {
       constexpr int R = per_warp();
       return launch(quantize_kernel<T, vec(), f(), R>, static_cast<unsigned>(ceil_div(rows, kRowWarps * R) * words),
-                    32 * kRowWarps, 0, stream, false, static_cast<const T*>(x), pitch, rows, static_cast<int>(cols),
+                    32 * kRowWarps, 0, stream, true, static_cast<const T*>(x), pitch, rows, static_cast<int>(cols),
                     static_cast<unsigned>(words), values, reinterpret_cast<uint32_t*>(scales));
     };
     // four rows a warp once that still gives every SM a few CTAs; one row a warp below
@@ -366,7 +372,7 @@ cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_
                                     const int* offsets, int fmt, uint8_t* values, uint8_t* scales, int* block_offsets,
                                     int* status, cudaStream_t stream) {
   const size_t capacity = column_blocks(rows, groups);
-  const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, false, offsets, static_cast<int>(rows),
+  const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, true, offsets, static_cast<int>(rows),
                                  groups, block_offsets, status);
   if (err != cudaSuccess || capacity == 0) return err;
   const dim3 grid(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, kBlock)));
@@ -385,7 +391,7 @@ cudaError_t launch_quantize_weight(const void* w, int type, int groups, size_t r
                   static_cast<unsigned>(groups));
   return variant(type, vector_rows(w, cols, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(quantize_weight_kernel<T, vec(), f()>, grid, 256, 0, stream, false, static_cast<const T*>(w),
+    return launch(quantize_weight_kernel<T, vec(), f()>, grid, 256, 0, stream, true, static_cast<const T*>(w),
                   static_cast<int>(rows), static_cast<int>(cols), values, scales, values_t, scales_t);
   });
 }

@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __
                                                                const int* __restrict__ position,
                                                                const int* __restrict__ total, int* status) {
   using V = typename Bytes<B>::type;
+  let_next_start();
   const size_t t = blockIdx.x / parts;
   const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
   V v{};
@@ -73,6 +74,8 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   __shared__ int place[ZC_MOE_MAX_K];
   __shared__ int bins[ZC_MOE_MAX_EXPERTS + 1];
   __shared__ int kept;
+  let_next_start();
+  wait_for_previous();
   const int t = static_cast<int>(blockIdx.x / parts), part = static_cast<int>(blockIdx.x % parts);
   const int c = part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x), lane = threadIdx.x % 32;
   V v{};
@@ -136,6 +139,8 @@ __global__ void __launch_bounds__(kMaxThreads) combine_kernel(const uint8_t* __r
                                                               const int* __restrict__ position,
                                                               const int* __restrict__ total, int* status) {
   constexpr int N = B / sizeof(T);
+  let_next_start();
+  wait_for_previous();
   const size_t t = blockIdx.x / parts;
   const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
   if (c >= vecs) return;
@@ -179,6 +184,8 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
   constexpr int N = B / sizeof(T);
   using V = typename Bytes<B>::type;
   __shared__ float sums[kBatch][kMaxThreads / 32];
+  let_next_start();
+  wait_for_previous();
   const size_t t = blockIdx.x;
   const int kept = *total, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int j0 = 0; j0 < k; j0 += kBatch) {
@@ -275,7 +282,7 @@ cudaError_t launch_small_dispatch(const RowShape& s, const void* ids, int id_byt
     const auto go = [&](auto* p) {
       using Id = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
       return launch(small_dispatch_kernel<Id, bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, threads, 0,
-                    stream, false, p, static_cast<int>(s.tokens * s.k), s.experts, static_cast<const uint8_t*>(x),
+                    stream, true, p, static_cast<int>(s.tokens * s.k), s.experts, static_cast<const uint8_t*>(x),
                     x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(vecs), cut.parts, s.k,
                     position, offsets);
     };
@@ -292,7 +299,7 @@ cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitc
   const Cut cut = cut_row(vecs, kMaxThreads);
   return by_type(s.type, v, [&](auto type, auto bytes) {
     return launch(combine_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, cut.threads, 0,
-                  stream, false, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
+                  stream, true, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
                   static_cast<uint8_t*>(out), out_pitch * b, static_cast<int>(vecs), cut.parts, s.k, s.tokens * s.k,
                   position, offsets + s.experts, status);
   });
@@ -307,7 +314,7 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
   const size_t vecs = s.hidden * b / v;
   return by_type(s.type, v, [&](auto type, auto bytes) {
     return launch(combine_grad_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens),
-                  cut_row(vecs, kMaxThreads).threads, 0, stream, false, static_cast<const uint8_t*>(d_out),
+                  cut_row(vecs, kMaxThreads).threads, 0, stream, true, static_cast<const uint8_t*>(d_out),
                   d_out_pitch * b, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
                   static_cast<uint8_t*>(d_rows), d_rows_pitch * b, d_weights, static_cast<int>(vecs), s.k,
                   s.tokens * s.k, position, offsets + s.experts, status);

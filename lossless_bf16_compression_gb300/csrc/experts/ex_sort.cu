@@ -33,6 +33,8 @@ template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const Id* __restrict__ ids, int slots, int run,
                                                              int experts, int* __restrict__ counts) {
   extern __shared__ int bins[];
+  wait_for_previous();
+  let_next_start();
   const int keys = experts + 1;
   const int begin = min(slots, static_cast<int>(blockIdx.x) * run), end = min(slots, begin + run);
   for (int i = threadIdx.x; i < keys; i += kSortThreads) bins[i] = 0;
@@ -40,7 +42,6 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const Id* __restric
   for (int s = begin + threadIdx.x; s < end; s += kSortThreads) atomicAdd(&bins[key_of(ids, s, experts)], 1);
   __syncthreads();
   for (int i = threadIdx.x; i < keys; i += kSortThreads) counts[static_cast<size_t>(blockIdx.x) * keys + i] = bins[i];
-  let_next_start();
 }
 
 // counts: [runs][experts + 1] from count_kernel; not read when there is one run.
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Id* __restric
   extern __shared__ int bins[];  // [kSortWarps][experts + 1]
   __shared__ int warp_sums[kSortWarps];
   __shared__ int carry;
+  if (runs == 1) wait_for_previous();  // else the ids are there: count_kernel started after them
   const int keys = experts + 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int first = min(slots, static_cast<int>(blockIdx.x) * run), last = min(slots, first + run);
   const int part = (last - first + kSortWarps - 1) / kSortWarps;
@@ -61,6 +63,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Id* __restric
   __syncthreads();
   for (int s = begin + lane; s < end; s += 32) atomicAdd(&mine[key_of(ids, s, experts)], 1);
   if (runs > 1) wait_for_previous();
+  let_next_start();  // not before the wait: what starts after this kernel reads x without one
   __syncthreads();
   for (int base = 0; base < keys; base += kSortThreads) {
     const int e = base + threadIdx.x;
@@ -113,7 +116,6 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Id* __restric
     }
     __syncwarp();
   }
-  let_next_start();
 }
 
 }  // namespace
@@ -136,9 +138,9 @@ cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts
       err = cudaFuncSetAttribute(place_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kSortWarps * row));
     if (err == cudaSuccess && runs > 1)
-      err = launch(count_kernel<Id>, runs, kSortThreads, row, stream, false, p, n, run, experts, counts);
+      err = launch(count_kernel<Id>, runs, kSortThreads, row, stream, true, p, n, run, experts, counts);
     if (err == cudaSuccess)
-      err = launch(place_kernel<Id>, runs, kSortThreads, kSortWarps * row, stream, runs > 1, p, n, run, runs, experts,
+      err = launch(place_kernel<Id>, runs, kSortThreads, kSortWarps * row, stream, true, p, n, run, runs, experts,
                    counts, position, offsets);
     return err;
   };

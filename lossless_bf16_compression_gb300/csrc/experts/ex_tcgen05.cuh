@@ -87,6 +87,9 @@ __device__ __forceinline__ void arrive_at_leader(uint64_t* bar) {
 
 // ------------------------------------------------------------------ TMA tile loads (this CTA's memory)
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // The bytes are counted at `bar`, a cluster address (with G = 2, the leader's).
 template <int G>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {

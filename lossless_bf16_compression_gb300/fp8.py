@@ -191,8 +191,11 @@ def matmul(a: Matrix, b: Matrix, offsets=None, out_dtype=torch.bfloat16, stream=
     rows, n = a.data.shape[0], held[-2]
     with on(stream, a.data, a.scales, b.data, b.scales, offsets):
         out = torch.empty((rows, n), dtype=out_dtype, device=a.data.device)
+        need = fn("zc_fp8_matmul_workspace")(rows, groups, n, k)
+        scratch = torch.empty(need, dtype=torch.uint8, device=a.data.device) if need else None
         call("zc_fp8_matmul", a.data.data_ptr(), a.scales.data_ptr(), FORMATS[a.fmt], rows, b.data.data_ptr(),
-             b.scales.data_ptr(), FORMATS[b.fmt], groups, n, k, at, out.data_ptr(), n, t, current(device))
+             b.scales.data_ptr(), FORMATS[b.fmt], groups, n, k, at, out.data_ptr(), n, t,
+             None if scratch is None else scratch.data_ptr(), current(device))
     return out
 
 
