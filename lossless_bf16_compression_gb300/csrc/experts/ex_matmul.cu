@@ -72,52 +72,65 @@ struct Shared {
   uint32_t tmem;
   unsigned failed;
   int start[ZC_MOE_MAX_EXPERTS + 2];         // first row (or block) of each group
-  long long tiles[ZC_MOE_MAX_EXPERTS + 2];   // tiles before each group
+  unsigned tiles[ZC_MOE_MAX_EXPERTS + 2];    // tiles before each group
 };
 
 struct Tile {
   int group, p0, q0, q1;  // rows p0 .. of P, rows q0 .. q1 - 1 of Q
   int b0, b1;             // blocks
-  long long index;        // tiles before it
+  unsigned index;         // tiles before it
 };
 
 // Walks the tiles of this CTA (or pair); every role walks them alike.
+// (32-bit arithmetic: the host refuses a product with 2^31 blocks of tiles; 64-bit divisions here
+// took 4 us before the first load.)
 template <int G>
 struct Walk {
   const TileParams& p;
   const Shared& s;
-  long long t;
+  unsigned t;
   int g = 0;
-  long long end = 0;              // of this CTA's blocks
-  long long whole = 0, all = 0;   // tiles that have blocks, and their blocks
-  long long ctas = 1;             // that share them: each gets a word of scales, four blocks, at least
-  __device__ Walk(const TileParams& p_, const Shared& s_) : p(p_), s(s_), t(blockIdx.x / G) {
+  const unsigned p_tiles;
+  unsigned end = 0;             // of this CTA's blocks
+  unsigned whole = 0;           // tiles that have blocks
+  unsigned ctas = 1;            // that share them: each gets a word of scales, four blocks, at least
+  unsigned each = 0, more = 0;  // blocks of a CTA; the first `more` get another one
+  __device__ Walk(const TileParams& p_, const Shared& s_)
+      : p(p_), s(s_), t(blockIdx.x / G), p_tiles((p_.p_rows + kTileP * G - 1) / (kTileP * G)) {
     if (p.parts) {
       whole = s.tiles[p.groups];
-      all = whole * p.blocks;
-      ctas = min(static_cast<long long>(gridDim.x), max(all / 4, 1ll));
+      const unsigned all = whole * p.blocks;
+      ctas = min(gridDim.x, max(all / 4, 1u));
+      each = all / ctas;
+      more = all - each * ctas;
       t = begin_of(blockIdx.x);
       end = begin_of(blockIdx.x + 1);
     }
   }
   // The first block of a CTA, all tiles' blocks in a row, and the CTA that has a block.
-  __device__ long long begin_of(long long cta) const { return min(cta, ctas) * all / ctas; }
-  __device__ long long cta_of(long long block) const { return ((block + 1) * ctas - 1) / all; }
+  __device__ unsigned begin_of(unsigned cta) const {
+    const unsigned c = min(cta, ctas);
+    return c * each + min(c, more);
+  }
+  __device__ unsigned cta_of(unsigned block) const {
+    const unsigned longer = more * (each + 1);
+    return block < longer ? block / (each + 1) : more + (block - longer) / each;
+  }
 
   __device__ bool next(Tile* out) {
     const int last = p.by_blocks ? p.groups : p.groups + 1;
     if (p.parts) {
       if (t >= end) {  // then the tiles without blocks, one after the other
-        const long long zero = whole + blockIdx.x + (t - end) * gridDim.x;
+        const unsigned zero = whole + blockIdx.x + (t - end) * gridDim.x;
         if (zero >= s.tiles[last]) return false;
         ++t;
         locate(zero, out);
         return true;
       }
-      const long long tile = t / p.blocks;
+      const unsigned tile = t / p.blocks;
       locate(tile, out);
-      out->b0 = static_cast<int>(t - tile * p.blocks);
-      out->b1 = static_cast<int>(min(static_cast<long long>(p.blocks), out->b0 + (end - t)));
+      out->b0 = t - tile * p.blocks;
+      out->b1 = min(static_cast<unsigned>(p.blocks), out->b0 + (end - t));
       t += out->b1 - out->b0;
       return true;
     }
@@ -127,24 +140,22 @@ struct Walk {
     return true;
   }
 
-  __device__ void locate(long long tile, Tile* out) {
+  __device__ void locate(unsigned tile, Tile* out) {
     while (s.tiles[g + 1] <= tile) ++g;
-    const int p_tiles = (p.p_rows + kTileP * G - 1) / (kTileP * G);
-    const long long local = tile - s.tiles[g], q_tiles = (s.tiles[g + 1] - s.tiles[g]) / p_tiles;
     // Within a group: bands of kBand rows of P, and in a band all of P's tiles for each of Q's, so
     // that the tiles in flight at a time cover about as many rows of P as of Q.  Shared-out tiles
     // follow one another in a CTA: there Q's tiles for each of P's, whose rows are then in the L2.
-    int q, pt;
+    const unsigned local = tile - s.tiles[g], q_tiles = (s.tiles[g + 1] - s.tiles[g]) / p_tiles;
+    unsigned q, pt;
     if (p.parts) {
-      q = static_cast<int>(local % q_tiles);
-      pt = static_cast<int>(local / q_tiles);
+      pt = local / q_tiles;
+      q = local - pt * q_tiles;
     } else {
-      constexpr int width = kBand / (kTileP * G);
-      const int band = static_cast<int>(local / (width * q_tiles));
-      const int inside = static_cast<int>(local - band * width * q_tiles);
-      const int here = min(width, p_tiles - band * width);
+      constexpr unsigned width = kBand / (kTileP * G);
+      const unsigned band = local / (width * q_tiles), inside = local - band * width * q_tiles;
+      const unsigned here = min(width, p_tiles - band * width);
       q = inside / here;
-      pt = band * width + inside % here;
+      pt = band * width + inside - q * here;
     }
     out->index = tile;
     out->group = g;
@@ -174,8 +185,8 @@ __device__ void plan_tiles(const TileParams& p, Shared& s) {
     if (p.offsets == nullptr) return g == 0 ? 0 : limit;
     return p.offsets[g];
   };
-  const long long p_tiles = (p.p_rows + kTileP * G - 1) / (kTileP * G);
-  long long before = 0;
+  const unsigned p_tiles = (p.p_rows + kTileP * G - 1) / (kTileP * G);
+  unsigned before = 0;
   int floor = 0;  // starts never go back below this
   bool bad = false;
   for (int base = 0; base <= n; base += 32) {
@@ -194,11 +205,11 @@ __device__ void plan_tiles(const TileParams& p, Shared& s) {
       const int r = g + 1 <= n ? start_of(g + 1) : limit;
       next = max(v, min(max(r, 0), limit));
     }
-    const long long q = p.by_blocks ? (p.q_rows + p.tile_q - 1) / p.tile_q : (next - v + p.tile_q - 1) / p.tile_q;
-    long long incl = g < n ? q * p_tiles : 0;
-    const long long mine = incl;
+    const unsigned q = ((p.by_blocks ? p.q_rows : next - v) + p.tile_q - 1) / p.tile_q;
+    unsigned incl = g < n ? q * p_tiles : 0;
+    const unsigned mine = incl;
     for (int d = 1; d < 32; d *= 2) {
-      const long long u = __shfl_up_sync(~0u, incl, d);
+      const unsigned u = __shfl_up_sync(~0u, incl, d);
       if (lane >= d) incl += u;
     }
     if (g <= n) {
@@ -238,10 +249,10 @@ template <typename Out>
 __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const Walk<1>& walk, const Tile& tile,
                                            uint32_t from, unsigned acc, int quarter) {
   const int lane = threadIdx.x % 32, row = 32 * quarter + lane;
-  const long long tile_begin = tile.index * p.blocks;
+  const unsigned tile_begin = tile.index * p.blocks;
   const size_t part = static_cast<size_t>(kTileP) * p.tile_q;
   // a CTA's first place is for the tile that it begins inside, its second for one that it begins
-  const auto place = [&](long long cta) {
+  const auto place = [&](unsigned cta) {
     return p.parts + (2 * cta + (walk.begin_of(cta) > tile_begin ? 0 : 1)) * part + row;
   };
   float* mine = place(blockIdx.x);
@@ -258,17 +269,17 @@ __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const
   unsigned before = 0;
   if (lane == 0) {
     mbar_arrive(&s.sum_empty[acc]);
-    before = atomicAdd(&p.arrivals[tile.index * 4 + quarter], 1u);
+    before = atomicAdd(&p.arrivals[static_cast<size_t>(tile.index) * 4 + quarter], 1u);
   }
   before = __shfl_sync(~0u, before, 0);
-  const long long first = walk.cta_of(tile_begin), last = walk.cta_of(tile_begin + p.blocks - 1);
+  const unsigned first = walk.cta_of(tile_begin), last = walk.cta_of(tile_begin + p.blocks - 1);
   if (before != last - first) return;
   __threadfence();
   const int pr = tile.p0 + row;
   Out* out = static_cast<Out*>(p.out) + static_cast<size_t>(tile.q0) * p.out_pitch + pr;
   for (int c = 0; c < tile.q1 - tile.q0; c += 16) {
     float sum[16] = {};
-    for (long long cta = first; cta <= last; cta += 4) {  // four parts' loads in flight
+    for (unsigned cta = first; cta <= last; cta += 4) {  // four parts' loads in flight
       float v[4][16];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -620,6 +631,7 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
   if (err != cudaSuccess) return err;
   const size_t most = ceil_div(t.p_rows, kTileP * G) *
                       (t.by_blocks ? ceil_div(t.q_rows, t.tile_q) * t.groups : t.q_rows / t.tile_q + t.groups + 1);
+  if (most * (t.parts ? t.blocks : 1) >= size_t(1) << 31) return cudaErrorInvalidValue;
   const size_t room = sm_count(dev) / G;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(t.parts ? room : G * (most < room ? most : room)));
