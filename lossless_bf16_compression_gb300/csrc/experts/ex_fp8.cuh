@@ -36,12 +36,6 @@ __device__ __forceinline__ unsigned nonfinite8(float v, int fmt) {
   const unsigned sign = __float_as_uint(v) >> 31 << 7;
   return fmt == ZC_FP8_E5M2 && isinf(v) ? sign | 0x7Cu : sign | 0x7Fu;
 }
-__device__ __forceinline__ bool finite_bits(uint32_t bits) { return (bits & 0x7F800000u) != 0x7F800000u; }
-// |v|'s bits when v is finite, else 0.
-__device__ __forceinline__ uint32_t finite_magnitude(float v) {
-  const uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
-  return m < 0x7F800000u ? m : 0u;
-}
 
 }  // namespace ex
 }  // namespace zc

@@ -14,6 +14,7 @@ namespace {
 template <typename T>
 union Raw8 {
   uint4 q[sizeof(T) / 2];
+  uint32_t w[2 * sizeof(T)];
   typename Bytes<sizeof(T)>::type bits[8];
   T v[8];
   __device__ Raw8() {}
@@ -36,40 +37,97 @@ __device__ __forceinline__ void load_end(const T* at, int left, Raw8<T>& r) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.bits[i] = load_if<sizeof(T)>(at + i, i < left);
 }
+
+// Magnitudes are compared as the type's own bits without the sign, which order like the values;
+// Inf and NaN are the bits from kInf on.  16-bit values go two at a time.
 template <typename T>
-__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_float(r.v[i]);
-}
+struct Bits;
+template <>
+struct Bits<__nv_bfloat16> {
+  static constexpr uint32_t kInf = 0x7F80;
+  static __device__ uint32_t fp32(uint32_t m) { return m << 16; }
+};
+template <>
+struct Bits<__half> {
+  static constexpr uint32_t kInf = 0x7C00;
+  static __device__ uint32_t fp32(uint32_t m) { return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m)))); }
+};
+template <>
+struct Bits<float> {
+  static constexpr uint32_t kInf = 0x7F800000u;
+  static __device__ uint32_t fp32(uint32_t m) { return m; }
+};
 
-// The bits of the largest finite magnitude of eight values.
-__device__ __forceinline__ uint32_t magnitude8(const float (&v)[8]) {
-  uint32_t m = 0;
+// The largest magnitude of N vectors, value by value: word w of `m` holds that of words w (two
+// values each for 16-bit types).  odd: there is an Inf or NaN among them; they are then left out.
+template <typename T, int N>
+__device__ __forceinline__ void magnitudes(const Raw8<T>* r, uint32_t (&m)[2 * sizeof(T)], bool& odd) {
+  constexpr bool wide = sizeof(T) == 4;
+  constexpr uint32_t mask = wide ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+  constexpr int words = 2 * sizeof(T);
+  uint32_t most = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  if (!finite_bits(m)) {  // Inf or NaN among them: look again without them
-    m = 0;
+  for (int w = 0; w < words; ++w) {
+    m[w] = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(v[i]));
+    for (int i = 0; i < N; ++i) m[w] = wide ? max(m[w], r[i].w[w] & mask) : max_u16x2(m[w], r[i].w[w] & mask);
+    most = wide ? max(most, m[w]) : max_u16x2(most, m[w]);
   }
-  return m;
+  odd = wide ? most >= Bits<T>::kInf : (most & 0xFFFFu) >= Bits<T>::kInf || most >> 16 >= Bits<T>::kInf;
+  if (odd) {
+#pragma unroll
+    for (int w = 0; w < words; ++w) {
+      m[w] = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t v = r[i].w[w] & mask;
+        if (wide) {
+          m[w] = max(m[w], v < Bits<T>::kInf ? v : 0u);
+        } else {
+          const uint32_t lo = v & 0xFFFFu, hi = v >> 16;
+          m[w] = max_u16x2(m[w], (lo < Bits<T>::kInf ? lo : 0u) | (hi < Bits<T>::kInf ? hi : 0u) << 16);
+        }
+      }
+    }
+  }
+}
+// The largest of the words' values.
+template <typename T>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&m)[2 * sizeof(T)]) {
+  uint32_t most = m[0];
+#pragma unroll
+  for (int w = 1; w < static_cast<int>(2 * sizeof(T)); ++w) most = sizeof(T) == 4 ? max(most, m[w]) : max_u16x2(most, m[w]);
+  return sizeof(T) == 4 ? most : max(most & 0xFFFFu, most >> 16);
 }
 
-// Four values times f rounded, the first in the low byte.
+// Four values times f rounded, the first in the low byte.  odd: there may be an Inf or NaN, which
+// does not go through the saturating conversion.
 template <int Fmt>
-__device__ __forceinline__ uint32_t round8x4(float a, float b, float c, float d, float f) {
+__device__ __forceinline__ uint32_t round8x4(float a, float b, float c, float d, float f, bool odd) {
   uint32_t r = round8x2(a * f, b * f, Fmt) | static_cast<uint32_t>(round8x2(c * f, d * f, Fmt)) << 16;
-  // an infinity or NaN does not go through the saturating conversion
-  const auto fix = [&](float v, int i) {
-    if (!isfinite(v)) r = (r & ~(0xFFu << (8 * i))) | nonfinite8(v, Fmt) << (8 * i);
-  };
-  if (!(isfinite(a) && isfinite(b) && isfinite(c) && isfinite(d))) {
+  if (odd) {
+    const auto fix = [&](float v, int i) {
+      if (!isfinite(v)) r = (r & ~(0xFFu << (8 * i))) | nonfinite8(v, Fmt) << (8 * i);
+    };
     fix(a, 0);
     fix(b, 1);
     fix(c, 2);
     fix(d, 3);
   }
   return r;
+}
+// Eight values of a row.
+template <int Fmt, typename T>
+__device__ __forceinline__ uint2 round_row(const Raw8<T>& r, float f, bool odd) {
+  return make_uint2(round8x4<Fmt>(to_float(r.v[0]), to_float(r.v[1]), to_float(r.v[2]), to_float(r.v[3]), f, odd),
+                    round8x4<Fmt>(to_float(r.v[4]), to_float(r.v[5]), to_float(r.v[6]), to_float(r.v[7]), f, odd));
+}
+// Value j of eight rows.
+template <int Fmt, typename T>
+__device__ __forceinline__ uint2 round_column(const Raw8<T> (&r)[8], int j, float f, bool odd) {
+  return make_uint2(
+      round8x4<Fmt>(to_float(r[0].v[j]), to_float(r[1].v[j]), to_float(r[2].v[j]), to_float(r[3].v[j]), f, odd),
+      round8x4<Fmt>(to_float(r[4].v[j]), to_float(r[5].v[j]), to_float(r[6].v[j]), to_float(r[7].v[j]), f, odd));
 }
 
 // A warp takes four blocks (one scale word) of each of R rows: lane l holds values 8l .. 8l + 7
@@ -111,15 +169,14 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
     int s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float a[8];
-      unpack8(raw[i][h], a);
-      uint32_t m = magnitude8(a);
+      uint32_t words[2 * sizeof(T)];
+      bool odd;
+      magnitudes<T, 1>(&raw[i][h], words, odd);
+      uint32_t m = largest<T>(words);
 #pragma unroll
       for (int d = 8; d; d /= 2) m = max(m, __shfl_xor_sync(~0u, m, d));
-      s[h] = block_exponent(m, Fmt);
-      const float f = inverse_scale(s[h]);
-      const uint2 q = make_uint2(round8x4<Fmt>(a[0], a[1], a[2], a[3], f),
-                                 round8x4<Fmt>(a[4], a[5], a[6], a[7], f));
+      s[h] = block_exponent(Bits<T>::fp32(m), Fmt);
+      const uint2 q = round_row<Fmt>(raw[i][h], inverse_scale(s[h]), odd);
       const int c = c0 + h * 2 * kBlock;
       if (c < wide) *reinterpret_cast<uint2*>(values + r * wide + c) = q;
     }
@@ -163,7 +220,7 @@ __global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restri
 
 struct TileShared {
   alignas(16) uint2 turned[kBlock * 16];  // [column][unit of 8 rows], the unit at place unit ^ (column / 8)
-  alignas(16) uint32_t amax[16][kBlock];
+  alignas(16) uint32_t amax[16][kBlock];  // 16-bit types: two columns a word
   float inverse[kBlock];
 };
 
@@ -179,7 +236,7 @@ __device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
 }
 
 template <typename T, bool Vec, int Fmt>
-__global__ void __launch_bounds__(256) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
                                                                int cols, int groups, const int* __restrict__ offsets,
                                                                int capacity, uint8_t* __restrict__ values,
                                                                uint8_t* __restrict__ scales,
@@ -204,30 +261,26 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const T* __restri
   }
   __syncthreads();
   Raw8<T> raw[8];
-  float v[8][8];
   const long long r0 = static_cast<long long>(first) + rg * 8;
 #pragma unroll
   for (int i = 0; i < 8; ++i) load8<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < last ? cols - c : 0, raw[i]);
   if (Vec && cols % 8)
 #pragma unroll
     for (int i = 0; i < 8; ++i) load_end<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < last ? cols - c : 0, raw[i]);
+  constexpr int words = 2 * sizeof(T);  // of eight columns
+  uint32_t most[words];
+  bool odd;
+  magnitudes<T, 8>(raw, most, odd);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) unpack8(raw[i], v[i]);
-  uint32_t most[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float column[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
-    most[j] = magnitude8(column);
-  }
-  uint4* to = reinterpret_cast<uint4*>(&s.amax[rg][cg * 8]);
-  to[0] = make_uint4(most[0], most[1], most[2], most[3]);
-  to[1] = make_uint4(most[4], most[5], most[6], most[7]);
+  for (int w = 0; w < words; w += 4)
+    *reinterpret_cast<uint4*>(&s.amax[rg][cg * words + w]) = make_uint4(most[w], most[w + 1], most[w + 2], most[w + 3]);
   __syncthreads();
   if (tid < kBlock) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, s.amax[i][tid]);
-    const int e = block_exponent(m, Fmt);
+    for (int i = 0; i < 16; ++i)
+      m = max(m, sizeof(T) == 4 ? s.amax[i][tid] : reinterpret_cast<const unsigned short*>(s.amax[i])[tid]);
+    const int e = block_exponent(Bits<T>::fp32(m), Fmt);
     s.inverse[tid] = inverse_scale(e);
     const size_t row = static_cast<size_t>(blockIdx.y) * kBlock + tid;
     if (row < static_cast<size_t>(cols)) {
@@ -238,12 +291,7 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const T* __restri
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = s.inverse[cg * 8 + j];
-    put_column(s, cg * 8 + j, rg,
-               make_uint2(round8x4<Fmt>(v[0][j], v[1][j], v[2][j], v[3][j], f),
-                          round8x4<Fmt>(v[4][j], v[5][j], v[6][j], v[7][j], f)));
-  }
+  for (int j = 0; j < 8; ++j) put_column(s, cg * 8 + j, rg, round_column<Fmt>(raw, j, s.inverse[cg * 8 + j], odd));
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -256,7 +304,7 @@ __global__ void __launch_bounds__(256) quantize_columns_kernel(const T* __restri
 
 // One scale for the tile; its rows are written from registers, its transpose through shared memory.
 template <typename T, bool Vec, int Fmt>
-__global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restrict__ w, int rows, int cols,
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_weight_kernel(const T* __restrict__ w, int rows, int cols,
                                                               uint8_t* __restrict__ values,
                                                               uint8_t* __restrict__ scales,
                                                               uint8_t* __restrict__ values_t,
@@ -270,8 +318,6 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restric
   const int c = bc * kBlock + cg * 8;
   w += g * rows * cols;
   Raw8<T> raw[8];
-  float v[8][8];
-  uint32_t m = 0;
   const int r0 = br * kBlock + rg * 8;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -280,25 +326,20 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restric
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       load_end<T, Vec>(w + static_cast<size_t>(r0 + i) * cols + c, r0 + i < rows ? cols - c : 0, raw[i]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) unpack8(raw[i], v[i]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, magnitude8(v[i]));
-  m = __reduce_max_sync(~0u, m);
+  uint32_t words[2 * sizeof(T)];
+  bool odd;
+  magnitudes<T, 8>(raw, words, odd);
+  uint32_t m = __reduce_max_sync(~0u, largest<T>(words));
   if (tid % 32 == 0) s.amax[0][tid / 32] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, s.amax[0][i]);
-  const int e = block_exponent(m, Fmt);
+  const int e = block_exponent(Bits<T>::fp32(m), Fmt);
   const float f = inverse_scale(e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = br * kBlock + rg * 8 + i;
-    if (r < rows)
-      *reinterpret_cast<uint2*>(values + ((g * rows + r) * cb + bc) * kBlock + cg * 8) =
-          make_uint2(round8x4<Fmt>(v[i][0], v[i][1], v[i][2], v[i][3], f),
-                     round8x4<Fmt>(v[i][4], v[i][5], v[i][6], v[i][7], f));
-  }
+  for (int i = 0; i < 8; ++i)
+    if (r0 + i < rows)
+      *reinterpret_cast<uint2*>(values + ((g * rows + r0 + i) * cb + bc) * kBlock + cg * 8) = round_row<Fmt>(raw[i], f, odd);
   // the block's scale for each of its rows (and, behind the last block, the word's empty bytes)
   const auto put_scales = [&](uint8_t* to, int n, int block_row, int b, int blocks) {
     to += g * ((blocks + 3) / 4) * 4 * n;
@@ -313,10 +354,7 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const T* __restric
   if (values_t == nullptr) return;
   put_scales(scales_t, cols, bc, br, rb);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    put_column(s, cg * 8 + j, rg,
-               make_uint2(round8x4<Fmt>(v[0][j], v[1][j], v[2][j], v[3][j], f),
-                          round8x4<Fmt>(v[4][j], v[5][j], v[6][j], v[7][j], f)));
+  for (int j = 0; j < 8; ++j) put_column(s, cg * 8 + j, rg, round_column<Fmt>(raw, j, f, odd));
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
