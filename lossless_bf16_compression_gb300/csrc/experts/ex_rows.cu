@@ -13,6 +13,9 @@ namespace ex {
 namespace {
 
 constexpr int kMaxThreads = 256;
+// Smaller CTAs keep an SM's loads further apart: combine of 16384 x 8 x 7168 with 256 threads 365
+// us, with 128 336 us; of 4999 x 6 x 2050 53 and 41 us.
+constexpr int kCombineThreads = 128;
 constexpr int kBatch = 8;  // slots whose rows a thread has in flight
 
 // A position that may be used as an address; reported otherwise.
@@ -22,41 +25,69 @@ __device__ __forceinline__ bool in_range(int p, size_t slots, int* status) {
   return false;
 }
 
-// How a row's vectors are shared out: `parts` CTAs a row, one vector a thread.
+// Vectors of a row that a thread takes, a row's threads apart.  Rows that only 4-byte (or smaller)
+// vectors divide need more of them in flight.
+constexpr int per_thread(int bytes) { return bytes == 16 ? 1 : 4; }
+
+// How a row's vectors are shared out: to `parts` CTAs of `threads`.
 struct Cut {
   unsigned parts, threads;
 };
-Cut cut_row(size_t vecs, unsigned most) {
+Cut cut_row(size_t vecs, int bytes, unsigned most_threads) {
+  const unsigned u = per_thread(bytes), most = most_threads * u;
   const unsigned parts = static_cast<unsigned>((vecs + most - 1) / most);
-  const unsigned each = static_cast<unsigned>((vecs + parts - 1) / parts);
+  const unsigned each = static_cast<unsigned>((vecs + parts * u - 1) / (parts * u));
   return {parts, (each + 31) / 32 * 32};
 }
-
-// Writes this thread's vector of a token to its slots' rows.
-template <typename V>
-__device__ __forceinline__ void spread(const V& v, uint8_t* rows, size_t rows_pitch, int c, const int* position, int k,
-                                       size_t slots, int kept, int* status) {
-  for (int j = 0; j < k; ++j) {
-    const int p = position[j];
-    if (in_range(p, slots, status)) reinterpret_cast<V*>(rows + p * rows_pitch)[c] = p < kept ? v : V{};
-  }
+// This thread's first vector.
+template <int B>
+__device__ __forceinline__ int first_vector(unsigned parts) {
+  return static_cast<int>(blockIdx.x % parts * blockDim.x * per_thread(B) + threadIdx.x);
 }
+// A token's vectors as a thread holds them, and to a slot's row.
+template <int B>
+struct Held {
+  static constexpr int U = per_thread(B);
+  using V = typename Bytes<B>::type;
+  V v[U];
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int vecs) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = c + u * static_cast<int>(blockDim.x);
+      v[u] = load_if<B>(row + static_cast<size_t>(at) * B, at < vecs);
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* row, int c, int vecs, bool zeros) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = c + u * static_cast<int>(blockDim.x);
+      if (at < vecs) reinterpret_cast<V*>(row)[at] = zeros ? V{} : v[u];
+    }
+  }
+};
 
-// rows[position[t, j]] = x[t].
+// rows[position[t, j]] = x[t].  Short rows share a CTA, one token for each threadIdx.y: it only stores,
+// so what bounds them is how fast CTAs start (16384 x 2 x 1024: 28 -> 22 us; the other kernels
+// lose more by giving up uniform registers for a token's positions and addresses, the combine
+// gradient at that size 53 -> 84 us).
 template <int B>
 __global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __restrict__ x, size_t x_pitch,
                                                                uint8_t* __restrict__ rows, size_t rows_pitch, int vecs,
-                                                               unsigned parts, int k, size_t slots,
+                                                               unsigned parts, size_t tokens, int k,
                                                                const int* __restrict__ position,
                                                                const int* __restrict__ total, int* status) {
-  using V = typename Bytes<B>::type;
   let_next_start();
-  const size_t t = blockIdx.x / parts;
-  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
-  V v{};
-  if (c < vecs) v = reinterpret_cast<const V*>(x + t * x_pitch)[c];  // x does not come from the sort
+  const size_t t = static_cast<size_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y, slots = tokens * k;
+  const int c = first_vector<B>(parts);
+  if (t >= tokens) return;
+  Held<B> held;
+  held.load(x + t * x_pitch, c, vecs);  // x does not come from the sort
   wait_for_previous();
-  if (c < vecs) spread(v, rows, rows_pitch, c, position + t * k, k, slots, *total, status);
+  const int kept = *total;
+  for (int j = 0; j < k; ++j) {
+    const int p = position[t * k + j];
+    if (in_range(p, slots, status)) held.store(rows + p * rows_pitch, c, vecs, p >= kept);
+  }
 }
 
 // Sort and dispatch of few slots in one launch: every CTA counts, for the slots of its token, the
@@ -69,7 +100,6 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
     const Id* __restrict__ ids, int slots, int experts, const uint8_t* __restrict__ x, size_t x_pitch,
     uint8_t* __restrict__ rows, size_t rows_pitch, int vecs, unsigned parts, int k, int* __restrict__ position,
     int* __restrict__ offsets) {
-  using V = typename Bytes<B>::type;
   __shared__ short keys[kSmallSlots];
   __shared__ int place[ZC_MOE_MAX_K];
   __shared__ int bins[ZC_MOE_MAX_EXPERTS + 1];
@@ -77,9 +107,9 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   let_next_start();
   wait_for_previous();
   const int t = static_cast<int>(blockIdx.x / parts), part = static_cast<int>(blockIdx.x % parts);
-  const int c = part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x), lane = threadIdx.x % 32;
-  V v{};
-  if (c < vecs) v = reinterpret_cast<const V*>(x + t * x_pitch)[c];
+  const int c = first_vector<B>(parts), lane = threadIdx.x % 32;
+  Held<B> held;
+  held.load(x + t * x_pitch, c, vecs);
   const bool starts = blockIdx.x == 0;  // this CTA writes the offsets as well
   if (threadIdx.x < ZC_MOE_MAX_K) place[threadIdx.x] = 0;
   if (threadIdx.x == 0) kept = 0;
@@ -109,11 +139,10 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   }
   __syncthreads();
   if (part == 0 && static_cast<int>(threadIdx.x) < k) position[t * k + threadIdx.x] = place[threadIdx.x];
-  if (c < vecs)
-    for (int j = 0; j < k; ++j) {
-      const int p = place[j];
-      reinterpret_cast<V*>(rows + p * rows_pitch)[c] = p < kept ? v : V{};
-    }
+  for (int j = 0; j < k; ++j) {
+    const int p = place[j];
+    held.store(rows + p * rows_pitch, c, vecs, p >= kept);
+  }
   if (starts && threadIdx.x < 32) {
     int before = 0;
     for (int base = 0; base <= experts; base += 32) {
@@ -130,48 +159,63 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   }
 }
 
-// out[t] = sum over j of weights[t, j] rows[position[t, j]].
-template <typename T, int B>
-__global__ void __launch_bounds__(kMaxThreads) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
+// out[t] = sum over j of weights[t, j] rows[position[t, j]].  A thread takes Tokens tokens that follow
+// one another, with kBatch / Tokens of each one's slots at a time: eight rows in flight however few
+// slots a token has.
+template <typename T, int B, int Tokens, bool Weighted>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
                                                               const float* __restrict__ weights,
                                                               uint8_t* __restrict__ out, size_t out_pitch, int vecs,
-                                                              unsigned parts, int k, size_t slots,
+                                                              unsigned parts, size_t tokens, int k,
                                                               const int* __restrict__ position,
                                                               const int* __restrict__ total, int* status) {
-  constexpr int N = B / sizeof(T);
+  constexpr int N = B / sizeof(T), U = per_thread(B), S = kBatch / Tokens;
   let_next_start();
   wait_for_previous();
-  const size_t t = blockIdx.x / parts;
-  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
-  if (c >= vecs) return;
+  const size_t t0 = static_cast<size_t>(blockIdx.x / parts) * Tokens, slots = tokens * k;
+  const int c = first_vector<B>(parts);
+  if (c >= vecs || t0 >= tokens) return;
   const int kept = *total;
-  float acc[N] = {};
-  for (int j0 = 0; j0 < k; j0 += kBatch) {
-    Pack<T, B> v[kBatch];
+  float acc[Tokens][U][N] = {};
+  for (int j0 = 0; j0 < k; j0 += S) {
+    Pack<T, B> v[kBatch][U];
     float w[kBatch];
     int at[kBatch];
     bool here[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const size_t s = t * k + min(j0 + i, k - 1);
+      const size_t t = min(t0 + i / S, tokens - 1), s = t * k + min(j0 + i % S, k - 1);
       at[i] = position[s];
-      w[i] = weights ? weights[s] : 1.f;
+      w[i] = Weighted ? weights[s] : 1.f;
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      here[i] = j0 + i < k && in_range(at[i], slots, status) && at[i] < kept;
-      v[i].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(c) * B, here[i]);
+      here[i] = j0 + i % S < k && t0 + i / S < tokens && in_range(at[i], slots, status) && at[i] < kept;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int cu = c + u * static_cast<int>(blockDim.x);
+        v[i][u].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(cu) * B, here[i] && cu < vecs);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        acc[e] = here[i] ? fmaf(w[i], to_float(v[i].v[e]), acc[e]) : acc[e];
-  }
-  Pack<T, B> o;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-  for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[e]);
-  reinterpret_cast<typename Bytes<B>::type*>(out + t * out_pitch)[c] = o.raw;
+        for (int e = 0; e < N; ++e)
+          acc[i / S][u][e] = here[i] ? fmaf(w[i], to_float(v[i][u].v[e]), acc[i / S][u][e]) : acc[i / S][u][e];
+  }
+#pragma unroll
+  for (int i = 0; i < Tokens; ++i)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int cu = c + u * static_cast<int>(blockDim.x);
+      Pack<T, B> o;
+#pragma unroll
+      for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[i][u][e]);
+      if (cu < vecs && t0 + i < tokens)
+        reinterpret_cast<typename Bytes<B>::type*>(out + (t0 + i) * out_pitch)[cu] = o.raw;
+    }
 }
 
 // d_rows[position[t, j]] = weights[t, j] d_out[t], d_weights[t, j] = <d_out[t], rows[...]>.  One
@@ -180,14 +224,14 @@ template <typename T, int B>
 __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
     const uint8_t* __restrict__ d_out, size_t d_out_pitch, const uint8_t* __restrict__ rows, size_t rows_pitch,
     const float* __restrict__ weights, uint8_t* __restrict__ d_rows, size_t d_rows_pitch, float* __restrict__ d_weights,
-    int vecs, int k, size_t slots, const int* __restrict__ position, const int* __restrict__ total, int* status) {
+    int vecs, size_t tokens, int k, const int* __restrict__ position, const int* __restrict__ total, int* status) {
   constexpr int N = B / sizeof(T);
   using V = typename Bytes<B>::type;
   __shared__ float sums[kBatch][kMaxThreads / 32];
   let_next_start();
   wait_for_previous();
-  const size_t t = blockIdx.x;
-  const int kept = *total, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const size_t t = blockIdx.x, slots = tokens * k;
+  const int kept = *total, warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int j0 = 0; j0 < k; j0 += kBatch) {
     int at[kBatch];
     float w[kBatch], dot[kBatch];
@@ -209,7 +253,6 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
         r[i].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(c) * B, here[i]);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        if (!ok[i]) continue;
         Pack<T, B> o;
         o.raw = V{};
         if (here[i]) {
@@ -220,7 +263,7 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
             dot[i] = fmaf(g, to_float(r[i].v[e]), dot[i]);
           }
         }
-        reinterpret_cast<V*>(d_rows + at[i] * d_rows_pitch)[c] = o.raw;
+        if (ok[i]) reinterpret_cast<V*>(d_rows + at[i] * d_rows_pitch)[c] = o.raw;
       }
     }
 #pragma unroll
@@ -231,7 +274,7 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
     __syncthreads();
     if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < k) {
       float s = 0.f;
-      for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += sums[threadIdx.x][i];
+      for (int i = 0; i < warps; ++i) s += sums[threadIdx.x][i];
       d_weights[t * k + j0 + threadIdx.x] = s;
     }
     __syncthreads();
@@ -261,11 +304,13 @@ cudaError_t launch_dispatch(const RowShape& s, const void* x, size_t x_pitch, vo
   const size_t b = type_bytes(s.type);
   const int v = vector_bytes(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
   const size_t vecs = s.hidden * b / v;
-  const Cut cut = cut_row(vecs, kMaxThreads);
+  const Cut cut = cut_row(vecs, v, kMaxThreads);
   return by_bytes(v, [&](auto bytes) {
-    return launch(dispatch_kernel<bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, cut.threads, 0, stream, true,
+    const unsigned together = kMaxThreads / cut.threads;  // tokens of a CTA
+    return launch(dispatch_kernel<bytes()>, static_cast<unsigned>((s.tokens + together - 1) / together) * cut.parts,
+                  dim3(cut.threads, together), 0, stream, true,
                   static_cast<const uint8_t*>(x), x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b,
-                  static_cast<int>(vecs), cut.parts, s.k, s.tokens * s.k, position, offsets + s.experts, status);
+                  static_cast<int>(vecs), cut.parts, s.tokens, s.k, position, offsets + s.experts, status);
   });
 }
 
@@ -276,7 +321,7 @@ cudaError_t launch_small_dispatch(const RowShape& s, const void* ids, int id_byt
   const size_t b = type_bytes(s.type);
   const int v = vector_bytes(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
   const size_t vecs = s.hidden * b / v;
-  const Cut cut = cut_row(vecs, kMaxThreads);
+  const Cut cut = cut_row(vecs, v, kMaxThreads);
   const unsigned threads = cut.threads < 64 ? 64 : cut.threads;  // at least ZC_MOE_MAX_K
   return by_bytes(v, [&](auto bytes) {
     const auto go = [&](auto* p) {
@@ -296,12 +341,20 @@ cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitc
   const size_t b = type_bytes(s.type);
   const int v = vector_bytes(b, s.hidden, {rows, out}, {rows_pitch, out_pitch});
   const size_t vecs = s.hidden * b / v;
-  const Cut cut = cut_row(vecs, kMaxThreads);
-  return by_type(s.type, v, [&](auto type, auto bytes) {
-    return launch(combine_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, cut.threads, 0,
-                  stream, true, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
-                  static_cast<uint8_t*>(out), out_pitch * b, static_cast<int>(vecs), cut.parts, s.k, s.tokens * s.k,
+  const Cut cut = cut_row(vecs, v, kCombineThreads);
+  const auto go = [&](auto type, auto bytes, auto tokens) {
+    return launch(weights ? combine_kernel<decltype(type), bytes(), tokens(), true>
+                          : combine_kernel<decltype(type), bytes(), tokens(), false>,
+                  static_cast<unsigned>((s.tokens + tokens() - 1) / tokens()) * cut.parts, cut.threads, 0, stream, true,
+                  static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(out), out_pitch * b, static_cast<int>(vecs), cut.parts, s.tokens, s.k,
                   position, offsets + s.experts, status);
+  };
+  return by_type(s.type, v, [&](auto type, auto bytes) {
+    // few tokens: one a thread, so that they spread over the SMs
+    const bool many = s.tokens * cut.parts >= 2048;
+    return many && s.k <= 2   ? go(type, bytes, std::integral_constant<int, 4>{})
+           : many && s.k <= 4 ? go(type, bytes, std::integral_constant<int, 2>{})
+                              : go(type, bytes, std::integral_constant<int, 1>{});
   });
 }
 
@@ -313,11 +366,16 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
   const int v = vector_bytes(b, s.hidden, {d_out, rows, d_rows}, {d_out_pitch, rows_pitch, d_rows_pitch});
   const size_t vecs = s.hidden * b / v;
   return by_type(s.type, v, [&](auto type, auto bytes) {
+    // A token's sums need all of its row, which the CTA's threads walk: with few tokens more threads
+    // finish a row sooner (1 token x 8 x 7168: 12 us with 256, 16 with 128, 25 with 64), with many
+    // fewer leave more CTAs to an SM (16384 x 2 x 1024: 41 us with 64, 53 with 128, 16384 x 8 x
+    // 7168: 582 and 576).
+    const unsigned most = s.tokens < 2048 ? 256 : vecs <= 256 ? 64 : 128;
     return launch(combine_grad_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens),
-                  cut_row(vecs, kMaxThreads).threads, 0, stream, true, static_cast<const uint8_t*>(d_out),
-                  d_out_pitch * b, static_cast<const uint8_t*>(rows), rows_pitch * b, weights,
-                  static_cast<uint8_t*>(d_rows), d_rows_pitch * b, d_weights, static_cast<int>(vecs), s.k,
-                  s.tokens * s.k, position, offsets + s.experts, status);
+                  cut_row(vecs, 16, most).threads, 0, stream, true,
+                  static_cast<const uint8_t*>(d_out), d_out_pitch * b, static_cast<const uint8_t*>(rows),
+                  rows_pitch * b, weights, static_cast<uint8_t*>(d_rows), d_rows_pitch * b, d_weights,
+                  static_cast<int>(vecs), s.tokens, s.k, position, offsets + s.experts, status);
   });
 }
 
