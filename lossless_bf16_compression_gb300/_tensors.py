@@ -45,7 +45,7 @@ def fn(name):
 
 
 def call(name, *args):
-    rc = fn(name)(*args)
+    rc = (_fns.get(name) or fn(name))(*args)
     if rc != binding.ZC_OK:
         raise binding.ZcError(rc, name)
 
@@ -65,7 +65,7 @@ def on_device(name, t, device, dtypes=None, dim=None):
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
     if device is None:
-        device = torch.cuda.current_device()
+        device = torch._C._cuda_getDevice()
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     return device
@@ -80,20 +80,16 @@ def rows_of(t):
     return t, (pitch if rows > 1 else cols)
 
 
-_same_stream = contextlib.nullcontext()
-
-
-def on(stream, *used):
-    """A context in which a call's outputs are allocated for `stream` (None: the current one).  The tensors `used`
-    there are kept from reuse until the stream has passed the call."""
+def on(stream, used, f, *args):
+    """f(*args) with `stream` (None: the current one) as the current stream, so that what it allocates is the
+    stream's.  The tensors `used` there are kept from reuse until the stream has passed the call."""
     if stream is None:
-        return _same_stream
+        return f(*args)
     for t in used:
         if t is not None:
             t.record_stream(stream)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
-def current(device):
-    """The handle of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device)
+current = torch._C._cuda_getCurrentRawStream  # (device) -> the handle of its current stream

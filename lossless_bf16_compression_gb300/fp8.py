@@ -12,8 +12,6 @@ scaling is exact and only the rounding to 8 bits loses anything.  Sums are taken
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
-
 import torch
 
 from ._tensors import MAX_EXPERTS, TYPES, call, check, current, fn, on, on_device, rows_of
@@ -23,7 +21,6 @@ FORMATS = {"e4m3": 0, "e5m2": 1}
 _FLOAT8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 
 
-@dataclass(frozen=True, eq=False)
 class Matrix:
     """A matrix (or one for each expert) in 8-bit blocks.
 
@@ -35,24 +32,22 @@ class Matrix:
     offsets  from quantize_columns: the first block of each group, int32 [groups + 1]
     """
 
-    data: torch.Tensor
-    scales: torch.Tensor
-    cols: int
-    fmt: str = "e4m3"
-    offsets: torch.Tensor | None = None
+    __slots__ = ("data", "scales", "cols", "fmt", "offsets")
 
-    def __post_init__(self):
-        check(self.fmt in FORMATS, f"fmt must be one of {', '.join(FORMATS)}, got {self.fmt!r}")
-        d, s = self.data, self.scales
-        if d.dtype != torch.uint8 or s.dtype != torch.uint8:
+    def __init__(self, data, scales, cols, fmt="e4m3", offsets=None):
+        _format(fmt)
+        if data.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("data and scales must be uint8")
-        check(d.device == s.device, f"data is on {d.device}, scales on {s.device}")
-        check(d.dim() in (2, 3) and s.dim() == d.dim() + 1, f"data {tuple(d.shape)} and scales {tuple(s.shape)} do not fit")
-        check(d.is_contiguous() and s.is_contiguous(), "data and scales must be contiguous")
-        pitch = _pitch(self.cols)
-        check(self.cols >= 0 and d.shape[-1] == pitch, f"rows of {self.cols} values take {pitch} bytes, got {d.shape[-1]}")
-        check(tuple(s.shape) == (*d.shape[:-2], -(-pitch // 512), d.shape[-2], 4),
-              f"scales of {tuple(d.shape)} cannot have the shape {tuple(s.shape)}")
+        if data.device != scales.device:
+            raise ValueError(f"data is on {data.device}, scales on {scales.device}")
+        if not (data.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("data and scales must be contiguous")
+        shape, pitch = data.shape, _pitch(cols)
+        if len(shape) not in (2, 3) or cols < 0 or shape[-1] != pitch:
+            raise ValueError(f"rows of {cols} values take {pitch} bytes, data is {tuple(shape)}")
+        if scales.shape != (*shape[:-2], -(-pitch // 512), shape[-2], 4):
+            raise ValueError(f"scales of {tuple(shape)} cannot have the shape {tuple(scales.shape)}")
+        self.data, self.scales, self.cols, self.fmt, self.offsets = data, scales, cols, fmt, offsets
 
     @property
     def rows(self) -> int:
@@ -75,7 +70,7 @@ _INT32 = (torch.int32,)
 def _made(data, scales, cols, fmt, offsets=None):
     """A Matrix of this module's own making: its parts fit and are not looked at again."""
     m = object.__new__(Matrix)
-    m.__dict__.update(data=data, scales=scales, cols=cols, fmt=fmt, offsets=offsets)
+    m.data, m.scales, m.cols, m.fmt, m.offsets = data, scales, cols, fmt, offsets
     return m
 
 
@@ -90,8 +85,10 @@ def _empty(lead, rows, cols, device):
 
 
 def _format(fmt):
-    check(fmt in FORMATS, f"fmt must be one of {', '.join(FORMATS)}, got {fmt!r}")
-    return FORMATS[fmt]
+    f = FORMATS.get(fmt)
+    if f is None:
+        raise ValueError(f"fmt must be one of {', '.join(FORMATS)}, got {fmt!r}")
+    return f
 
 
 def _input(name, x):
@@ -116,12 +113,15 @@ def quantize(x, fmt: str = "e4m3", stream=None) -> Matrix:
     """x [rows, cols] (bfloat16, float16 or float32, any row stride) in blocks of 128 along its rows."""
     f = _format(fmt)
     device = _input("x", x)
+    return on(stream, (x,), _quantize, x, f, fmt, device)
+
+
+def _quantize(x, f, fmt, device):
+    x, pitch = rows_of(x)
     rows, cols = x.shape
-    with on(stream, x):
-        x, pitch = rows_of(x)
-        data, scales = _empty((), rows, cols, x.device)
-        call("zc_fp8_quantize", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, f, data.data_ptr(), scales.data_ptr(),
-             current(device))
+    data, scales = _empty((), rows, cols, x.device)
+    call("zc_fp8_quantize", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, f, data.data_ptr(), scales.data_ptr(),
+         current(device))
     return _made(data, scales, cols, fmt)
 
 
@@ -133,14 +133,17 @@ def quantize_columns(x, offsets=None, fmt: str = "e4m3", stream=None) -> Matrix:
     f = _format(fmt)
     device = _input("x", x)
     groups, at = _offsets(offsets, device)
+    return on(stream, (x, offsets), _quantize_columns, x, groups, at, f, fmt, device)
+
+
+def _quantize_columns(x, groups, at, f, fmt, device):
+    x, pitch = rows_of(x)
     rows, cols = x.shape
-    with on(stream, x, offsets):
-        x, pitch = rows_of(x)
-        wide = fn("zc_fp8_column_blocks")(rows, groups) * BLOCK
-        data, scales = _empty((), cols, wide, x.device)
-        starts = torch.empty(groups + 1, dtype=torch.int32, device=x.device)
-        call("zc_fp8_quantize_columns", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, groups, at, f,
-             data.data_ptr(), scales.data_ptr(), starts.data_ptr(), current(device))
+    wide = fn("zc_fp8_column_blocks")(rows, groups) * BLOCK
+    data, scales = _empty((), cols, wide, x.device)
+    starts = torch.empty(groups + 1, dtype=torch.int32, device=x.device)
+    call("zc_fp8_quantize_columns", x.data_ptr(), pitch, TYPES[x.dtype], rows, cols, groups, at, f, data.data_ptr(),
+         scales.data_ptr(), starts.data_ptr(), current(device))
     return _made(data, scales, wide, fmt, starts)
 
 
@@ -149,16 +152,18 @@ def quantize_weight(w, fmt: str = "e4m3", transposed: bool = True, stream=None) 
     f = _format(fmt)
     device = on_device("w", w, None, _ROW_TYPES)
     check(w.dim() in (2, 3) and min(w.shape) >= 1, f"w must be [n, k] or [experts, n, k], got {tuple(w.shape)}")
+    check(w.dim() == 2 or w.shape[0] <= MAX_EXPERTS, f"at most {MAX_EXPERTS} experts")
+    return on(stream, (w,), _quantize_weight, w, f, fmt, transposed, device)
+
+
+def _quantize_weight(w, f, fmt, transposed, device):
+    w = w.contiguous()
     lead, n, k = tuple(w.shape[:-2]), *w.shape[-2:]
-    groups = lead[0] if lead else 1
-    check(groups <= MAX_EXPERTS, f"at most {MAX_EXPERTS} experts")
-    with on(stream, w):
-        w = w.contiguous()
-        data, scales = _empty(lead, n, k, w.device)
-        data_t, scales_t = _empty(lead, k, n, w.device) if transposed else (None, None)
-        call("zc_fp8_quantize_weight", w.data_ptr(), TYPES[w.dtype], groups, n, k, f, data.data_ptr(),
-             scales.data_ptr(), data_t.data_ptr() if transposed else None, scales_t.data_ptr() if transposed else None,
-             current(device))
+    data, scales = _empty(lead, n, k, w.device)
+    data_t, scales_t = _empty(lead, k, n, w.device) if transposed else (None, None)
+    call("zc_fp8_quantize_weight", w.data_ptr(), TYPES[w.dtype], lead[0] if lead else 1, n, k, f, data.data_ptr(),
+         scales.data_ptr(), data_t.data_ptr() if transposed else None, scales_t.data_ptr() if transposed else None,
+         current(device))
     return _made(data, scales, k, fmt), _made(data_t, scales_t, n, fmt) if transposed else None
 
 
@@ -182,20 +187,23 @@ def matmul(a: Matrix, b: Matrix, offsets=None, out_dtype=torch.bfloat16, stream=
     device = _operand("a", a, None, 2)
     _operand("b", b, device)
     groups, at = _offsets(offsets, device)
-    k = a.cols
-    if k != b.cols or k < 1:
-        raise ValueError(f"a has rows of {k} values, b of {b.cols}")
+    if a.cols != b.cols or a.cols < 1:
+        raise ValueError(f"a has rows of {a.cols} values, b of {b.cols}")
     held = b.data.shape
     if (held[0] if len(held) == 3 else 1) != groups:
         raise ValueError(f"b must hold {groups} matrices, got {tuple(held)}")
-    rows, n = a.data.shape[0], held[-2]
-    with on(stream, a.data, a.scales, b.data, b.scales, offsets):
-        out = torch.empty((rows, n), dtype=out_dtype, device=a.data.device)
-        need = fn("zc_fp8_matmul_workspace")(rows, groups, n, k)
-        scratch = torch.empty(need, dtype=torch.uint8, device=a.data.device) if need else None
-        call("zc_fp8_matmul", a.data.data_ptr(), a.scales.data_ptr(), FORMATS[a.fmt], rows, b.data.data_ptr(),
-             b.scales.data_ptr(), FORMATS[b.fmt], groups, n, k, at, out.data_ptr(), n, t,
-             None if scratch is None else scratch.data_ptr(), current(device))
+    return on(stream, (a.data, a.scales, b.data, b.scales, offsets), _matmul, a, b, groups, at, out_dtype, t, device)
+
+
+def _matmul(a, b, groups, at, out_dtype, t, device):
+    a_data, b_data, k = a.data, b.data, a.cols
+    rows, n = a_data.shape[0], b_data.shape[-2]
+    out = torch.empty((rows, n), dtype=out_dtype, device=a_data.device)
+    need = fn("zc_fp8_matmul_workspace")(rows, groups, n, k)
+    scratch = torch.empty(need, dtype=torch.uint8, device=a_data.device) if need else None
+    call("zc_fp8_matmul", a_data.data_ptr(), a.scales.data_ptr(), FORMATS[a.fmt], rows, b_data.data_ptr(),
+         b.scales.data_ptr(), FORMATS[b.fmt], groups, n, k, at, out.data_ptr(), n, t,
+         None if scratch is None else scratch.data_ptr(), current(device))
     return out
 
 
@@ -208,9 +216,13 @@ def weight_grad(dy: Matrix, x: Matrix, out_dtype=torch.bfloat16, stream=None) ->
     check(dy.offsets is not None and x.offsets is not None, "dy and x must come from quantize_columns")
     check(dy.cols == x.cols and dy.offsets.shape == x.offsets.shape, "dy and x must have the same groups")
     groups, at = _offsets(x.offsets, device)
-    with on(stream, dy.data, dy.scales, x.data, x.scales, x.offsets):
-        out = torch.empty((groups, dy.rows, x.rows), dtype=out_dtype, device=x.data.device)
-        call("zc_fp8_weight_grad", dy.data.data_ptr(), dy.scales.data_ptr(), FORMATS[dy.fmt], x.data.data_ptr(),
-             x.scales.data_ptr(), FORMATS[x.fmt], x.cols // BLOCK, groups, dy.rows, x.rows, at, out.data_ptr(), t,
-             current(device))
+    return on(stream, (dy.data, dy.scales, x.data, x.scales, x.offsets), _weight_grad, dy, x, groups, at, out_dtype, t,
+              device)
+
+
+def _weight_grad(dy, x, groups, at, out_dtype, t, device):
+    out = torch.empty((groups, dy.rows, x.rows), dtype=out_dtype, device=x.data.device)
+    call("zc_fp8_weight_grad", dy.data.data_ptr(), dy.scales.data_ptr(), FORMATS[dy.fmt], x.data.data_ptr(),
+         x.scales.data_ptr(), FORMATS[x.fmt], x.cols // BLOCK, groups, dy.rows, x.rows, at, out.data_ptr(), t,
+         current(device))
     return out

@@ -69,86 +69,96 @@ def _plan(plan):
 
 def _rows(name, t, device, rows, dtypes=_ROW_TYPES, hidden=None):
     on_device(name, t, device, dtypes, 2)
-    if t.shape[0] != rows or t.shape[1] < 1 or (hidden is not None and t.shape[1] != hidden):
+    n, h = t.shape
+    if n != rows or h < 1 or (hidden is not None and h != hidden):
         raise ValueError(f"{name} must be [{rows}, {'hidden' if hidden is None else hidden}], got {tuple(t.shape)}")
+    return h
 
 
 def _weights(weights, device, plan):
     on_device("weights", weights, device, _FLOAT32, 2)
-    if weights.shape != plan.position.shape:
-        raise ValueError(f"weights must have the shape {tuple(plan.position.shape)}, got {tuple(weights.shape)}")
+    if weights.shape != plan[0].shape:
+        raise ValueError(f"weights must have the shape {tuple(plan[0].shape)}, got {tuple(weights.shape)}")
 
 
 def sort(experts_of, num_experts: int, stream=None) -> Plan:
     """The plan of a routing: the place of each slot in the order by expert, ties in slot order."""
     device = _ids(experts_of, num_experts)
-    with on(stream, experts_of):
-        ids = experts_of.contiguous()
-        plan, scratch, _keep = _new_plan(ids, num_experts)
-        call("zc_moe_sort", ids.data_ptr(), ids.element_size(), ids.shape[0], ids.shape[1], num_experts,
-             plan.position.data_ptr(), plan.offsets.data_ptr(), scratch, current(device))
+    return on(stream, (experts_of,), _sort, experts_of, num_experts, device)
+
+
+def _sort(ids, num_experts, device):
+    ids = ids.contiguous()
+    tokens, k = ids.shape
+    plan, scratch, _keep = _new_plan(ids, num_experts)
+    call("zc_moe_sort", ids.data_ptr(), ids.element_size(), tokens, k, num_experts, plan[0].data_ptr(),
+         plan[1].data_ptr(), scratch, current(device))
     return plan
 
 
 def dispatch(x, experts_of, num_experts: int, stream=None) -> tuple[torch.Tensor, Plan]:
     """x [tokens, hidden] as rows [tokens * k, hidden] sorted by expert, and the plan."""
     device = _ids(experts_of, num_experts)
-    tokens, k = experts_of.shape
-    _rows("x", x, device, tokens)
-    hidden = x.shape[1]
-    with on(stream, experts_of, x):
-        ids = experts_of.contiguous()
-        x, pitch = rows_of(x)
-        plan, scratch, _keep = _new_plan(ids, num_experts)
-        rows = x.new_empty((tokens * k, hidden))
-        call("zc_moe_dispatch", x.data_ptr(), pitch, TYPES[x.dtype], ids.data_ptr(), ids.element_size(), tokens, k,
-             num_experts, hidden, rows.data_ptr(), hidden, plan.position.data_ptr(), plan.offsets.data_ptr(),
-             scratch, current(device))
+    hidden = _rows("x", x, device, experts_of.shape[0])
+    return on(stream, (experts_of, x), _dispatch, x, experts_of, num_experts, hidden, device)
+
+
+def _dispatch(x, ids, num_experts, hidden, device):
+    ids = ids.contiguous()
+    tokens, k = ids.shape
+    x, pitch = rows_of(x)
+    plan, scratch, _keep = _new_plan(ids, num_experts)
+    rows = torch.empty((tokens * k, hidden), dtype=x.dtype, device=x.device)
+    call("zc_moe_dispatch", x.data_ptr(), pitch, TYPES[x.dtype], ids.data_ptr(), ids.element_size(), tokens, k,
+         num_experts, hidden, rows.data_ptr(), hidden, plan[0].data_ptr(), plan[1].data_ptr(), scratch,
+         current(device))
     return rows, plan
 
 
-def _combine(rows, weights, plan, stream):
-    device, tokens, k, experts = _plan(plan)
-    _rows("rows", rows, device, tokens * k)
+def _combine(rows, weights, plan, shape):
+    device, tokens, k, experts, hidden = shape
+    rows, pitch = rows_of(rows)
     if weights is not None:
-        _weights(weights, device, plan)
-    hidden = rows.shape[1]
-    with on(stream, rows, weights, *plan):
-        rows, pitch = rows_of(rows)
-        weights = None if weights is None else weights.contiguous()
-        out = rows.new_empty((tokens, hidden))
-        call("zc_moe_combine", rows.data_ptr(), pitch, TYPES[rows.dtype], None if weights is None else weights.data_ptr(),
-             plan.position.data_ptr(), plan.offsets.data_ptr(), tokens, k, experts, hidden, out.data_ptr(), hidden,
-             current(device))
+        weights = weights.contiguous()
+    out = torch.empty((tokens, hidden), dtype=rows.dtype, device=rows.device)
+    call("zc_moe_combine", rows.data_ptr(), pitch, TYPES[rows.dtype], None if weights is None else weights.data_ptr(),
+         plan[0].data_ptr(), plan[1].data_ptr(), tokens, k, experts, hidden, out.data_ptr(), hidden, current(device))
     return out
 
 
 def dispatch_grad(d_rows, plan: Plan, stream=None) -> torch.Tensor:
     """The gradient of dispatch with respect to x: each token's sum of its rows' gradients."""
-    return _combine(d_rows, None, plan, stream)
+    device, tokens, k, experts = _plan(plan)
+    hidden = _rows("d_rows", d_rows, device, tokens * k)
+    return on(stream, (d_rows, *plan), _combine, d_rows, None, plan, (device, tokens, k, experts, hidden))
 
 
 def combine(rows, weights, plan: Plan, stream=None) -> torch.Tensor:
     """Each token's rows [tokens * k, hidden] brought back and added with weights [tokens, k] (float32)."""
-    if weights is None:
-        raise TypeError("weights must be a CUDA tensor")
-    return _combine(rows, weights, plan, stream)
+    device, tokens, k, experts = _plan(plan)
+    hidden = _rows("rows", rows, device, tokens * k)
+    _weights(weights, device, plan)
+    return on(stream, (rows, weights, *plan), _combine, rows, weights, plan, (device, tokens, k, experts, hidden))
 
 
 def combine_grad(d_out, rows, weights, plan: Plan, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The gradients of combine with respect to rows and weights."""
     device, tokens, k, experts = _plan(plan)
     _weights(weights, device, plan)
-    _rows("rows", rows, device, tokens * k)
-    hidden = rows.shape[1]
+    hidden = _rows("rows", rows, device, tokens * k)
     _rows("d_out", d_out, device, tokens, (rows.dtype,), hidden)
-    with on(stream, rows, d_out, weights, *plan):
-        rows, pitch = rows_of(rows)
-        d_out, d_pitch = rows_of(d_out)
-        weights = weights.contiguous()
-        d_rows = rows.new_empty((tokens * k, hidden))
-        d_weights = torch.empty_like(weights)
-        call("zc_moe_combine_grad", d_out.data_ptr(), d_pitch, rows.data_ptr(), pitch, TYPES[rows.dtype],
-             weights.data_ptr(), plan.position.data_ptr(), plan.offsets.data_ptr(), tokens, k, experts, hidden,
-             d_rows.data_ptr(), hidden, d_weights.data_ptr(), current(device))
+    return on(stream, (d_out, rows, weights, *plan), _combine_grad, d_out, rows, weights, plan,
+              (device, tokens, k, experts, hidden))
+
+
+def _combine_grad(d_out, rows, weights, plan, shape):
+    device, tokens, k, experts, hidden = shape
+    rows, pitch = rows_of(rows)
+    d_out, d_pitch = rows_of(d_out)
+    weights = weights.contiguous()
+    d_rows = torch.empty((tokens * k, hidden), dtype=rows.dtype, device=rows.device)
+    d_weights = torch.empty_like(weights)
+    call("zc_moe_combine_grad", d_out.data_ptr(), d_pitch, rows.data_ptr(), pitch, TYPES[rows.dtype],
+         weights.data_ptr(), plan[0].data_ptr(), plan[1].data_ptr(), tokens, k, experts, hidden, d_rows.data_ptr(),
+         hidden, d_weights.data_ptr(), current(device))
     return d_rows, d_weights
