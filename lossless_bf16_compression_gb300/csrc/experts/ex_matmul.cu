@@ -91,8 +91,10 @@ struct Walk {
   unsigned t;
   int g = 0;
   const unsigned p_tiles;
-  unsigned end = 0;             // of this CTA's blocks
+  unsigned begin = 0, end = 0;  // this CTA's blocks
+  int phase = 0;
   unsigned whole = 0;           // tiles that have blocks
+  unsigned zeros = 0;           // tiles without blocks walked so far
   unsigned ctas = 1;            // that share them: each gets a word of scales, four blocks, at least
   unsigned each = 0, more = 0;  // blocks of a CTA; the first `more` get another one
   __device__ Walk(const TileParams& p_, const Shared& s_)
@@ -103,7 +105,7 @@ struct Walk {
       ctas = min(gridDim.x, max(all / 4, 1u));
       each = all / ctas;
       more = all - each * ctas;
-      t = begin_of(blockIdx.x);
+      t = begin = begin_of(blockIdx.x);
       end = begin_of(blockIdx.x + 1);
     }
   }
@@ -120,18 +122,30 @@ struct Walk {
   __device__ bool next(Tile* out) {
     const int last = p.by_blocks ? p.groups : p.groups + 1;
     if (p.parts) {
-      if (t >= end) {  // then the tiles without blocks, one after the other
-        const unsigned zero = whole + blockIdx.x + (t - end) * gridDim.x;
-        if (zero >= s.tiles[last]) return false;
-        ++t;
-        locate(zero, out);
-        return true;
+      // The parts of tiles first -- of the one that the CTA ends inside, then of the one that it
+      // begins inside -- so that they are joined while the whole tiles are under way.
+      const unsigned blocks = p.blocks;
+      if (phase == 0) {
+        phase = 1;
+        const unsigned from = end - end % blocks;
+        if (from != end && from >= begin) return part(from, end, out);
       }
-      const unsigned tile = t / p.blocks;
-      locate(tile, out);
-      out->b0 = t - tile * p.blocks;
-      out->b1 = min(static_cast<unsigned>(p.blocks), out->b0 + (end - t));
-      t += out->b1 - out->b0;
+      if (phase == 1) {
+        phase = 2;
+        if (begin % blocks && begin < end) {
+          t = min(end, begin - begin % blocks + blocks);
+          return part(begin, t, out);
+        }
+      }
+      if (t + blocks <= end) {
+        t += blocks;
+        return part(t - blocks, t, out);
+      }
+      // then the tiles without blocks, one after the other
+      const unsigned zero = whole + blockIdx.x + zeros * gridDim.x;
+      if (zero >= s.tiles[last]) return false;
+      ++zeros;
+      locate(zero, out);
       return true;
     }
     if (t >= s.tiles[last]) return false;
@@ -140,7 +154,16 @@ struct Walk {
     return true;
   }
 
+  __device__ bool part(unsigned from, unsigned to, Tile* out) {
+    const unsigned tile = from / p.blocks;
+    locate(tile, out);
+    out->b0 = from - tile * p.blocks;
+    out->b1 = out->b0 + (to - from);
+    return true;
+  }
+
   __device__ void locate(unsigned tile, Tile* out) {
+    if (s.tiles[g] > tile) g = 0;
     while (s.tiles[g + 1] <= tile) ++g;
     // Within a group: bands of kBand rows of P, and in a band all of P's tiles for each of Q's, so
     // that the tiles in flight at a time cover about as many rows of P as of Q.  Shared-out tiles

@@ -133,7 +133,7 @@ __device__ __forceinline__ uint2 round_column(const Raw8<T> (&r)[8], int j, floa
 // A warp takes four blocks (one scale word) of each of R rows: lane l holds values 8l .. 8l + 7
 // of the first two blocks and of the last two, so 16 lanes share a block.  CTA: 8 R rows, whose
 // scale words lie next to each other.  With R = 4 a lane has 128 bytes of 16-bit input in flight.
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 4;  // (32768 x 7168: 102 us; 8 warps 108, 16 warps 117)
 template <typename T, bool Vec, int Fmt, int R>
 __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __restrict__ x, size_t pitch, size_t rows,
                                                                   int cols, unsigned words,
