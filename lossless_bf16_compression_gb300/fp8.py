@@ -56,11 +56,12 @@ class Matrix:
     def values(self) -> torch.Tensor:
         """The 8-bit values without their scales (a view)."""
         v = self.data.view(_FLOAT8[self.fmt])
-        return v if self.cols == v.shape[-1] else v[..., : self.cols]
+        return v if self.cols == v.shape[-1] else v.narrow(-1, 0, self.cols)
 
     def scale_values(self) -> torch.Tensor:
         """The scales as float32 powers of two, in their own layout."""
-        return self.scales.view(torch.float8_e8m0fnu).float()
+        out = torch.empty(self.scales.shape, dtype=torch.float32, device=self.scales.device)
+        return out.copy_(self.scales.view(torch.float8_e8m0fnu))
 
 
 _ROW_TYPES = tuple(TYPES)

@@ -216,6 +216,43 @@ def test_matmul_many_row_tiles_and_wide_scales():
     check_product(doubles(got), dequantize(a), dequantize(b), k, torch.float32)
 
 
+@pytest.mark.parametrize("counts,n,k", [
+    ((2048,), 2432, 300),             # 152 tiles of 128 x 256: one wave of single CTAs, two of pairs
+    ((100,) * 38, 500, 260),          # 152 tiles of 128 x 128
+    ((64,) * 3 + (0, 200), 2100, 520),  # blocks shared out, groups above and below the average
+    ((1,) * 300, 130, 140),           # more groups than CTAs
+    ((256, 255, 257, 1, 511), 256, 128),  # tile ends on, before and after group ends, one block
+    ((500,) * 6, 2050, 640),          # several bands of tiles, rows of out not whole 32-bit words apart
+])
+def test_matmul_cuts(counts, n, k):
+    """Every way a product is cut into tiles, with groups that end inside them."""
+    offsets = starts(counts)
+    e = len(counts)
+    x = activations((int(offsets[-1]), k), n)
+    w = (torch.randn((e, n, k), generator=torch.Generator().manual_seed(n)) * 0.02).cuda()
+    a, (b, _) = fp8.quantize(x), fp8.quantize_weight(w, transposed=False)
+    got = doubles(fp8.matmul(a, b, torch.from_numpy(offsets).cuda(), torch.bfloat16))
+    av, bv = dequantize(a), dequantize(b)
+    for g in range(e):
+        s = slice(offsets[g], offsets[g + 1])
+        check_product(got[s], av[s], bv[g], k, torch.bfloat16)
+
+
+def test_matmul_into_unaligned_rows():
+    """Odd row widths: neighbouring rows of out start on and off word boundaries."""
+    for n in (1, 31, 33, 127, 129, 255):
+        a, b = fp8.quantize(activations((290, 200), n)), fp8.quantize(activations((n, 200), 1))
+        check_product(doubles(fp8.matmul(a, b)), dequantize(a), dequantize(b), 200, torch.bfloat16)
+
+
+def test_matmul_long_sums():
+    """Many blocks in one sum, and many CTAs' parts in one tile."""
+    for rows in (1, 40, 200):
+        a, b = fp8.quantize(activations((rows, 40000), 1)), fp8.quantize(activations((70, 40000), 2))
+        got = fp8.matmul(a, b, out_dtype=torch.float32)
+        check_product(doubles(got), dequantize(a), dequantize(b), 40000, torch.float32)
+
+
 @pytest.mark.parametrize("rows", [3, 400])
 def test_matmul_keeps_infinity_and_nan_in_their_rows(rows):
     x = activations((rows, 384), 6)

@@ -172,6 +172,19 @@ def test_combine_grad(tokens, k, experts, hidden, dtype):
     check_sum(doubles(d_w), prod.sum(2), np.abs(prod).sum(2), torch.float32, hidden + 1)
 
 
+@pytest.mark.parametrize("tokens,k,hidden", [(2100, 1, 24), (2101, 2, 36), (2103, 3, 7), (2049, 4, 40), (2050, 7, 10)])
+def test_many_tokens_of_few_slots(tokens, k, hidden):
+    """Token counts at which a thread takes several tokens, not a multiple of them."""
+    ids = routing(tokens, k, 11, tokens)
+    position, offsets = sort(ids, 11)
+    plan = moe.Plan(torch.from_numpy(position).cuda(), torch.from_numpy(offsets).cuda())
+    rows, w = values((tokens * k, hidden), torch.bfloat16, 1), values((tokens, k), torch.float32, 2)
+    r = np.where((position < offsets[-1])[..., None], doubles(rows)[position], 0.0)
+    check_sum(doubles(moe.dispatch_grad(rows, plan)), r.sum(1), np.abs(r).sum(1), torch.bfloat16, k)
+    r = r * doubles(w)[..., None]
+    check_sum(doubles(moe.combine(rows, w, plan)), r.sum(1), np.abs(r).sum(1), torch.bfloat16, k)
+
+
 def test_gradients_against_differences():
     """combine and dispatch are linear in rows and in weights: central differences of the loss <out, g>, in fp32.
 
