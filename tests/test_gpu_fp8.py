@@ -253,6 +253,44 @@ def test_matmul_long_sums():
         check_product(doubles(got), dequantize(a), dequantize(b), 40000, torch.float32)
 
 
+@pytest.mark.parametrize("rows", [5, 300])
+def test_matmul_extreme_scales(rows):
+    """Scale bytes from 0 (2^-127) up, met by the other side's inverse so that the products are ordinary numbers."""
+    g = torch.Generator().manual_seed(1)
+    k, n = 640, 150
+    e = torch.tensor([-127.0, -120.0, -60.0, 60.0, 110.0])
+    x = torch.randint(-28, 29, (rows, k), generator=g) * torch.exp2(e + 4).repeat_interleave(128)
+    w = torch.randint(-28, 29, (n, k), generator=g) * torch.exp2(-e - 10).repeat_interleave(128)
+    x[:, ::128], w[:, ::128] = 28 * torch.exp2(e + 4), 28 * torch.exp2(-e - 10)  # (each block has its largest)
+    a, b = fp8.quantize(x.cuda()), fp8.quantize(w.cuda())
+    assert a.scales.min().item() == 0 and a.scales.max().item() == 127 + 110
+    got = fp8.matmul(a, b, out_dtype=torch.float32)
+    check_product(doubles(got), dequantize(a), dequantize(b), k, torch.float32)
+
+
+def test_sizes_past_32_bit_offsets():
+    """An output of more than 2^31 values, and 8-bit rows of more than 2^31 bytes."""
+    rows, n = 50000, 45000
+    a, b = fp8.quantize(activations((rows, 128), 1)), fp8.quantize(activations((n, 128), 2))
+    got = fp8.matmul(a, b)
+    assert got.numel() > 1 << 31
+    av, bv = dequantize(a), dequantize(b)
+    for r in (0, 1, rows // 2, rows - 1):
+        check_product(doubles(got[r:r + 1]), av[r:r + 1], bv, 128, torch.bfloat16)
+    del got
+    x = torch.zeros((300001, 7168), dtype=torch.bfloat16, device="cuda")
+    x[-1] = activations((7168,), 3, torch.bfloat16)
+    q = fp8.quantize(x)
+    last = fp8.quantize(x[-1:])
+    assert q.data.numel() > 1 << 31 and torch.equal(q.data[-1], last.data[0])
+    assert torch.equal(q.scales[:, -1], last.scales[:, 0]) and not q.data[:-1].any().item()
+    c = fp8.quantize_columns(x)
+    assert torch.equal(c.offsets, torch.tensor([0, -(-300001 // 128)], dtype=torch.int32, device="cuda"))
+    got = c.values()[:, 300000].float() * torch.exp2(c.scales[300000 // 128 // 4, :, 300000 // 128 % 4].float() - 127)
+    one = fp8.quantize_columns(x[-1:])
+    assert torch.equal(got, one.values()[:, 0].float() * torch.exp2(one.scales[0, :, 0].float() - 127))
+
+
 @pytest.mark.parametrize("rows", [3, 400])
 def test_matmul_keeps_infinity_and_nan_in_their_rows(rows):
     x = activations((rows, 384), 6)
