@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <initializer_list>
+
 #include "zc_common.cuh"
 #include "zc_moe.h"
 
@@ -69,13 +71,75 @@ __device__ __forceinline__ unsigned short load_if<2>(const void* p, bool on) {
   return v;
 }
 
-// The widest vector that every one of these row sets allows: 16 bytes, else 4, else one value.
-inline int vector_bytes(size_t element, size_t row_values, std::initializer_list<const void*> bases,
-                        std::initializer_list<size_t> pitches) {
+// ------------------------------------------------------------------ rows as 16-byte vectors
+//
+// Aligned: every row starts on a 16-byte boundary.  Otherwise 16 bytes of a row are put together from
+// the two aligned vectors that hold them (the second is the neighbouring lane's first one, so it
+// comes from the L1): loads stay as wide as on aligned rows.  An aligned vector is only touched
+// when it holds a byte of the row.
+
+// Bytes s .. s + 15 of a and b, 0 <= s < 16, a multiple of two.  (s is the same for a row's lanes: a
+// branch on the word costs less than selecting among them.)
+__device__ __forceinline__ uint4 shift_words(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4,
+                                             unsigned s) {
+  const unsigned bits = (s & 2) * 8;
+  return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits), __funnelshift_r(w2, w3, bits),
+                    __funnelshift_r(w3, w4, bits));
+}
+__device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, unsigned s) {
+  if (s < 8) return s < 4 ? shift_words(a.x, a.y, a.z, a.w, b.x, s) : shift_words(a.y, a.z, a.w, b.x, b.y, s);
+  return s < 12 ? shift_words(a.z, a.w, b.x, b.y, b.z, s) : shift_words(a.w, b.x, b.y, b.z, b.w, s);
+}
+
+__device__ __forceinline__ unsigned low4(const void* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u; }
+
+// What holds bytes from .. from + 15 of a row of `bytes` bytes (from may lie outside it).
+struct Loaded {
+  uint4 a, b;
+};
+template <bool Aligned>
+__device__ __forceinline__ Loaded fetch16(const uint8_t* row, int from, int bytes, bool on) {
+  Loaded l;
+  if (Aligned) {
+    l.a = load_if<16>(row + from, on && from < bytes);
+  } else {
+    const unsigned s = low4(row + from);
+    const int at = from - static_cast<int>(s);  // of the first vector, from the row's start
+    l.a = load_if<16>(row + at, on && at > -16 && at < bytes);
+    l.b = load_if<16>(row + at + 16, on && s && at > -32 && at + 16 < bytes);
+  }
+  return l;
+}
+template <bool Aligned>
+__device__ __forceinline__ uint4 settle(const Loaded& l, const uint8_t* row, int from) {
+  return Aligned ? l.a : shift_bytes(l.a, l.b, low4(row + from));
+}
+
+// Stores bytes from .. from + 15 of a row, an aligned vector, as far as they lie in it; E: bytes of a value.
+template <bool Aligned, int E>
+__device__ __forceinline__ void put16(uint8_t* row, int from, int bytes, const uint4& v) {
+  if (from >= 0 && from + 16 <= bytes) {
+    *reinterpret_cast<uint4*>(row + from) = v;
+  } else if (!Aligned) {
+    using V = typename Bytes<E>::type;
+    union {
+      uint4 q;
+      V v[16 / E];
+    } u;
+    u.q = v;
+#pragma unroll
+    for (int i = 0; i < 16 / E; ++i)
+      if (from + i * E >= 0 && from + i * E < bytes) *reinterpret_cast<V*>(row + from + i * E) = u.v[i];
+  }
+}
+
+// Whether all of these rows of `row_values` values are whole aligned vectors.
+inline bool whole_vectors(size_t element, size_t row_values, std::initializer_list<const void*> bases,
+                          std::initializer_list<size_t> pitches) {
   uintptr_t all = row_values * element;
   for (const void* b : bases) all |= reinterpret_cast<uintptr_t>(b);
   for (size_t p : pitches) all |= p * element;
-  return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+  return all % 16 == 0;
 }
 
 inline size_t type_bytes(int type) { return type == ZC_TYPE_FP32 ? 4 : 2; }

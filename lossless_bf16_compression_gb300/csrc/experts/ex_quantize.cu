@@ -9,8 +9,7 @@ namespace zc {
 namespace ex {
 namespace {
 
-// Eight consecutive values of a row as they lie in memory, zeros past `left` values (none where left
-// <= 0).  Vec: the address allows 16-byte loads.
+// Eight consecutive values of a row as they lie in memory.
 template <typename T>
 union Raw8 {
   uint4 q[sizeof(T) / 2];
@@ -19,24 +18,34 @@ union Raw8 {
   T v[8];
   __device__ Raw8() {}
 };
+// The loads of eight values, `left` of them in the row (none where left <= 0), and the values, zeros
+// past them.  Vec: rows start on 16-byte boundaries; otherwise the values lie in one aligned vector
+// more.  All of a thread's loads are issued before the first value is made.
 template <typename T, bool Vec>
-__device__ __forceinline__ void load8(const T* at, int left, Raw8<T>& r) {
-  if (Vec) {
+struct Fetch8 {
+  static constexpr int kVectors = sizeof(T) / 2 + (Vec ? 0 : 1);
+  uint4 q[kVectors];
+  __device__ __forceinline__ void load(const T* at, int left) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(at);
+    const unsigned s = Vec ? 0 : low4(p);
+    const int bytes = min(left, 8) * static_cast<int>(sizeof(T)) + static_cast<int>(s);
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-      r.q[i] = load_if<16>(at + i * (16 / sizeof(T)), left >= 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.bits[i] = load_if<sizeof(T)>(at + i, i < left);
+    for (int i = 0; i < kVectors; ++i) q[i] = load_if<16>(p - s + 16 * i, left > 0 && 16 * i < bytes);
   }
-}
-// After all of a thread's vector loads: the values of a row's end that is not a whole vector.
-template <typename T, bool Vec>
-__device__ __forceinline__ void load_end(const T* at, int left, Raw8<T>& r) {
-  if (Vec && left > 0 && left < 8)
+  __device__ __forceinline__ void values(const T* at, int left, Raw8<T>& r) const {
+    if constexpr (Vec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.bits[i] = load_if<sizeof(T)>(at + i, i < left);
-}
+      for (int i = 0; i < kVectors; ++i) r.q[i] = q[i];
+    } else {
+      const unsigned s = low4(at);
+#pragma unroll
+      for (int i = 0; i + 1 < kVectors; ++i) r.q[i] = shift_bytes(q[i], q[i + 1], s);
+    }
+    if (left < 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.bits[i] = i < left ? r.bits[i] : 0;
+  }
+};
 
 // Magnitudes are compared as the type's own bits without the sign, which order like the values;
 // Inf and NaN are the bits from kInf on.  16-bit values go two at a time.
@@ -146,22 +155,13 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
   const size_t r0 = (static_cast<size_t>(blockIdx.x / words) * kRowWarps + threadIdx.x / 32) * R;
   const int blocks = (cols + kBlock - 1) / kBlock, wide = blocks * kBlock;
   const int c0 = static_cast<int>(word) * 4 * kBlock + lane * 8;
-  Raw8<T> raw[R][2];
+  Fetch8<T, Vec> in[R][2];
+  const auto place = [&](int i, int h) { return x + (r0 + i) * pitch + c0 + h * 2 * kBlock; };
+  const auto left = [&](int i, int h) { return r0 + i < rows ? cols - (c0 + h * 2 * kBlock) : 0; };
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 + h * 2 * kBlock;
-      load8<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < rows ? cols - c : 0, raw[i][h]);
-    }
-  if (Vec && cols % 8)
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0 + h * 2 * kBlock;
-        load_end<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < rows ? cols - c : 0, raw[i][h]);
-      }
+    for (int h = 0; h < 2; ++h) in[i][h].load(place(i, h), left(i, h));
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const size_t r = r0 + i;
@@ -169,14 +169,16 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
     int s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      Raw8<T> raw;
+      in[i][h].values(place(i, h), left(i, h), raw);
       uint32_t words[2 * sizeof(T)];
       bool odd;
-      magnitudes<T, 1>(&raw[i][h], words, odd);
+      magnitudes<T, 1>(&raw, words, odd);
       uint32_t m = largest<T>(words);
 #pragma unroll
       for (int d = 8; d; d /= 2) m = max(m, __shfl_xor_sync(~0u, m, d));
       s[h] = block_exponent(Bits<T>::fp32(m), Fmt);
-      const uint2 q = round_row<Fmt>(raw[i][h], inverse_scale(s[h]), odd);
+      const uint2 q = round_row<Fmt>(raw, inverse_scale(s[h]), odd);
       const int c = c0 + h * 2 * kBlock;
       if (c < wide) *reinterpret_cast<uint2*>(values + r * wide + c) = q;
     }
@@ -224,6 +226,16 @@ struct TileShared {
   float inverse[kBlock];
 };
 
+// Eight values of each of eight rows (`rows` of them real), `left` of a row's in it.
+template <typename T, bool Vec>
+__device__ __forceinline__ void load_tile(const T* at, size_t pitch, int rows, int left, Raw8<T> (&raw)[8]) {
+  Fetch8<T, Vec> in[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) in[i].load(at + i * pitch, i < rows ? left : 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) in[i].values(at + i * pitch, i < rows ? left : 0, raw[i]);
+}
+
 // The tile's transpose by way of shared memory: column c's bytes of rows 8 rg .. as one unit.  The
 // places are chosen so that the 16 column groups of a store, and the 8 lanes of a load, hit
 // different banks.
@@ -236,7 +248,7 @@ __device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
 }
 
 template <typename T, bool Vec, int Fmt>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
                                                                int cols, int groups, const int* __restrict__ offsets,
                                                                int capacity, uint8_t* __restrict__ values,
                                                                uint8_t* __restrict__ scales,
@@ -260,13 +272,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_columns_
     }
   }
   __syncthreads();
-  Raw8<T> raw[8];
   const long long r0 = static_cast<long long>(first) + rg * 8;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) load8<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < last ? cols - c : 0, raw[i]);
-  if (Vec && cols % 8)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) load_end<T, Vec>(x + (r0 + i) * pitch + c, r0 + i < last ? cols - c : 0, raw[i]);
+  Raw8<T> raw[8];
+  load_tile<T, Vec>(x + r0 * pitch + c, pitch, static_cast<int>(min(8ll, last - r0)), cols - c, raw);
   constexpr int words = 2 * sizeof(T);  // of eight columns
   uint32_t most[words];
   bool odd;
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_columns_
 
 // One scale for the tile; its rows are written from registers, its transpose through shared memory.
 template <typename T, bool Vec, int Fmt>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_weight_kernel(const T* __restrict__ w, int rows, int cols,
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantize_weight_kernel(const T* __restrict__ w, int rows, int cols,
                                                               uint8_t* __restrict__ values,
                                                               uint8_t* __restrict__ scales,
                                                               uint8_t* __restrict__ values_t,
@@ -317,15 +325,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) quantize_weight_k
   const size_t g = blockIdx.z;
   const int c = bc * kBlock + cg * 8;
   w += g * rows * cols;
-  Raw8<T> raw[8];
   const int r0 = br * kBlock + rg * 8;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    load8<T, Vec>(w + static_cast<size_t>(r0 + i) * cols + c, r0 + i < rows ? cols - c : 0, raw[i]);
-  if (Vec && cols % 8)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      load_end<T, Vec>(w + static_cast<size_t>(r0 + i) * cols + c, r0 + i < rows ? cols - c : 0, raw[i]);
+  Raw8<T> raw[8];
+  load_tile<T, Vec>(w + static_cast<size_t>(r0) * cols + c, cols, min(8, rows - r0), cols - c, raw);
   uint32_t words[2 * sizeof(T)];
   bool odd;
   magnitudes<T, 8>(raw, words, odd);
@@ -401,7 +403,7 @@ cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, 
                     static_cast<unsigned>(words), values, reinterpret_cast<uint32_t*>(scales));
     };
     // four rows a warp once that still gives every SM a few CTAs; one row a warp below
-    return ceil_div(rows, kRowWarps * 4) * words >= 1024 ? go(std::integral_constant<int, 4>{})
+    return ceil_div(rows, kRowWarps * 4) * words >= 2048 ? go(std::integral_constant<int, vec() ? 4 : 2>{})
                                                          : go(std::integral_constant<int, 1>{});
   });
 }

@@ -16,7 +16,6 @@ constexpr int kMaxThreads = 256;
 // Smaller CTAs keep an SM's loads further apart: combine of 16384 x 8 x 7168 with 256 threads 365
 // us, with 128 336 us; of 4999 x 6 x 2050 53 and 41 us.
 constexpr int kCombineThreads = 128;
-constexpr int kBatch = 8;  // slots whose rows a thread has in flight
 
 // A position that may be used as an address; reported otherwise.
 __device__ __forceinline__ bool in_range(int p, size_t slots, int* status) {
@@ -25,44 +24,48 @@ __device__ __forceinline__ bool in_range(int p, size_t slots, int* status) {
   return false;
 }
 
-// Vectors of a row that a thread takes, a row's threads apart.  Rows that only 4-byte (or smaller)
-// vectors divide need more of them in flight.
-constexpr int per_thread(int bytes) { return bytes == 16 ? 1 : 4; }
-
-// How a row's vectors are shared out: to `parts` CTAs of `threads`.
+// How a row's vectors are shared out: to `parts` CTAs of `threads`, one vector a thread.
 struct Cut {
   unsigned parts, threads;
 };
-Cut cut_row(size_t vecs, int bytes, unsigned most_threads) {
-  const unsigned u = per_thread(bytes), most = most_threads * u;
+Cut cut_row(size_t vecs, unsigned most) {
   const unsigned parts = static_cast<unsigned>((vecs + most - 1) / most);
-  const unsigned each = static_cast<unsigned>((vecs + parts * u - 1) / (parts * u));
+  const unsigned each = static_cast<unsigned>((vecs + parts - 1) / parts);
   return {parts, (each + 31) / 32 * 32};
 }
-// This thread's first vector.
-template <int B>
-__device__ __forceinline__ int first_vector(unsigned parts) {
-  return static_cast<int>(blockIdx.x % parts * blockDim.x * per_thread(B) + threadIdx.x);
-}
-// A token's vectors as a thread holds them, and to a slot's row.
-template <int B>
+// Vectors of a row; one more where a row may start inside a vector.
+size_t row_vectors(size_t bytes, bool aligned) { return (bytes + 15) / 16 + (aligned ? 0 : 1); }
+
+// 16 bytes of a token's row, vector c of it, as a thread holds them to store them in rows that start
+// elsewhere: a vector of such a row holds bytes of this vector and of the one before.
+template <bool Aligned, int E>
 struct Held {
-  static constexpr int U = per_thread(B);
-  using V = typename Bytes<B>::type;
-  V v[U];
-  __device__ __forceinline__ void load(const uint8_t* row, int c, int vecs) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = c + u * static_cast<int>(blockDim.x);
-      v[u] = load_if<B>(row + static_cast<size_t>(at) * B, at < vecs);
+  uint4 before, here;
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int bytes) {
+    if (Aligned) {
+      here = load_if<16>(row + 16 * c, 16 * c < bytes);
+      return;
     }
+    const unsigned s = low4(row);
+    uint4 v[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int at = 16 * (c + i - 1) - static_cast<int>(s);
+      v[i] = load_if<16>(row + at, at > -16 && at < bytes && (i < 2 || s));
+    }
+    before = shift_bytes(v[0], v[1], s);
+    here = shift_bytes(v[1], v[2], s);
   }
-  __device__ __forceinline__ void store(uint8_t* row, int c, int vecs, bool zeros) const {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = c + u * static_cast<int>(blockDim.x);
-      if (at < vecs) reinterpret_cast<V*>(row)[at] = zeros ? V{} : v[u];
-    }
+  // The bytes that lie in vector c of a row at `row`, and where they start in the row.
+  __device__ __forceinline__ uint4 for_row(const uint8_t* row, int c, int* from) const {
+    const unsigned s = Aligned ? 0 : low4(row);
+    *from = 16 * c - static_cast<int>(s);
+    return s ? shift_bytes(before, here, 16 - s) : here;
+  }
+  __device__ __forceinline__ void store(uint8_t* row, int c, int bytes, bool zeros) const {
+    int from;
+    const uint4 v = for_row(row, c, &from);
+    put16<Aligned, E>(row, from, bytes, zeros ? make_uint4(0, 0, 0, 0) : v);
   }
 };
 
@@ -70,23 +73,23 @@ struct Held {
 // so what bounds them is how fast CTAs start (16384 x 2 x 1024: 28 -> 22 us; the other kernels
 // lose more by giving up uniform registers for a token's positions and addresses, the combine
 // gradient at that size 53 -> 84 us).
-template <int B>
+template <bool Aligned, int E>
 __global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __restrict__ x, size_t x_pitch,
-                                                               uint8_t* __restrict__ rows, size_t rows_pitch, int vecs,
+                                                               uint8_t* __restrict__ rows, size_t rows_pitch, int bytes,
                                                                unsigned parts, size_t tokens, int k,
                                                                const int* __restrict__ position,
                                                                const int* __restrict__ total, int* status) {
   let_next_start();
   const size_t t = static_cast<size_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y, slots = tokens * k;
-  const int c = first_vector<B>(parts);
+  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
   if (t >= tokens) return;
-  Held<B> held;
-  held.load(x + t * x_pitch, c, vecs);  // x does not come from the sort
+  Held<Aligned, E> held;
+  held.load(x + t * x_pitch, c, bytes);  // x does not come from the sort
   wait_for_previous();
   const int kept = *total;
   for (int j = 0; j < k; ++j) {
     const int p = position[t * k + j];
-    if (in_range(p, slots, status)) held.store(rows + p * rows_pitch, c, vecs, p >= kept);
+    if (in_range(p, slots, status)) held.store(rows + p * rows_pitch, c, bytes, p >= kept);
   }
 }
 
@@ -95,10 +98,10 @@ __global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __
 // for another.  At 64 tokens x 8 that is 16 comparisons a thread.
 constexpr size_t kSmallSlots = 1024;
 
-template <typename Id, int B>
+template <typename Id, bool Aligned, int E>
 __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
     const Id* __restrict__ ids, int slots, int experts, const uint8_t* __restrict__ x, size_t x_pitch,
-    uint8_t* __restrict__ rows, size_t rows_pitch, int vecs, unsigned parts, int k, int* __restrict__ position,
+    uint8_t* __restrict__ rows, size_t rows_pitch, int bytes, unsigned parts, int k, int* __restrict__ position,
     int* __restrict__ offsets) {
   __shared__ short keys[kSmallSlots];
   __shared__ int place[ZC_MOE_MAX_K];
@@ -107,9 +110,9 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   let_next_start();
   wait_for_previous();
   const int t = static_cast<int>(blockIdx.x / parts), part = static_cast<int>(blockIdx.x % parts);
-  const int c = first_vector<B>(parts), lane = threadIdx.x % 32;
-  Held<B> held;
-  held.load(x + t * x_pitch, c, vecs);
+  const int c = part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x), lane = threadIdx.x % 32;
+  Held<Aligned, E> held;
+  held.load(x + t * x_pitch, c, bytes);
   const bool starts = blockIdx.x == 0;  // this CTA writes the offsets as well
   if (threadIdx.x < ZC_MOE_MAX_K) place[threadIdx.x] = 0;
   if (threadIdx.x == 0) kept = 0;
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   if (part == 0 && static_cast<int>(threadIdx.x) < k) position[t * k + threadIdx.x] = place[threadIdx.x];
   for (int j = 0; j < k; ++j) {
     const int p = place[j];
-    held.store(rows + p * rows_pitch, c, vecs, p >= kept);
+    held.store(rows + p * rows_pitch, c, bytes, p >= kept);
   }
   if (starts && threadIdx.x < 32) {
     int before = 0;
@@ -160,25 +163,30 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
 }
 
 // out[t] = sum over j of weights[t, j] rows[position[t, j]].  A thread takes Tokens tokens that follow
-// one another, with kBatch / Tokens of each one's slots at a time: eight rows in flight however few
-// slots a token has.
-template <typename T, int B, int Tokens, bool Weighted>
+// one another, with a share of each one's slots at a time: as many rows in flight however few slots a
+// token has.
+template <typename T, bool Aligned, int Tokens, bool Weighted>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
-                                                              const float* __restrict__ weights,
-                                                              uint8_t* __restrict__ out, size_t out_pitch, int vecs,
-                                                              unsigned parts, size_t tokens, int k,
-                                                              const int* __restrict__ position,
-                                                              const int* __restrict__ total, int* status) {
-  constexpr int N = B / sizeof(T), U = per_thread(B), S = kBatch / Tokens;
+                                                                  const float* __restrict__ weights,
+                                                                  uint8_t* __restrict__ out, size_t out_pitch,
+                                                                  int bytes, unsigned parts, size_t tokens, int k,
+                                                                  const int* __restrict__ position,
+                                                                  const int* __restrict__ total, int* status) {
+  constexpr int N = 16 / sizeof(T), kBatch = Aligned ? 8 : 4, S = kBatch / Tokens;
   let_next_start();
   wait_for_previous();
   const size_t t0 = static_cast<size_t>(blockIdx.x / parts) * Tokens, slots = tokens * k;
-  const int c = first_vector<B>(parts);
-  if (c >= vecs || t0 >= tokens) return;
+  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
+  if (t0 >= tokens || 16 * c >= bytes + (Aligned ? 0 : 16)) return;
   const int kept = *total;
-  float acc[Tokens][U][N] = {};
+  // vector c of each token's row of out: its first byte in the row
+  int from[Tokens];
+#pragma unroll
+  for (int i = 0; i < Tokens; ++i)
+    from[i] = 16 * c - (Aligned ? 0 : static_cast<int>(low4(out + (t0 + i) * out_pitch)));
+  float acc[Tokens][N] = {};
   for (int j0 = 0; j0 < k; j0 += S) {
-    Pack<T, B> v[kBatch][U];
+    Loaded l[kBatch];
     float w[kBatch];
     int at[kBatch];
     bool here[kBatch];
@@ -191,53 +199,46 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t*
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       here[i] = j0 + i % S < k && t0 + i / S < tokens && in_range(at[i], slots, status) && at[i] < kept;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int cu = c + u * static_cast<int>(blockDim.x);
-        v[i][u].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(cu) * B, here[i] && cu < vecs);
-      }
+      l[i] = fetch16<Aligned>(rows + at[i] * rows_pitch, from[i / S], bytes, here[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < kBatch; ++i) {
+      if (!here[i]) continue;
+      Pack<T, 16> v;
+      v.raw = settle<Aligned>(l[i], rows + at[i] * rows_pitch, from[i / S]);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          acc[i / S][u][e] = here[i] ? fmaf(w[i], to_float(v[i][u].v[e]), acc[i / S][u][e]) : acc[i / S][u][e];
+      for (int e = 0; e < N; ++e) acc[i / S][e] = fmaf(w[i], to_float(v.v[e]), acc[i / S][e]);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < Tokens; ++i)
+  for (int i = 0; i < Tokens; ++i) {
+    Pack<T, 16> o;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int cu = c + u * static_cast<int>(blockDim.x);
-      Pack<T, B> o;
-#pragma unroll
-      for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[i][u][e]);
-      if (cu < vecs && t0 + i < tokens)
-        reinterpret_cast<typename Bytes<B>::type*>(out + (t0 + i) * out_pitch)[cu] = o.raw;
-    }
+    for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[i][e]);
+    if (t0 + i < tokens) put16<Aligned, sizeof(T)>(out + (t0 + i) * out_pitch, from[i], bytes, o.raw);
+  }
 }
 
 // d_rows[position[t, j]] = weights[t, j] d_out[t], d_weights[t, j] = <d_out[t], rows[...]>.  One
 // CTA a token: each thread sums its vectors' products, then lanes, then warps, in a fixed order.
-template <typename T, int B>
+template <typename T, bool Aligned, int Batch>
 __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
     const uint8_t* __restrict__ d_out, size_t d_out_pitch, const uint8_t* __restrict__ rows, size_t rows_pitch,
     const float* __restrict__ weights, uint8_t* __restrict__ d_rows, size_t d_rows_pitch, float* __restrict__ d_weights,
-    int vecs, size_t tokens, int k, const int* __restrict__ position, const int* __restrict__ total, int* status) {
-  constexpr int N = B / sizeof(T);
-  using V = typename Bytes<B>::type;
-  __shared__ float sums[kBatch][kMaxThreads / 32];
+    int bytes, size_t tokens, int k, const int* __restrict__ position, const int* __restrict__ total, int* status) {
+  constexpr int N = 16 / sizeof(T);
+  __shared__ float sums[Batch][kMaxThreads / 32];
   let_next_start();
   wait_for_previous();
   const size_t t = blockIdx.x, slots = tokens * k;
+  const int vecs = (bytes + 15) / 16 + (Aligned ? 0 : 1);
   const int kept = *total, warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int j0 = 0; j0 < k; j0 += kBatch) {
-    int at[kBatch];
-    float w[kBatch], dot[kBatch];
-    bool ok[kBatch], here[kBatch];
+  for (int j0 = 0; j0 < k; j0 += Batch) {
+    int at[Batch];
+    float w[Batch], dot[Batch];
+    bool ok[Batch], here[Batch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < Batch; ++i) {
       const size_t s = t * k + j0 + i;
       at[i] = j0 + i < k ? position[s] : 0;
       ok[i] = j0 + i < k && in_range(at[i], slots, status);
@@ -246,33 +247,41 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
       dot[i] = 0.f;
     }
     for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-      Pack<T, B> d, r[kBatch];
-      d.raw = reinterpret_cast<const V*>(d_out + t * d_out_pitch)[c];
+      Held<Aligned, sizeof(T)> held;
+      held.load(d_out + t * d_out_pitch, c, bytes);
+      Loaded l[Batch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        r[i].raw = load_if<B>(rows + at[i] * rows_pitch + static_cast<size_t>(c) * B, here[i]);
+      for (int i = 0; i < Batch; ++i) l[i] = fetch16<Aligned>(rows + at[i] * rows_pitch, 16 * c, bytes, here[i]);
+      const int real = (bytes - 16 * c) / static_cast<int>(sizeof(T));  // values of this vector in the row
+      Pack<T, 16> d;
+      d.raw = held.here;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        Pack<T, B> o;
-        o.raw = V{};
+      for (int i = 0; i < Batch; ++i) {
+        if (!ok[i]) continue;
+        uint8_t* to = d_rows + at[i] * d_rows_pitch;
+        int from;
+        Pack<T, 16> o, r;
+        o.raw = held.for_row(to, c, &from);
+        r.raw = settle<Aligned>(l[i], rows + at[i] * rows_pitch, 16 * c);
         if (here[i]) {
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            const float g = to_float(d.v[e]);
-            o.v[e] = from_float<T>(w[i] * g);
-            dot[i] = fmaf(g, to_float(r[i].v[e]), dot[i]);
+            o.v[e] = from_float<T>(w[i] * to_float(o.v[e]));
+            if (Aligned || e < real) dot[i] = fmaf(to_float(d.v[e]), to_float(r.v[e]), dot[i]);
           }
+        } else {
+          o.raw = make_uint4(0, 0, 0, 0);
         }
-        if (ok[i]) reinterpret_cast<V*>(d_rows + at[i] * d_rows_pitch)[c] = o.raw;
+        put16<Aligned, sizeof(T)>(to, from, bytes, o.raw);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < Batch; ++i) {
       for (int m = 16; m; m /= 2) dot[i] += __shfl_xor_sync(~0u, dot[i], m);
       if (lane == 0) sums[i][warp] = dot[i];
     }
     __syncthreads();
-    if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < k) {
+    if (threadIdx.x < Batch && j0 + static_cast<int>(threadIdx.x) < k) {
       float s = 0.f;
       for (int i = 0; i < warps; ++i) s += sums[threadIdx.x][i];
       d_weights[t * k + j0 + threadIdx.x] = s;
@@ -282,19 +291,20 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
 }
 
 template <typename F>
-cudaError_t by_bytes(int bytes, F&& f) {
-  using std::integral_constant;
-  return bytes == 16  ? f(integral_constant<int, 16>{})
-         : bytes == 4 ? f(integral_constant<int, 4>{})
-                      : f(integral_constant<int, 2>{});
+cudaError_t by_alignment(bool aligned, F&& f) {
+  return aligned ? f(std::true_type{}) : f(std::false_type{});
 }
 template <typename F>
-cudaError_t by_type(int type, int bytes, F&& f) {
-  using std::integral_constant;
-  if (type == ZC_TYPE_FP32)
-    return bytes == 16 ? f(float{}, integral_constant<int, 16>{}) : f(float{}, integral_constant<int, 4>{});
-  const auto half = [&](auto t) { return by_bytes(bytes, [&](auto b) { return f(t, b); }); };
-  return type == ZC_TYPE_FP16 ? half(__half{}) : half(__nv_bfloat16{});
+cudaError_t by_size(int type, bool aligned, F&& f) {
+  return by_alignment(aligned, [&](auto a) {
+    return type_bytes(type) == 4 ? f(a, std::integral_constant<int, 4>{}) : f(a, std::integral_constant<int, 2>{});
+  });
+}
+template <typename F>
+cudaError_t by_type(int type, bool aligned, F&& f) {
+  return by_alignment(aligned, [&](auto a) {
+    return type == ZC_TYPE_FP32 ? f(float{}, a) : type == ZC_TYPE_FP16 ? f(__half{}, a) : f(__nv_bfloat16{}, a);
+  });
 }
 
 }  // namespace
@@ -302,15 +312,14 @@ cudaError_t by_type(int type, int bytes, F&& f) {
 cudaError_t launch_dispatch(const RowShape& s, const void* x, size_t x_pitch, void* rows, size_t rows_pitch,
                             const int* position, const int* offsets, int* status, cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
-  const int v = vector_bytes(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
-  const size_t vecs = s.hidden * b / v;
-  const Cut cut = cut_row(vecs, v, kMaxThreads);
-  return by_bytes(v, [&](auto bytes) {
+  const bool aligned = whole_vectors(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
+  const Cut cut = cut_row(row_vectors(s.hidden * b, aligned), kMaxThreads);
+  return by_size(s.type, aligned, [&](auto a, auto e) {
     const unsigned together = kMaxThreads / cut.threads;  // tokens of a CTA
-    return launch(dispatch_kernel<bytes()>, static_cast<unsigned>((s.tokens + together - 1) / together) * cut.parts,
-                  dim3(cut.threads, together), 0, stream, true,
-                  static_cast<const uint8_t*>(x), x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b,
-                  static_cast<int>(vecs), cut.parts, s.tokens, s.k, position, offsets + s.experts, status);
+    return launch(dispatch_kernel<a(), e()>, static_cast<unsigned>((s.tokens + together - 1) / together) * cut.parts,
+                  dim3(cut.threads, together), 0, stream, true, static_cast<const uint8_t*>(x), x_pitch * b,
+                  static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(s.hidden * b), cut.parts, s.tokens,
+                  s.k, position, offsets + s.experts, status);
   });
 }
 
@@ -319,17 +328,16 @@ bool small_dispatch(size_t slots) { return slots > 0 && slots <= kSmallSlots; }
 cudaError_t launch_small_dispatch(const RowShape& s, const void* ids, int id_bytes, const void* x, size_t x_pitch,
                                   void* rows, size_t rows_pitch, int* position, int* offsets, cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
-  const int v = vector_bytes(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
-  const size_t vecs = s.hidden * b / v;
-  const Cut cut = cut_row(vecs, v, kMaxThreads);
+  const bool aligned = whole_vectors(b, s.hidden, {x, rows}, {x_pitch, rows_pitch});
+  const Cut cut = cut_row(row_vectors(s.hidden * b, aligned), kMaxThreads);
   const unsigned threads = cut.threads < 64 ? 64 : cut.threads;  // at least ZC_MOE_MAX_K
-  return by_bytes(v, [&](auto bytes) {
+  return by_size(s.type, aligned, [&](auto a, auto e) {
     const auto go = [&](auto* p) {
       using Id = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
-      return launch(small_dispatch_kernel<Id, bytes()>, static_cast<unsigned>(s.tokens) * cut.parts, threads, 0,
+      return launch(small_dispatch_kernel<Id, a(), e()>, static_cast<unsigned>(s.tokens) * cut.parts, threads, 0,
                     stream, true, p, static_cast<int>(s.tokens * s.k), s.experts, static_cast<const uint8_t*>(x),
-                    x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(vecs), cut.parts, s.k,
-                    position, offsets);
+                    x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(s.hidden * b),
+                    cut.parts, s.k, position, offsets);
     };
     return id_bytes == 8 ? go(static_cast<const long long*>(ids)) : go(static_cast<const int*>(ids));
   });
@@ -339,22 +347,22 @@ cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitc
                            const int* position, const int* offsets, void* out, size_t out_pitch, int* status,
                            cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
-  const int v = vector_bytes(b, s.hidden, {rows, out}, {rows_pitch, out_pitch});
-  const size_t vecs = s.hidden * b / v;
-  const Cut cut = cut_row(vecs, v, kCombineThreads);
-  const auto go = [&](auto type, auto bytes, auto tokens) {
-    return launch(weights ? combine_kernel<decltype(type), bytes(), tokens(), true>
-                          : combine_kernel<decltype(type), bytes(), tokens(), false>,
+  const bool aligned = whole_vectors(b, s.hidden, {rows, out}, {rows_pitch, out_pitch});
+  const Cut cut = cut_row(row_vectors(s.hidden * b, aligned), kCombineThreads);
+  const auto go = [&](auto type, auto a, auto tokens) {
+    return launch(weights ? combine_kernel<decltype(type), a(), tokens(), true>
+                          : combine_kernel<decltype(type), a(), tokens(), false>,
                   static_cast<unsigned>((s.tokens + tokens() - 1) / tokens()) * cut.parts, cut.threads, 0, stream, true,
-                  static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(out), out_pitch * b, static_cast<int>(vecs), cut.parts, s.tokens, s.k,
-                  position, offsets + s.experts, status);
+                  static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(out),
+                  out_pitch * b, static_cast<int>(s.hidden * b), cut.parts, s.tokens, s.k, position,
+                  offsets + s.experts, status);
   };
-  return by_type(s.type, v, [&](auto type, auto bytes) {
+  return by_type(s.type, aligned, [&](auto type, auto a) {
     // few tokens: one a thread, so that they spread over the SMs
     const bool many = s.tokens * cut.parts >= 2048;
-    return many && s.k <= 2   ? go(type, bytes, std::integral_constant<int, 4>{})
-           : many && s.k <= 4 ? go(type, bytes, std::integral_constant<int, 2>{})
-                              : go(type, bytes, std::integral_constant<int, 1>{});
+    return many && s.k <= 2   ? go(type, a, std::integral_constant<int, 4>{})
+           : many && s.k <= 4 ? go(type, a, std::integral_constant<int, 2>{})
+                              : go(type, a, std::integral_constant<int, 1>{});
   });
 }
 
@@ -363,19 +371,28 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
                                 void* d_rows, size_t d_rows_pitch, float* d_weights, int* status,
                                 cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
-  const int v = vector_bytes(b, s.hidden, {d_out, rows, d_rows}, {d_out_pitch, rows_pitch, d_rows_pitch});
-  const size_t vecs = s.hidden * b / v;
-  return by_type(s.type, v, [&](auto type, auto bytes) {
-    // A token's sums need all of its row, which the CTA's threads walk: with few tokens more threads
-    // finish a row sooner (1 token x 8 x 7168: 12 us with 256, 16 with 128, 25 with 64), with many
-    // fewer leave more CTAs to an SM (16384 x 2 x 1024: 41 us with 64, 53 with 128, 16384 x 8 x
-    // 7168: 582 and 576).
-    const unsigned most = s.tokens < 2048 ? 256 : vecs <= 256 ? 64 : 128;
-    return launch(combine_grad_kernel<decltype(type), bytes()>, static_cast<unsigned>(s.tokens),
-                  cut_row(vecs, 16, most).threads, 0, stream, true,
-                  static_cast<const uint8_t*>(d_out), d_out_pitch * b, static_cast<const uint8_t*>(rows),
-                  rows_pitch * b, weights, static_cast<uint8_t*>(d_rows), d_rows_pitch * b, d_weights,
-                  static_cast<int>(vecs), s.tokens, s.k, position, offsets + s.experts, status);
+  const bool aligned = whole_vectors(b, s.hidden, {d_out, rows, d_rows}, {d_out_pitch, rows_pitch, d_rows_pitch});
+  const size_t vecs = row_vectors(s.hidden * b, aligned);
+  // A token's sums need all of its row, which the CTA's threads walk: with few tokens more threads
+  // finish a row sooner (1 token x 8 x 7168: 12 us with 256, 16 with 128, 25 with 64), with many
+  // fewer leave more CTAs to an SM (16384 x 2 x 1024: 41 us with 64, 53 with 128, 16384 x 8 x
+  // 7168: 582 and 576).
+  const unsigned most = s.tokens < 2048 ? 256 : vecs <= 256 ? 64 : 128;
+  const auto go = [&](auto type, auto a, auto batch) {
+    return launch(combine_grad_kernel<decltype(type), a(), batch()>, static_cast<unsigned>(s.tokens),
+                  cut_row(vecs, most).threads, 0, stream, true, static_cast<const uint8_t*>(d_out), d_out_pitch * b,
+                  static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(d_rows),
+                  d_rows_pitch * b, d_weights, static_cast<int>(s.hidden * b), s.tokens, s.k, position,
+                  offsets + s.experts, status);
+  };
+  // Slots taken together: no more than there are, which leaves room for more CTAs, and two where
+  // every row's vector takes two registers' worth of loads (4999 x 6 x 2050: 72 us by twos, 99 by
+  // fours, 88 by eights).
+  return by_type(s.type, aligned, [&](auto type, auto a) {
+    if (s.k == 1) return go(type, a, std::integral_constant<int, 1>{});
+    if (s.k == 2 || !a()) return go(type, a, std::integral_constant<int, 2>{});
+    return s.k <= 4 ? go(type, std::true_type{}, std::integral_constant<int, 4>{})
+                    : go(type, std::true_type{}, std::integral_constant<int, 8>{});
   });
 }
 
