@@ -164,8 +164,17 @@ struct Walk {
   }
 
   __device__ void locate(unsigned tile, Tile* out) {
+    // the group, 32 looked at a time (every role's warp walks as a whole)
     if (s.tiles[g] > tile) g = 0;
-    while (s.tiles[g + 1] <= tile) ++g;
+    const int lane = threadIdx.x % 32, groups = p.by_blocks ? p.groups : p.groups + 1;
+    for (;;) {
+      const unsigned before = __ballot_sync(~0u, g + lane < groups && s.tiles[min(g + lane, groups - 1) + 1] <= tile);
+      if (before != ~0u) {
+        g += __ffs(~before) - 1;
+        break;
+      }
+      g += 32;
+    }
     // Within a group: bands of kBand rows of P, and in a band all of P's tiles for each of Q's, so
     // that the tiles in flight at a time cover about as many rows of P as of Q.  Shared-out tiles
     // follow one another in a CTA: there Q's tiles for each of P's, whose rows are then in the L2.

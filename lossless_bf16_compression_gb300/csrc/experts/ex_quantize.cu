@@ -189,19 +189,18 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
   }
 }
 
-// block_offsets[g] = blocks of the groups before g, by one CTA of 1024 threads.
-__global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restrict__ offsets, int rows, int groups,
-                                                             int* __restrict__ block_offsets, int* status) {
-  __shared__ int sums[32];
-  let_next_start();
-  wait_for_previous();
-  const int g = threadIdx.x, lane = g % 32, warp = g / 32;
-  int n = 0;
-  if (g < groups) {
-    const int a = offsets ? offsets[g] : 0, z = offsets ? offsets[g + 1] : rows;
-    if (a < 0 || z < a || z > rows || (g == 0 && a != 0)) set_error(status, ZC_ERR_CORRUPT);
-    else n = (z - a + kBlock - 1) / kBlock;
+// Blocks of group g (none, and reported, where its rows are not in range).
+__device__ __forceinline__ int group_blocks(const int* offsets, int g, int rows, int* status) {
+  const int a = offsets ? offsets[g] : 0, z = offsets ? offsets[g + 1] : rows;
+  if (a < 0 || z < a || z > rows || (g == 0 && a != 0)) {
+    set_error(status, ZC_ERR_CORRUPT);
+    return 0;
   }
+  return (z - a + kBlock - 1) / kBlock;
+}
+// The sum of the values of the threads before this one (up to 32 warps, all of which call it).
+__device__ __forceinline__ int sum_before(int n, int* sums) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int incl = n;
   for (int d = 1; d < 32; d *= 2) {
     const int u = __shfl_up_sync(~0u, incl, d);
@@ -211,6 +210,18 @@ __global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restri
   __syncthreads();
   int before = incl - n;
   for (int w = 0; w < warp; ++w) before += sums[w];
+  return before;
+}
+
+// block_offsets[g] = blocks of the groups before g, by one CTA of 1024 threads.
+__global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restrict__ offsets, int rows, int groups,
+                                                             int* __restrict__ block_offsets, int* status) {
+  __shared__ int sums[32];
+  let_next_start();
+  wait_for_previous();
+  const int g = threadIdx.x;
+  const int n = g < groups ? group_blocks(offsets, g, rows, status) : 0;
+  const int before = sum_before(n, sums);
   if (g < groups) block_offsets[g] = before;
   if (g == groups - 1) block_offsets[groups] = before + n;
 }
@@ -247,28 +258,45 @@ __device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
   return x % 2 ? make_uint4(v.z, v.w, v.x, v.y) : v;
 }
 
-template <typename T, bool Vec, int Fmt>
+// Inline: every CTA counts the blocks before its own, one group a thread, and the first writes
+// block_offsets, which saves a launch; otherwise they come from block_offsets_kernel.  With many
+// CTAs the counting costs more than the launch (8192 x 4096, 2304 CTAs: 26.6 us with the launch,
+// 24.6 without; 32768 x 7168, 15,232 CTAs: 119.5 and 123).
+constexpr int kInlineGroups = 256;
+constexpr size_t kInlineCtas = 4096;
+template <typename T, bool Vec, int Fmt, bool Inline>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
                                                                int cols, int groups, const int* __restrict__ offsets,
                                                                int capacity, uint8_t* __restrict__ values,
                                                                uint8_t* __restrict__ scales,
-                                                               const int* __restrict__ block_offsets) {
+                                                               int* __restrict__ block_offsets, int* status) {
   __shared__ TileShared s;
   __shared__ int first, last;  // this block's rows
+  __shared__ int sums[8];
   const int b = blockIdx.x, tid = threadIdx.x, cg = tid % 16, rg = tid / 16;
   const int c = blockIdx.y * kBlock + cg * 8;
   if (tid == 0) first = last = 0;
   let_next_start();
   wait_for_previous();
-  __syncthreads();
-  for (int g = tid; g < groups; g += 256) {
-    const int b0 = block_offsets[g];
-    if (b0 <= b && b < block_offsets[g + 1]) {
-      const long long a = (offsets ? offsets[g] : 0) + static_cast<long long>(b - b0) * kBlock;
-      const int z = offsets ? offsets[g + 1] : rows;
-      // (a group with bad starts has no blocks)
-      first = static_cast<int>(a);
-      last = static_cast<int>(min(static_cast<long long>(z), a + kBlock));
+  const auto take = [&](int g, int b0) {  // this block is the group's, whose first one is b0
+    const long long a = (offsets ? offsets[g] : 0) + static_cast<long long>(b - b0) * kBlock;
+    const int z = offsets ? offsets[g + 1] : rows;
+    first = static_cast<int>(a);
+    last = static_cast<int>(min(static_cast<long long>(z), a + kBlock));
+  };
+  if (Inline) {
+    const int n = tid < groups ? group_blocks(offsets, tid, rows, status) : 0;
+    const int b0 = sum_before(n, sums);
+    if (b0 <= b && b < b0 + n) take(tid, b0);
+    if (b == 0 && blockIdx.y == 0) {
+      if (tid < groups) block_offsets[tid] = b0;
+      if (tid == groups - 1) block_offsets[groups] = b0 + n;
+    }
+  } else {
+    __syncthreads();
+    for (int g = tid; g < groups; g += 256) {
+      const int b0 = block_offsets[g];
+      if (b0 <= b && b < block_offsets[g + 1]) take(g, b0);  // (a group with bad starts has no blocks)
     }
   }
   __syncthreads();
@@ -412,15 +440,21 @@ cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_
                                     const int* offsets, int fmt, uint8_t* values, uint8_t* scales, int* block_offsets,
                                     int* status, cudaStream_t stream) {
   const size_t capacity = column_blocks(rows, groups);
-  const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, true, offsets, static_cast<int>(rows),
-                                 groups, block_offsets, status);
-  if (err != cudaSuccess || capacity == 0) return err;
+  const bool inline_groups =
+      capacity > 0 && groups <= kInlineGroups && capacity * ceil_div(cols, kBlock) <= kInlineCtas;
+  if (!inline_groups) {
+    const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, true, offsets, static_cast<int>(rows),
+                                   groups, block_offsets, status);
+    if (err != cudaSuccess || capacity == 0) return err;
+  }
   const dim3 grid(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, kBlock)));
   return variant(type, vector_rows(x, pitch, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(quantize_columns_kernel<T, vec(), f()>, grid, 256, 0, stream, true, static_cast<const T*>(x), pitch,
-                  static_cast<int>(rows), static_cast<int>(cols), groups, offsets, static_cast<int>(capacity), values,
-                  scales, block_offsets);
+    return launch(inline_groups ? quantize_columns_kernel<T, vec(), f(), true>
+                                : quantize_columns_kernel<T, vec(), f(), false>,
+                  grid, 256, 0, stream, true, static_cast<const T*>(x), pitch, static_cast<int>(rows),
+                  static_cast<int>(cols), groups, offsets, static_cast<int>(capacity), values, scales, block_offsets,
+                  status);
   });
 }
 

@@ -55,8 +55,8 @@ class Matrix:
 
     def values(self) -> torch.Tensor:
         """The 8-bit values without their scales (a view)."""
-        v = self.data.view(_FLOAT8[self.fmt])
-        return v if self.cols == v.shape[-1] else v.narrow(-1, 0, self.cols)
+        v, cols = self.data.view(_FLOAT8[self.fmt]), self.cols
+        return v if cols == v.shape[-1] else v.as_strided((*v.shape[:-1], cols), v.stride())
 
     def scale_values(self) -> torch.Tensor:
         """The scales as float32 powers of two, in their own layout."""
