@@ -118,7 +118,7 @@ int zc_fp8_quantize_weight(const void* w, int type, int groups, size_t rows, siz
  * rows).  Rows from offsets[groups] on get zeros.  Products of values and scales are exact; sums
  * are in fp32; out (rows x n of out_type ZC_TYPE_BF16 or ZC_TYPE_FP32) is rounded once.
  * values arrays 128-byte aligned, scales 4-byte aligned.  workspace: zc_fp8_matmul_workspace bytes,
- * 16-byte aligned, null where that is 0 (groups of many rows). */
+ * 16-byte aligned, null where that is 0 (all but few rows with long sums). */
 size_t zc_fp8_matmul_workspace(size_t rows, int groups, size_t n, size_t k);
 int zc_fp8_matmul(const void* a, const void* a_scales, int a_fmt, size_t rows, const void* b, const void* b_scales,
                   int b_fmt, int groups, size_t n, size_t k, const int* offsets, void* out, size_t out_pitch,

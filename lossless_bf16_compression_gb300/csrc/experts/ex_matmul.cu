@@ -613,6 +613,7 @@ size_t smem_bytes(int load_q, int stages) {
   return 1024 + static_cast<size_t>(stages) * (kTileP + load_q) * kBlock + sizeof(Shared);
 }
 constexpr size_t kSmemLimit = 227 * 1024;
+constexpr size_t kSms = 152;      // of a GB300, where a cut is chosen without asking the device
 constexpr size_t kMaxCtas = 160;  // CTAs of a launch, for the size of a workspace
 size_t sm_count(const DeviceInfo& dev) { return dev.sm_count < static_cast<int>(kMaxCtas) ? dev.sm_count : kMaxCtas; }
 
@@ -707,17 +708,21 @@ struct Shape {
 };
 
 // Groups of up to 64 rows on average are bound by the weights' bytes: one tile for all of a group's
-// rows where it is no more than half again the average, and the blocks shared out, so that every
-// SM streams the same amount (8 rows x 7168 x 4096: 24.6 us by whole tiles, %SHARE8% shared out; 32
-// rows over 16 such experts: 86 and %SHARE32%).  Larger groups are bound by the products: the
-// cut with the least time by the measured cycles of a block, given its waves.
+// rows where they are no more than half again the average.  With few such tiles of many blocks the
+// blocks are shared out among all the SMs.  That takes about 0.27 us for each block that a CTA has
+// less to do and adds 6 to 12 us of joining, so it pays from 32 blocks on: one group of 8 rows,
+// 7168 x 4096, 32 tiles, 44 blocks less: 16.2 us against 19.4; 14336 x 4096, 88 less: 20 against 34.6;
+// 64 rows of four groups, 4096 x 512, 28 less: 13.3 both; 100 rows of eight groups, 2048 x 2048, 2
+// less: 17.3 against 11.3.  Larger groups are bound by the products: the cut with the least time by
+// the measured cycles of a block, given its waves.
 Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool by_blocks) {
   const size_t active = by_blocks ? groups : q_rows < groups ? q_rows : groups;
   const size_t average = by_blocks ? q_rows : ceil_div(q_rows, active);
   if (!by_blocks && average <= 64) {
     int t = 16;
     while (2 * static_cast<size_t>(t) < 3 * average) t *= 2;
-    return {t, false, true};
+    const size_t shared = ceil_div(active * ceil_div(p_rows, kTileP) * blocks, kSms);
+    return {t, false, shared + 32 <= blocks};
   }
   struct {
     Shape shape;
@@ -728,7 +733,7 @@ Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool 
   for (const auto& c : cuts) {
     const size_t g = c.shape.pair ? 2 : 1;
     const double tiles = static_cast<double>(active) * ceil_div(average, c.shape.tile_q) * ceil_div(p_rows, kTileP * g);
-    const double waves = std::ceil(tiles / (152 / g));
+    const double waves = std::ceil(tiles / (kSms / g));
     const double time = waves * c.cycles;
     if (best == nullptr || time < least) best = &c.shape, least = time;
   }

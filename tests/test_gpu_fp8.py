@@ -219,7 +219,10 @@ def test_matmul_many_row_tiles_and_wide_scales():
 @pytest.mark.parametrize("counts,n,k", [
     ((2048,), 2432, 300),             # 152 tiles of 128 x 256: one wave of single CTAs, two of pairs
     ((100,) * 38, 500, 260),          # 152 tiles of 128 x 128
-    ((64,) * 3 + (0, 200), 2100, 520),  # blocks shared out, groups above and below the average
+    ((64,) * 3 + (0, 200), 2100, 520),  # groups above and below the average
+    ((40,) * 3 + (0, 90), 300, 5000),   # blocks shared out, a group of two tiles, one of none
+    ((3, 0, 1, 20), 257, 6000),         # the same with the smallest tiles
+    ((1,) * 20, 130, 20000),            # parts of several tiles in one CTA
     ((1,) * 300, 130, 140),           # more groups than CTAs
     ((256, 255, 257, 1, 511), 256, 128),  # tile ends on, before and after group ends, one block
     ((500,) * 6, 2050, 640),          # several bands of tiles, rows of out not whole 32-bit words apart

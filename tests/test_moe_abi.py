@@ -51,6 +51,7 @@ def test_sizes():
     assert f("zc_moe_sort_workspace")(100000, 8) >= 9 * 4
     assert f("zc_fp8_matmul_workspace")(8, 1, 4096, 7168) > 0 == f("zc_fp8_matmul_workspace")(0, 1, 4096, 7168)
     assert f("zc_fp8_matmul_workspace")(4096, 1, 4096, 7168) == 0 == f("zc_fp8_matmul_workspace")(8, 0, 4096, 7168)
+    assert f("zc_fp8_matmul_workspace")(8, 1, 4096, 2048) == 0  # short sums need none
     assert f("zc_moe_sort_workspace")((1 << 30) + 1, 8) == 0 == f("zc_moe_sort_workspace")(10, 0)
 
 
@@ -106,7 +107,9 @@ def test_products_refuse():
     refused("zc_fp8_matmul", [A, B, 0, 10, C, D, 0, 2, 64, 128, E, F, 64, 0, F * 2, 0],
             [(0, 0, INV), (1, 0, INV), (2, 2, INV), (4, 0, INV), (5, 0, INV), (6, -1, INV), (7, 0, INV), (8, 0, INV),
              (9, 0, INV), (10, 0, INV), (11, 0, INV), (12, 63, INV), (13, 1, INV), (0, A + 16, MIS), (4, C + 64, MIS),
-             (1, B + 2, MIS), (11, F + 1, MIS), (11, A, INV), (11, C, INV), (14, 0, INV), (14, F * 2 + 4, MIS), (14, F, INV)])
+             (1, B + 2, MIS), (11, F + 1, MIS), (11, A, INV), (11, C, INV)])
+    refused("zc_fp8_matmul", [A, B, 0, 10, C, D, 0, 2, 64, 8192, E, F, 64, 0, F * 2, 0],  # long sums: a workspace
+            [(14, 0, INV), (14, F * 2 + 4, MIS), (14, F, INV)])
     refused("zc_fp8_weight_grad", [A, B, 0, C, D, 0, 4, 2, 64, 128, E, F, 0, 0],
             [(0, 0, INV), (1, 0, INV), (2, 2, INV), (3, 0, INV), (5, 5, INV), (7, 0, INV), (8, 0, INV), (9, 0, INV),
              (10, 0, INV), (11, 0, INV), (12, 1, INV), (0, A + 16, MIS), (10, E + 2, MIS), (11, C, INV)])
