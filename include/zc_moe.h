@@ -93,6 +93,9 @@ int zc_moe_combine_grad(const void* d_out, size_t d_out_pitch, const void* rows,
 int zc_fp8_quantize(const void* x, size_t pitch, int type, size_t rows, size_t cols, int fmt, void* values,
                     void* scales, cudaStream_t stream);
 
+/* Scale bytes as fp32: 4 `words` values 2^(byte - 127) (NaN for byte 255).  out: 16-byte aligned. */
+int zc_fp8_scale_values(const void* scales, size_t words, float* out, cudaStream_t stream);
+
 /* Blocks of 128 along the rows of each group, for products that sum over the rows: the result
  * is the transpose, `cols` rows of 128 * capacity values, capacity = zc_fp8_column_blocks(rows,
  * groups).  Group g (rows offsets[g] .. offsets[g + 1] - 1 of x) starts at block

@@ -18,6 +18,7 @@ SIGNATURES = {
     "zc_moe_combine": (_I, [_P, _N, _I, _P, _P, _P, _N, _I, _I, _N, _P, _N, _P]),
     "zc_moe_combine_grad": (_I, [_P, _N, _P, _N, _I, _P, _P, _P, _N, _I, _I, _N, _P, _N, _P, _P]),
     "zc_fp8_quantize": (_I, [_P, _N, _I, _N, _N, _I, _P, _P, _P]),
+    "zc_fp8_scale_values": (_I, [_P, _N, _P, _P]),
     "zc_fp8_column_blocks": (_N, [_N, _I]),
     "zc_fp8_quantize_columns": (_I, [_P, _N, _I, _N, _N, _I, _P, _I, _P, _P, _P, _P]),
     "zc_fp8_quantize_weight": (_I, [_P, _I, _I, _N, _N, _I, _P, _P, _P, _P, _P]),

@@ -174,6 +174,15 @@ int zc_fp8_quantize(const void* x, size_t pitch, int type, size_t rows, size_t c
                                     static_cast<uint8_t*>(scales), stream));
 }
 
+int zc_fp8_scale_values(const void* scales, size_t words, float* out, cudaStream_t stream) {
+  if (words > kMaxRows) return ZC_ERR_INVALID_ARG;
+  if (words == 0) return ZC_OK;
+  if (!scales || !out) return ZC_ERR_INVALID_ARG;
+  if (!aligned(scales, 4) || !aligned(out, 16)) return ZC_ERR_MISALIGNED;
+  if (clash({{out, 16 * words}}, {{scales, 4 * words}})) return ZC_ERR_INVALID_ARG;
+  return finish(ex::launch_scale_values(scales, words, out, stream));
+}
+
 size_t zc_fp8_column_blocks(size_t rows, int groups) {
   if (rows > kMaxRows || !groups_ok(groups)) return 0;
   return ex::column_blocks(rows, groups);

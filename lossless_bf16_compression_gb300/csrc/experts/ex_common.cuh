@@ -191,6 +191,7 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
 size_t column_blocks(size_t rows, int groups);
 cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, size_t cols, int fmt, uint8_t* values,
                             uint8_t* scales, cudaStream_t stream);
+cudaError_t launch_scale_values(const void* scales, size_t words, float* out, cudaStream_t stream);
 cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_t rows, size_t cols, int groups,
                                     const int* offsets, int fmt, uint8_t* values, uint8_t* scales, int* block_offsets,
                                     int* status, cudaStream_t stream);

@@ -140,9 +140,10 @@ __device__ __forceinline__ uint2 round_column(const Raw8<T> (&r)[8], int j, floa
 }
 
 // A warp takes four blocks (one scale word) of each of R rows: lane l holds values 8l .. 8l + 7
-// of the first two blocks and of the last two, so 16 lanes share a block.  CTA: 8 R rows, whose
-// scale words lie next to each other.  With R = 4 a lane has 128 bytes of 16-bit input in flight.
-constexpr int kRowWarps = 4;  // (32768 x 7168: 102 us; 8 warps 108, 16 warps 117)
+// of the first two blocks and of the last two, so 16 lanes share a block.  A CTA's 4 R rows have
+// their scale words next to each other.  With R = 4 a lane has 128 bytes of 16-bit input in flight
+// (R = 8, with the registers that takes: 138 us for 102 below).
+constexpr int kRowWarps = 4;  // (32768 x 7168, bf16: 102 us, 6.9 TB/s; 8 warps 108, 16 warps 117)
 template <typename T, bool Vec, int Fmt, int R>
 __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __restrict__ x, size_t pitch, size_t rows,
                                                                   int cols, unsigned words,
@@ -187,6 +188,20 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
     const uint32_t odd = __shfl_sync(~0u, even, 16);
     if (lane == 0) scales[word * rows + r] = even | odd << 8;
   }
+}
+
+// The scales as fp32: 2^(byte - 127), by the bits; byte 0 is the subnormal 2^-127, 255 a NaN.
+__global__ void __launch_bounds__(256) scale_values_kernel(const uint32_t* __restrict__ scales, size_t words,
+                                                           float4* __restrict__ out) {
+  let_next_start();
+  wait_for_previous();
+  const size_t i = blockIdx.x * size_t(256) + threadIdx.x;
+  if (i >= words) return;
+  const uint32_t w = scales[i];
+  const auto value = [](uint32_t b) {
+    return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+  };
+  out[i] = make_float4(value(w & 255), value(w >> 8 & 255), value(w >> 16 & 255), value(w >> 24));
 }
 
 // Blocks of group g (none, and reported, where its rows are not in range).
@@ -434,6 +449,11 @@ cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, 
     return ceil_div(rows, kRowWarps * 4) * words >= 2048 ? go(std::integral_constant<int, vec() ? 4 : 2>{})
                                                          : go(std::integral_constant<int, 1>{});
   });
+}
+
+cudaError_t launch_scale_values(const void* scales, size_t words, float* out, cudaStream_t stream) {
+  return launch(scale_values_kernel, static_cast<unsigned>(ceil_div(words, 256)), 256, 0, stream, true,
+                static_cast<const uint32_t*>(scales), words, reinterpret_cast<float4*>(out));
 }
 
 cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_t rows, size_t cols, int groups,

@@ -55,13 +55,12 @@ class Matrix:
 
     def values(self) -> torch.Tensor:
         """The 8-bit values without their scales (a view)."""
-        v, cols = self.data.view(_FLOAT8[self.fmt]), self.cols
-        return v if cols == v.shape[-1] else v.as_strided((*v.shape[:-1], cols), v.stride())
+        return self.data.view(_FLOAT8[self.fmt]).narrow(-1, 0, self.cols)
 
-    def scale_values(self) -> torch.Tensor:
+    def scale_values(self, stream=None) -> torch.Tensor:
         """The scales as float32 powers of two, in their own layout."""
-        out = torch.empty(self.scales.shape, dtype=torch.float32, device=self.scales.device)
-        return out.copy_(self.scales.view(torch.float8_e8m0fnu))
+        device = on_device("scales", self.scales, None)
+        return on(stream, (self.scales,), _scale_values, self.scales, device)
 
 
 _ROW_TYPES = tuple(TYPES)
@@ -73,6 +72,12 @@ def _made(data, scales, cols, fmt, offsets=None):
     m = object.__new__(Matrix)
     m.data, m.scales, m.cols, m.fmt, m.offsets = data, scales, cols, fmt, offsets
     return m
+
+
+def _scale_values(scales, device):
+    out = torch.empty(scales.shape, dtype=torch.float32, device=scales.device)
+    call("zc_fp8_scale_values", scales.data_ptr(), scales.numel() // 4, out.data_ptr(), current(device))
+    return out
 
 
 def _pitch(cols):

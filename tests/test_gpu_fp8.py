@@ -57,6 +57,26 @@ def check_matrix(m, values, exponents, cols):
     assert not m.data[:, cols:].any().item()
 
 
+def test_scale_values():
+    """Every scale byte, in words of which the last CTA has only a part: 2^(byte - 127), 255 a NaN."""
+    for words in (1, 64, 257, 5000):
+        data = (torch.arange(4 * words) % 256).to(torch.uint8).view(1, words, 4).cuda()
+        m = fp8.Matrix(torch.zeros((words, 128), dtype=torch.uint8, device="cuda"), data, cols=100)
+        got = doubles(m.scale_values())
+        expect = np.exp2((np.arange(4 * words) % 256).reshape(1, words, 4) - 127.0)
+        expect[expect == 2.0**128] = np.nan
+        assert got.shape == expect.shape and np.array_equal(got, expect, equal_nan=True)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        again = m.scale_values(stream=side)
+        side.synchronize()
+        assert np.array_equal(doubles(again), expect, equal_nan=True)
+    with pytest.raises(TypeError):
+        fp8.Matrix(torch.zeros((1, 128), dtype=torch.uint8), torch.zeros((1, 1, 4), dtype=torch.uint8), 3).scale_values()
+    assert fp8.quantize(torch.zeros((0, 200), device="cuda")).scale_values().shape == (1, 0, 4)
+    assert fp8.quantize(torch.zeros((0, 200), device="cuda")).values().shape == (0, 200)
+
+
 SHAPES = [(1, 1), (1, 128), (2, 127), (5, 129), (33, 512), (64, 640), (7, 1000), (131, 2048), (3, 7168)]
 
 

@@ -95,6 +95,8 @@ def test_quantize_refuses():
     refused("zc_fp8_quantize", [A, 256, 0, 10, 256, 0, B, C, 0],
             [(0, 0, INV), (1, 255, INV), (2, 3, INV), (4, 0, INV), (5, 2, INV), (6, 0, INV), (7, 0, INV), (0, A + 1, MIS),
              (6, B + 8, MIS), (7, C + 2, MIS), (6, A, INV), (7, B, INV), (4, (1 << 20) + 1, INV), (3, 1 << 31, INV)])
+    refused("zc_fp8_scale_values", [A, 64, B, 0],
+            [(0, 0, INV), (1, 1 << 31, INV), (2, 0, INV), (0, A + 1, MIS), (2, B + 8, MIS), (2, A + 240, INV)])
     refused("zc_fp8_quantize_columns", [A, 256, 0, 10, 256, 3, B, 0, C, D, E, 0],
             [(0, 0, INV), (1, 255, INV), (5, 0, INV), (5, 1025, INV), (6, 0, INV), (7, 2, INV), (8, 0, INV), (9, 0, INV),
              (10, 0, INV), (8, C + 8, MIS), (8, A, INV), (10, C, INV)])
