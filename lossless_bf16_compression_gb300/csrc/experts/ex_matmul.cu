@@ -16,7 +16,7 @@
 // each CTA loading half of both, which takes a third off what the SMs read from the L2
 // and off the shared-memory traffic that a CTA alone is bound by (8192^3: 304 us against 347).
 // Roles: warp 0 issues the TMA loads (128 columns a stage), warp 1 the products, warps 2, 3, 8 and 9
-// bring the scales, warps 4-7 write the results while the next tile's products run.
+// bring the scales, warps 4-7 and 10-13 write the results while the next tile's products run.
 //
 // Scales are kept four blocks to a word, [word][row].  A product's scales lie in tensor memory, row
 // r at lane r % 32 (in each quarter of the lanes) and column r / 32, so a warp reads 32 rows' words
@@ -32,9 +32,10 @@ namespace zc {
 namespace ex {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
 constexpr int kBand = 2048;  // rows of P: 152 SMs hold 16 x 9.5 tiles of 128 x 256
 constexpr int kTileP = 128;
+constexpr int kWriters = 8;    // warps of the epilogue
 constexpr int kMaxStages = 12;
 constexpr int kMaxTurns = 4;   // words of scales in tensor memory; two where accumulators leave no more room
 constexpr int kWordsAhead = 4;
@@ -57,8 +58,8 @@ struct TileParams {
   const int* offsets;         // rows (or blocks) of each group; null: one group
   // Where tiles are few or uneven: the blocks of all tiles are shared out evenly, so that a CTA
   // begins and ends inside tiles.  Its sums of a part of a tile go to `parts` (two a CTA, [column][128
-  // rows]), and whichever warp comes last to a tile's quarter of rows, by `arrivals` (four a
-  // tile, zero at the start), adds the parts in their order.  Null: whole tiles.
+  // rows]), and whichever warp comes last to its share of a tile, by `arrivals` (eight a tile, zero
+  // at the start), adds the parts in their order.  Null: whole tiles.
   float* parts;
   unsigned* arrivals;
   void* out;
@@ -276,11 +277,15 @@ __device__ __forceinline__ uint32_t pair_up(uint32_t v0, uint32_t v1) {
   return r;
 }
 
-// The epilogue: warps 4-7, each its 32 lanes (rows of P) of every finished tile.
-// A warp's quarter of a part of a tile: to its place among the parts, and the whole if it is the last.
+// The epilogue: two warps for each quarter of the tensor-memory lanes (32 rows of P), one taking the even
+// chunks of a tile's columns and one the odd ones.  A warp reads a chunk, waits and stores it; a second
+// chunk in flight made it slower (16 groups of 8 blocks, 2048 x 7168: 180 us; 172 without, and with
+// 1 block a group 150 and 135), the second warp covers the wait (1 block: 108 us, 4.3 TB/s written).
+
+// A warp's share of a part of a tile: to its place among the parts, and the whole if it is the last.
 template <typename Out>
 __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const Walk<1>& walk, const Tile& tile,
-                                           uint32_t from, unsigned acc, int quarter) {
+                                           uint32_t from, unsigned acc, int quarter, int half) {
   const int lane = threadIdx.x % 32, row = 32 * quarter + lane;
   const unsigned tile_begin = tile.index * p.blocks;
   const size_t part = static_cast<size_t>(kTileP) * p.tile_q;
@@ -289,7 +294,7 @@ __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const
     return p.parts + (2 * cta + (walk.begin_of(cta) > tile_begin ? 0 : 1)) * part + row;
   };
   float* mine = place(blockIdx.x);
-  for (int c = 0; c < p.tile_q; c += 16) {
+  for (int c = 16 * half; c < p.tile_q; c += 32) {
     uint32_t v[16];
     tmem_load(from + c, v);
     tmem_load_wait(v);
@@ -302,7 +307,7 @@ __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const
   unsigned before = 0;
   if (lane == 0) {
     mbar_arrive(&s.sum_empty[acc]);
-    before = atomicAdd(&p.arrivals[static_cast<size_t>(tile.index) * 4 + quarter], 1u);
+    before = atomicAdd(&p.arrivals[static_cast<size_t>(tile.index) * kWriters + 2 * quarter + half], 1u);
   }
   before = __shfl_sync(~0u, before, 0);
   const unsigned first = walk.cta_of(tile_begin), last = walk.cta_of(tile_begin + p.blocks - 1);
@@ -310,7 +315,7 @@ __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const
   __threadfence();
   const int pr = tile.p0 + row;
   Out* out = static_cast<Out*>(p.out) + static_cast<size_t>(tile.q0) * p.out_pitch + pr;
-  for (int c = 0; c < tile.q1 - tile.q0; c += 16) {
+  for (int c = 16 * half; c < tile.q1 - tile.q0; c += 32) {
     float sum[16] = {};
     for (unsigned cta = first; cta <= last; cta += 4) {  // four parts' loads in flight
       float v[4][16];
@@ -335,7 +340,7 @@ __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const
 template <int G, typename Out>
 __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint32_t tmem, uint32_t accumulator,
                                            int first_row) {
-  const int quarter = threadIdx.x / 32 % 4, lane = threadIdx.x % 32;
+  const int quarter = threadIdx.x / 32 % 4, lane = threadIdx.x % 32, half = threadIdx.x / 32 >= 10;
   volatile unsigned* failed = &s.failed;
   const bool shared_columns = p.tile_q > kSecond;
   Walk<G> walk(p, s);
@@ -348,7 +353,7 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
     const int chunks = (columns + kChunk - 1) / kChunk;
     if (tile.b0 == tile.b1) {
       if (pr < p.p_rows)
-        for (int c = 0; c < columns; ++c) put(out + c * p.out_pitch, 0u);
+        for (int c = half; c < columns; c += 2) put(out + c * p.out_pitch, 0u);
       continue;
     }
     if (!__all_sync(~0u, wait_phase(&s.sum_full[sums % 2], sums / 2 % 2, failed))) break;
@@ -356,7 +361,7 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
     const uint32_t from = tmem + (static_cast<uint32_t>(quarter) << 21) + sums % 2 * accumulator;
     if constexpr (G == 1) {
       if (p.parts && tile.b1 - tile.b0 != p.blocks) {
-        write_part<Out>(p, s, walk, tile, from, sums % 2, quarter);
+        write_part<Out>(p, s, walk, tile, from, sums % 2, quarter, half);
         ++sums;
         continue;
       }
@@ -397,23 +402,26 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
     };
     if (p.tile_q < kChunk) {  // 16 columns
       uint32_t v[16];
-      tmem_load(from, v);
-      tmem_load_wait(v);
+      if (half == 0) {
+        tmem_load(from, v);
+        tmem_load_wait(v);
+      }
       release();
-      if (pr < p.p_rows)
+      if (half == 0 && pr < p.p_rows)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (i < columns) put(out + i * p.out_pitch, v[i]);
     } else {
-      // one chunk is stored while the next one is read
-      uint32_t v[2][kChunk];
-      tmem_load(from + chunk_at(0) * kChunk, v[0]);
-#pragma unroll 2
-      for (int i = 0; i < all; ++i) {
-        tmem_load_wait(v[i % 2]);
-        if (i == (shared_columns ? 0 : all - 1)) release();
-        if (i + 1 < all) tmem_load(from + chunk_at(i + 1) * kChunk, v[(i + 1) % 2]);
-        if (chunk_at(i) < chunks) store(v[i % 2], chunk_at(i));
+      // this warp has done with the columns that the other accumulator shares, or with all, after:
+      const int done = shared_columns ? half : (all - 1 - half) / 2 * 2 + half;
+      if (half >= all) release();
+#pragma unroll 1
+      for (int i = half; i < all; i += 2) {
+        uint32_t v[kChunk];
+        tmem_load(from + chunk_at(i) * kChunk, v);
+        tmem_load_wait(v);
+        if (i == done) release();
+        if (chunk_at(i) < chunks) store(v, chunk_at(i));
         __syncwarp();
       }
     }
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s.sum_full[i], 1);
-        mbar_init(&s.sum_empty[i], 4 * G);
+        mbar_init(&s.sum_empty[i], kWriters * G);
       }
       mbar_init(&s.drained, 1);
       s.failed = 0;
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         while (!phase_done(&s.drained, 0) && now_ns() - start < kWaitLimitNs) {}
       }
     }
-  } else if (warp < 4 || warp >= 8) {
+  } else if (warp < 4 || warp == 8 || warp == 9) {
     // The scales: one warp for each quarter of the tensor-memory lanes, which all hold the same
     // words.  Next to the tiles' traffic a load takes about 2000 cycles, as long as a word's
     // products, so the words of the next kWordsAhead - 1 are on their way in registers.
@@ -741,7 +749,7 @@ Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool 
 }
 
 size_t parts_bytes(const Shape& shape, size_t tiles) {
-  return shape.share ? 2 * kMaxCtas * kTileP * shape.tile_q * sizeof(float) + 4 * tiles * sizeof(unsigned) : 0;
+  return shape.share ? 2 * kMaxCtas * kTileP * shape.tile_q * sizeof(float) + kWriters * tiles * sizeof(unsigned) : 0;
 }
 // Tiles of a row-grouped product, at most.
 size_t most_tiles(const Shape& shape, size_t q_rows, size_t groups, size_t p_rows) {
@@ -784,9 +792,10 @@ cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t 
   if (shape.share) {
     const size_t tiles = most_tiles(shape, p.rows, p.groups, p.n);
     t.arrivals = static_cast<unsigned*>(p.workspace);
-    t.parts = reinterpret_cast<float*>(t.arrivals + 4 * tiles);
-    const cudaError_t err = launch(clear_kernel, static_cast<unsigned>(tiles < 8192 ? ceil_div(tiles, 256) : 32), 256,
-                                   0, stream, true, static_cast<uint4*>(p.workspace), tiles);
+    t.parts = reinterpret_cast<float*>(t.arrivals + kWriters * tiles);
+    const size_t clear = tiles * kWriters / 4;
+    const cudaError_t err = launch(clear_kernel, static_cast<unsigned>(clear < 8192 ? ceil_div(clear, 256) : 32), 256,
+                                   0, stream, true, static_cast<uint4*>(p.workspace), clear);
     if (err != cudaSuccess) return err;
   }
   return launch_any(t, shape, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, dev, stream);
