@@ -15,6 +15,9 @@
 // columns.  Tiles of 256 rows of Q are shared by a pair of CTAs, 256 rows of P by 256 of Q with
 // each CTA loading half of both, which takes a third off what the SMs read from the L2
 // and off the shared-memory traffic that a CTA alone is bound by (8192^3: 304 us against 347).
+// Many rows are bound by the tensor cores (32768 rows, 7168 x 4096, 16 groups: 528 us, 3.6 PFLOP/s; back to
+// back the power limit brings the clock down to 1.4 GHz and that to 3.1), few by the weights' bytes (32
+// rows: 69 us, 6.0 TB/s of the active groups' weights).
 // Roles: warp 0 issues the TMA loads (128 columns a stage), warp 1 the products, warps 2, 3, 8 and 9
 // bring the scales, warps 4-7 and 10-13 write the results while the next tile's products run.
 //
@@ -279,8 +282,8 @@ __device__ __forceinline__ uint32_t pair_up(uint32_t v0, uint32_t v1) {
 
 // The epilogue: two warps for each quarter of the tensor-memory lanes (32 rows of P), one taking the even
 // chunks of a tile's columns and one the odd ones.  A warp reads a chunk, waits and stores it; a second
-// chunk in flight made it slower (16 groups of 8 blocks, 2048 x 7168: 180 us; 172 without, and with
-// 1 block a group 150 and 135), the second warp covers the wait (1 block: 108 us, 4.3 TB/s written).
+// chunk in flight made it slower (weights' gradient, 2048 x 7168, 16 groups of 8 blocks: 180 us, 172
+// without; of 1 block 150 and 135), the second warp covers the wait (1 block: 110 us, 4.3 TB/s written).
 
 // A warp's share of a part of a tile: to its place among the parts, and the whole if it is the last.
 template <typename Out>
@@ -373,8 +376,8 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
       Out* to = out + static_cast<size_t>(chunk) * kChunk * p.out_pitch;
       const int n = columns - chunk * kChunk;
       if (sizeof(Out) == 2 && p.out_words && n >= kChunk) {
-        // two columns a store, half as many stores (weights' gradient of 16384 x 7168 x 2048, whose
-        // tiles sum only 8 blocks: 232 -> 218 us; whole rows by way of shared memory: 317 us, the
+        // two columns a store, half as many stores (16 groups of 8 blocks, 2048 x 7168: 176 -> 170 us,
+        // of 1 block 121 -> 110; whole rows by way of shared memory took half as long again, the
         // operands' traffic leaves it no bandwidth)
         uint32_t w[kChunk / 2];
 #pragma unroll

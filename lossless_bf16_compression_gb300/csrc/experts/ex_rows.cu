@@ -3,7 +3,9 @@
 // tokens: a token's row is read (or written) once and its k sorted rows once each, which is all
 // the traffic there is, and every sum over j runs inside one thread in slot order (no atomics).
 // Bound by HBM when there are many tokens, by two dependent loads (position, then row) when there
-// are few; so a thread asks for the rows of eight slots before it uses the first.
+// are few; so a thread asks for the rows of eight slots before it uses the first.  16384 tokens x 8 x
+// 7168, bf16: dispatch 320 us (6.6 TB/s), combine 317 (6.7), combine's gradient 576 (7.3, part of it from the
+// L2); one token 8, 8 and 13 us with the launches, of which the sort's part is in dispatch.
 #include <initializer_list>
 
 #include "ex_common.cuh"
