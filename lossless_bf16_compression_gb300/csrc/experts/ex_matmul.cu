@@ -48,6 +48,13 @@ constexpr int kChunk = 32;           // accumulator columns a warp reads at once
 // Two accumulators of 256 columns and the scales do not fit in 512 columns: with tiles of 256 the
 // second accumulator starts at column 224, and the epilogue reads the 32 columns they share first.
 constexpr int kSecond = 224;
+// Sharing out takes about 0.27 us for each block that a CTA has less to do and adds up to 8 us (the
+// clearing, the parts, the join), so it pays from 24 blocks on: one group of 8 rows, 7168 x 4096, 32 tiles, 44
+// blocks less: 17.8 us against 19.4; 14336 x 4096, 88 less: 21 against 34.6; 64 rows of four groups, 4096 x
+// 512, 28 less: 11.1 against 13.2; 48 rows of 16 groups, 7168 x 4096, 480 tiles or 24 more than three
+// rounds, 47 less: 76.5 against 82; 20 rows of 64 groups, 7168 x 2048, 18 less: 47.4 against 45.6; 100
+// rows of eight groups, 2048 x 2048, 2 less: 17.3 against 11.3.
+constexpr int kWorthSharing = 24;
 
 struct TileParams {
   const uint32_t *p_scales, *q_scales;  // words
@@ -59,7 +66,7 @@ struct TileParams {
   int tile_q, stages;
   bool out_words;             // rows of out may be stored two 16-bit values at a time
   const int* offsets;         // rows (or blocks) of each group; null: one group
-  // Where tiles are few or uneven: the blocks of all tiles are shared out evenly, so that a CTA
+  // Where tiles are few: the blocks of those beyond whole rounds are shared out evenly, so that a CTA
   // begins and ends inside tiles.  Its sums of a part of a tile go to `parts` (two a CTA, [column][128
   // rows]), and whichever warp comes last to its share of a tile, by `arrivals` (eight a tile, zero
   // at the start), adds the parts in their order.  Null: whole tiles.
@@ -96,22 +103,23 @@ struct Walk {
   unsigned t;
   int g = 0;
   const unsigned p_tiles;
-  unsigned begin = 0, end = 0;  // this CTA's blocks
+  // Shared out: the first tiles, those beyond whole rounds of all the CTAs, where that is worth it.
+  unsigned begin = 0, end = 0;  // this CTA's blocks of them
   int phase = 0;
-  unsigned whole = 0;           // tiles that have blocks
-  unsigned zeros = 0;           // tiles without blocks walked so far
   unsigned ctas = 1;            // that share them: each gets a word of scales, four blocks, at least
   unsigned each = 0, more = 0;  // blocks of a CTA; the first `more` get another one
   __device__ Walk(const TileParams& p_, const Shared& s_)
       : p(p_), s(s_), t(blockIdx.x / G), p_tiles((p_.p_rows + kTileP * G - 1) / (kTileP * G)) {
     if (p.parts) {
-      whole = s.tiles[p.groups];
-      const unsigned all = whole * p.blocks;
-      ctas = min(gridDim.x, max(all / 4, 1u));
-      each = all / ctas;
-      more = all - each * ctas;
-      t = begin = begin_of(blockIdx.x);
-      end = begin_of(blockIdx.x + 1);
+      const unsigned tiles = s.tiles[p.groups] % gridDim.x, all = tiles * p.blocks;  // (of tiles that have blocks)
+      if (all && (all + gridDim.x - 1) / gridDim.x + kWorthSharing <= static_cast<unsigned>(p.blocks)) {
+        ctas = min(gridDim.x, max(all / 4, 1u));
+        each = all / ctas;
+        more = all - each * ctas;
+        begin = begin_of(blockIdx.x);
+        end = begin_of(blockIdx.x + 1);
+        t += tiles;
+      }
     }
   }
   // The first block of a CTA, all tiles' blocks in a row, and the CTA that has a block.
@@ -126,7 +134,7 @@ struct Walk {
 
   __device__ bool next(Tile* out) {
     const int last = p.by_blocks ? p.groups : p.groups + 1;
-    if (p.parts) {
+    if (begin < end && phase < 2) {
       // The parts of tiles first -- of the one that the CTA ends inside, then of the one that it
       // begins inside -- so that they are joined while the whole tiles are under way.
       const unsigned blocks = p.blocks;
@@ -135,23 +143,8 @@ struct Walk {
         const unsigned from = end - end % blocks;
         if (from != end && from >= begin) return part(from, end, out);
       }
-      if (phase == 1) {
-        phase = 2;
-        if (begin % blocks && begin < end) {
-          t = min(end, begin - begin % blocks + blocks);
-          return part(begin, t, out);
-        }
-      }
-      if (t + blocks <= end) {
-        t += blocks;
-        return part(t - blocks, t, out);
-      }
-      // then the tiles without blocks, one after the other
-      const unsigned zero = whole + blockIdx.x + zeros * gridDim.x;
-      if (zero >= s.tiles[last]) return false;
-      ++zeros;
-      locate(zero, out);
-      return true;
+      phase = 2;
+      if (begin % blocks) return part(begin, min(end, begin - begin % blocks + blocks), out);
     }
     if (t >= s.tiles[last]) return false;
     locate(t, out);
@@ -290,6 +283,10 @@ template <typename Out>
 __device__ __forceinline__ void write_part(const TileParams& p, Shared& s, const Walk<1>& walk, const Tile& tile,
                                            uint32_t from, unsigned acc, int quarter, int half) {
   const int lane = threadIdx.x % 32, row = 32 * quarter + lane;
+  if (16 * half >= p.tile_q) {  // 16 columns: all the other warp's
+    if (lane == 0) mbar_arrive(&s.sum_empty[acc]);
+    return;
+  }
   const unsigned tile_begin = tile.index * p.blocks;
   const size_t part = static_cast<size_t>(kTileP) * p.tile_q;
   // a CTA's first place is for the tile that it begins inside, its second for one that it begins
@@ -706,34 +703,29 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
   return cudaLaunchKernelEx(&cfg, matmul_kernel<G>, t, p_map, q_map);
 }
 
-__global__ void __launch_bounds__(256) clear_kernel(uint4* to, size_t n) {
+__global__ void __launch_bounds__(1024) clear_kernel(uint4* to) {
   let_next_start();
   wait_for_previous();
-  for (size_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) to[i] = make_uint4(0, 0, 0, 0);
+  to[threadIdx.x] = make_uint4(0, 0, 0, 0);
 }
 
 // How a product is cut, from sizes alone (the groups' own sizes are on the device).
 struct Shape {
   int tile_q;
-  bool pair, share;  // share: the blocks of all tiles shared out evenly
+  bool pair, share;  // share: tiles may be shared out
 };
 
 // Groups of up to 64 rows on average are bound by the weights' bytes: one tile for all of a group's
-// rows where they are no more than half again the average.  With few such tiles of many blocks the
-// blocks are shared out among all the SMs.  That takes about 0.27 us for each block that a CTA has
-// less to do and adds 6 to 12 us of joining, so it pays from 32 blocks on: one group of 8 rows,
-// 7168 x 4096, 32 tiles, 44 blocks less: 16.2 us against 19.4; 14336 x 4096, 88 less: 20 against 34.6;
-// 64 rows of four groups, 4096 x 512, 28 less: 13.3 both; 100 rows of eight groups, 2048 x 2048, 2
-// less: 17.3 against 11.3.  Larger groups are bound by the products: the cut with the least time by
-// the measured cycles of a block, given its waves.
+// rows where they are no more than half again the average.  Sums of more than kWorthSharing blocks
+// may be shared out (the kernel knows how many tiles there are).  Larger groups are bound by the
+// products: the cut with the least time by the measured cycles of a block, given its waves.
 Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool by_blocks) {
   const size_t active = by_blocks ? groups : q_rows < groups ? q_rows : groups;
   const size_t average = by_blocks ? q_rows : ceil_div(q_rows, active);
   if (!by_blocks && average <= 64) {
     int t = 16;
     while (2 * static_cast<size_t>(t) < 3 * average) t *= 2;
-    const size_t shared = ceil_div(active * ceil_div(p_rows, kTileP) * blocks, kSms);
-    return {t, false, shared + 32 <= blocks};
+    return {t, false, blocks > kWorthSharing};
   }
   struct {
     Shape shape;
@@ -751,12 +743,9 @@ Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool 
   return *best;
 }
 
-size_t parts_bytes(const Shape& shape, size_t tiles) {
-  return shape.share ? 2 * kMaxCtas * kTileP * shape.tile_q * sizeof(float) + kWriters * tiles * sizeof(unsigned) : 0;
-}
-// Tiles of a row-grouped product, at most.
-size_t most_tiles(const Shape& shape, size_t q_rows, size_t groups, size_t p_rows) {
-  return ceil_div(p_rows, kTileP) * (q_rows / shape.tile_q + groups + 1);
+constexpr size_t kArrivals = kMaxCtas * kWriters;
+size_t parts_bytes(const Shape& shape) {
+  return shape.share ? 2 * kMaxCtas * kTileP * shape.tile_q * sizeof(float) + kArrivals * sizeof(unsigned) : 0;
 }
 
 cudaError_t launch_any(TileParams& t, const Shape& shape, const uint8_t* pv, size_t p_pitch, size_t p_matrices,
@@ -769,8 +758,7 @@ cudaError_t launch_any(TileParams& t, const Shape& shape, const uint8_t* pv, siz
 }  // namespace
 
 size_t matmul_workspace(size_t rows, int groups, size_t n, size_t k) {
-  const Shape shape = shape_of(rows, groups, n, ceil_div(k, kBlock), false);
-  return parts_bytes(shape, most_tiles(shape, rows, groups, n));
+  return parts_bytes(shape_of(rows, groups, n, ceil_div(k, kBlock), false));
 }
 
 cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t stream) {
@@ -793,12 +781,9 @@ cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t 
   t.out_pitch = p.out_pitch;
   const Shape shape = shape_of(p.rows, p.groups, p.n, blocks, false);
   if (shape.share) {
-    const size_t tiles = most_tiles(shape, p.rows, p.groups, p.n);
     t.arrivals = static_cast<unsigned*>(p.workspace);
-    t.parts = reinterpret_cast<float*>(t.arrivals + kWriters * tiles);
-    const size_t clear = tiles * kWriters / 4;
-    const cudaError_t err = launch(clear_kernel, static_cast<unsigned>(clear < 8192 ? ceil_div(clear, 256) : 32), 256,
-                                   0, stream, true, static_cast<uint4*>(p.workspace), clear);
+    t.parts = reinterpret_cast<float*>(t.arrivals + kArrivals);
+    const cudaError_t err = launch(clear_kernel, 1, kArrivals / 4, 0, stream, true, static_cast<uint4*>(p.workspace));
     if (err != cudaSuccess) return err;
   }
   return launch_any(t, shape, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, dev, stream);

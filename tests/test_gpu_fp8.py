@@ -242,7 +242,9 @@ def test_matmul_many_row_tiles_and_wide_scales():
     ((64,) * 3 + (0, 200), 2100, 520),  # groups above and below the average
     ((40,) * 3 + (0, 90), 300, 5000),   # blocks shared out, a group of two tiles, one of none
     ((3, 0, 1, 20), 257, 6000),         # the same with the smallest tiles
-    ((1,) * 20, 130, 20000),            # parts of several tiles in one CTA
+    ((1,) * 20, 130, 20000),            # parts of two tiles in one CTA
+    ((1,) * 40, 500, 5000),             # 8 tiles more than SMs, shared out, and whole ones
+    ((1,) * 30, 500, 5000),             # too many tiles to share out
     ((1,) * 300, 130, 140),           # more groups than CTAs
     ((256, 255, 257, 1, 511), 256, 128),  # tile ends on, before and after group ends, one block
     ((500,) * 6, 2050, 640),          # several bands of tiles, rows of out not whole 32-bit words apart
