@@ -164,22 +164,39 @@ __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
   }
 }
 
+// A warp's lanes on unaligned rows: each loads one aligned vector and takes the next one from the
+// lane above it, so that as many rows are in flight as on aligned ones (without weights 4999 x 6 x 2050, fp16:
+// 33 us, by two loads a lane 39; 16384 x 8 x 7167 351 and 445).  The last lane only loads.
+constexpr int kTaking = 31;
+__device__ __forceinline__ uint4 from_next_lane(const uint4& v) {
+  return make_uint4(__shfl_down_sync(~0u, v.x, 1), __shfl_down_sync(~0u, v.y, 1), __shfl_down_sync(~0u, v.z, 1),
+                    __shfl_down_sync(~0u, v.w, 1));
+}
+// The aligned vector that holds byte `from` of a row.
+__device__ __forceinline__ uint4 vector_at(const uint8_t* row, int from, int bytes, bool on) {
+  const int at = from - static_cast<int>(low4(row + from));
+  return load_if<16>(row + at, on && at > -16 && at < bytes);
+}
+
 // out[t] = sum over j of weights[t, j] rows[position[t, j]].  A thread takes Tokens tokens that follow
 // one another, with a share of each one's slots at a time: as many rows in flight however few slots a
 // token has.
+// (Nine CTAs to an SM: 16384 x 8 x 7167 with weights 381 us, without the bound on registers 394, ten 423.)
 template <typename T, bool Aligned, int Tokens, bool Weighted>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
+__global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 : 0) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
                                                                   const float* __restrict__ weights,
                                                                   uint8_t* __restrict__ out, size_t out_pitch,
                                                                   int bytes, unsigned parts, size_t tokens, int k,
                                                                   const int* __restrict__ position,
                                                                   const int* __restrict__ total, int* status) {
-  constexpr int N = 16 / sizeof(T), kBatch = Aligned ? 8 : 4, S = kBatch / Tokens;
+  // (four tokens of one slot on unaligned rows: 80 us for 16384 x 1 x 5851 by four, 108 by eight)
+  constexpr int N = 16 / sizeof(T), kBatch = !Aligned && Tokens == 4 ? 4 : 8, S = kBatch / Tokens;
   let_next_start();
   wait_for_previous();
   const size_t t0 = static_cast<size_t>(blockIdx.x / parts) * Tokens, slots = tokens * k;
-  const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
-  if (t0 >= tokens || 16 * c >= bytes + (Aligned ? 0 : 16)) return;
+  const int thread = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x), lane = threadIdx.x % 32;
+  const int c = Aligned ? thread : thread / 32 * kTaking + lane;
+  if (t0 >= tokens || (Aligned ? 16 * c >= bytes : 16 * (c - lane) >= bytes + 16)) return;  // (whole warps of unaligned rows)
   const int kept = *total;
   // vector c of each token's row of out: its first byte in the row
   int from[Tokens];
@@ -188,10 +205,10 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t*
     from[i] = 16 * c - (Aligned ? 0 : static_cast<int>(low4(out + (t0 + i) * out_pitch)));
   float acc[Tokens][N] = {};
   for (int j0 = 0; j0 < k; j0 += S) {
-    Loaded l[kBatch];
+    uint4 l[kBatch];
     float w[kBatch];
     int at[kBatch];
-    bool here[kBatch];
+    bool here[kBatch];  // (the same for all of a warp)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const size_t t = min(t0 + i / S, tokens - 1), s = t * k + min(j0 + i % S, k - 1);
@@ -201,13 +218,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t*
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       here[i] = j0 + i % S < k && t0 + i / S < tokens && in_range(at[i], slots, status) && at[i] < kept;
-      l[i] = fetch16<Aligned>(rows + at[i] * rows_pitch, from[i / S], bytes, here[i]);
+      l[i] = vector_at(rows + at[i] * rows_pitch, from[i / S], bytes, here[i]);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (!here[i]) continue;
       Pack<T, 16> v;
-      v.raw = settle<Aligned>(l[i], rows + at[i] * rows_pitch, from[i / S]);
+      v.raw = Aligned ? l[i] : shift_bytes(l[i], from_next_lane(l[i]), low4(rows + at[i] * rows_pitch + from[i / S]));
 #pragma unroll
       for (int e = 0; e < N; ++e) acc[i / S][e] = fmaf(w[i], to_float(v.v[e]), acc[i / S][e]);
     }
@@ -217,7 +234,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint8_t*
     Pack<T, 16> o;
 #pragma unroll
     for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[i][e]);
-    if (t0 + i < tokens) put16<Aligned, sizeof(T)>(out + (t0 + i) * out_pitch, from[i], bytes, o.raw);
+    if (t0 + i < tokens && (Aligned || lane < kTaking)) put16<Aligned, sizeof(T)>(out + (t0 + i) * out_pitch, from[i], bytes, o.raw);
   }
 }
 
@@ -350,7 +367,8 @@ cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitc
                            cudaStream_t stream) {
   const size_t b = type_bytes(s.type);
   const bool aligned = whole_vectors(b, s.hidden, {rows, out}, {rows_pitch, out_pitch});
-  const Cut cut = cut_row(row_vectors(s.hidden * b, aligned), kCombineThreads);
+  const size_t vecs = row_vectors(s.hidden * b, aligned);
+  const Cut cut = cut_row(aligned ? vecs : (vecs + kTaking - 1) / kTaking * 32, kCombineThreads);
   const auto go = [&](auto type, auto a, auto tokens) {
     return launch(weights ? combine_kernel<decltype(type), a(), tokens(), true>
                           : combine_kernel<decltype(type), a(), tokens(), false>,
