@@ -78,42 +78,29 @@ __device__ __forceinline__ unsigned short load_if<2>(const void* p, bool on) {
 // comes from the L1): loads stay as wide as on aligned rows.  An aligned vector is only touched
 // when it holds a byte of the row.
 
-// Bytes s .. s + 15 of a and b, 0 <= s < 16, a multiple of two.  (s is the same for a row's lanes: a
-// branch on the word costs less than selecting among them.)
+// Bytes s .. s + 15 of a and b, 0 <= s < 16, a multiple of two.  s is the same for a row's lanes, so a
+// branch on the word costs less than selecting among them, except where a kernel has many of them and
+// their code no longer fits the caches.  (Dispatch of 16384 x 8 x 7167: 328 us by branches, 374 by
+// selection; combine's gradient, which shifts twice for each slot: 864 and 797.)
 __device__ __forceinline__ uint4 shift_words(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4,
                                              unsigned s) {
   const unsigned bits = (s & 2) * 8;
   return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits), __funnelshift_r(w2, w3, bits),
                     __funnelshift_r(w3, w4, bits));
 }
+template <bool Select = false>
 __device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, unsigned s) {
+  if (Select) {
+    const bool h = s & 8, q = s & 4;
+    const uint32_t w0 = h ? a.z : a.x, w1 = h ? a.w : a.y, w2 = h ? b.x : a.z, w3 = h ? b.y : a.w,
+                   w4 = h ? b.z : b.x, w5 = h ? b.w : b.y;
+    return shift_words(q ? w1 : w0, q ? w2 : w1, q ? w3 : w2, q ? w4 : w3, q ? w5 : w4, s);
+  }
   if (s < 8) return s < 4 ? shift_words(a.x, a.y, a.z, a.w, b.x, s) : shift_words(a.y, a.z, a.w, b.x, b.y, s);
   return s < 12 ? shift_words(a.z, a.w, b.x, b.y, b.z, s) : shift_words(a.w, b.x, b.y, b.z, b.w, s);
 }
 
 __device__ __forceinline__ unsigned low4(const void* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u; }
-
-// What holds bytes from .. from + 15 of a row of `bytes` bytes (from may lie outside it).
-struct Loaded {
-  uint4 a, b;
-};
-template <bool Aligned>
-__device__ __forceinline__ Loaded fetch16(const uint8_t* row, int from, int bytes, bool on) {
-  Loaded l;
-  if (Aligned) {
-    l.a = load_if<16>(row + from, on && from < bytes);
-  } else {
-    const unsigned s = low4(row + from);
-    const int at = from - static_cast<int>(s);  // of the first vector, from the row's start
-    l.a = load_if<16>(row + at, on && at > -16 && at < bytes);
-    l.b = load_if<16>(row + at + 16, on && s && at > -32 && at + 16 < bytes);
-  }
-  return l;
-}
-template <bool Aligned>
-__device__ __forceinline__ uint4 settle(const Loaded& l, const uint8_t* row, int from) {
-  return Aligned ? l.a : shift_bytes(l.a, l.b, low4(row + from));
-}
 
 // Stores bytes from .. from + 15 of a row, an aligned vector, as far as they lie in it; E: bytes of a value.
 template <bool Aligned, int E>

@@ -40,7 +40,7 @@ size_t row_vectors(size_t bytes, bool aligned) { return (bytes + 15) / 16 + (ali
 
 // 16 bytes of a token's row, vector c of it, as a thread holds them to store them in rows that start
 // elsewhere: a vector of such a row holds bytes of this vector and of the one before.
-template <bool Aligned, int E>
+template <bool Aligned, int E, bool Select = false>
 struct Held {
   uint4 before, here;
   __device__ __forceinline__ void load(const uint8_t* row, int c, int bytes) {
@@ -55,14 +55,14 @@ struct Held {
       const int at = 16 * (c + i - 1) - static_cast<int>(s);
       v[i] = load_if<16>(row + at, at > -16 && at < bytes && (i < 2 || s));
     }
-    before = shift_bytes(v[0], v[1], s);
-    here = shift_bytes(v[1], v[2], s);
+    before = shift_bytes<Select>(v[0], v[1], s);
+    here = shift_bytes<Select>(v[1], v[2], s);
   }
   // The bytes that lie in vector c of a row at `row`, and where they start in the row.
   __device__ __forceinline__ uint4 for_row(const uint8_t* row, int c, int* from) const {
     const unsigned s = Aligned ? 0 : low4(row);
     *from = 16 * c - static_cast<int>(s);
-    return s ? shift_bytes(before, here, 16 - s) : here;
+    return s ? shift_bytes<Select>(before, here, 16 - s) : here;
   }
   __device__ __forceinline__ void store(uint8_t* row, int c, int bytes, bool zeros) const {
     int from;
@@ -238,6 +238,28 @@ __global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 :
   }
 }
 
+// What holds bytes from .. from + 15 of a row of `bytes` bytes (from may lie outside it).
+struct Loaded {
+  uint4 a, b;
+};
+template <bool Aligned>
+__device__ __forceinline__ Loaded fetch16(const uint8_t* row, int from, int bytes, bool on) {
+  Loaded l;
+  if (Aligned) {
+    l.a = load_if<16>(row + from, on && from < bytes);
+  } else {
+    const unsigned s = low4(row + from);
+    const int at = from - static_cast<int>(s);  // of the first vector, from the row's start
+    l.a = load_if<16>(row + at, on && at > -16 && at < bytes);
+    l.b = load_if<16>(row + at + 16, on && s && at > -32 && at + 16 < bytes);
+  }
+  return l;
+}
+template <bool Aligned>
+__device__ __forceinline__ uint4 settle(const Loaded& l, const uint8_t* row, int from) {
+  return Aligned ? l.a : shift_bytes<true>(l.a, l.b, low4(row + from));
+}
+
 // d_rows[position[t, j]] = weights[t, j] d_out[t], d_weights[t, j] = <d_out[t], rows[...]>.  One
 // CTA a token: each thread sums its vectors' products, then lanes, then warps, in a fixed order.
 template <typename T, bool Aligned, int Batch>
@@ -266,7 +288,7 @@ __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
       dot[i] = 0.f;
     }
     for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-      Held<Aligned, sizeof(T)> held;
+      Held<Aligned, sizeof(T), true> held;
       held.load(d_out + t * d_out_pitch, c, bytes);
       Loaded l[Batch];
 #pragma unroll
@@ -406,8 +428,8 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
                   offsets + s.experts, status);
   };
   // Slots taken together: no more than there are, which leaves room for more CTAs, and two where
-  // every row's vector takes two registers' worth of loads (4999 x 6 x 2050: 72 us by twos, 99 by
-  // fours, 88 by eights).
+  // every row's vector takes two registers' worth of loads and a shift (4999 x 6 x 2050: 70 us by
+  // twos, 84 by fours, 88 by eights).
   return by_type(s.type, aligned, [&](auto type, auto a) {
     if (s.k == 1) return go(type, a, std::integral_constant<int, 1>{});
     if (s.k == 2 || !a()) return go(type, a, std::integral_constant<int, 2>{});
