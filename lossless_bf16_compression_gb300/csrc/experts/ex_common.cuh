@@ -80,8 +80,9 @@ __device__ __forceinline__ unsigned short load_if<2>(const void* p, bool on) {
 
 // Bytes s .. s + 15 of a and b, 0 <= s < 16, a multiple of two.  s is the same for a row's lanes, so a
 // branch on the word costs less than selecting among them, except where a kernel has many of them and
-// their code no longer fits the caches.  (Dispatch of 16384 x 8 x 7167: 328 us by branches, 374 by
-// selection; combine's gradient, which shifts twice for each slot: 864 and 797.)
+// their code no longer fits the caches, or where lanes of a warp are in several rows.  (Dispatch of
+// 16384 x 8 x 7167: 328 us by branches, 374 by selection, quantized rows of 16384 x 7167 72 and 76; combine's
+// gradient, which shifts twice for each slot: 864 and 797, quantized columns 106 and 94.)
 __device__ __forceinline__ uint4 shift_words(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4,
                                              unsigned s) {
   const unsigned bits = (s & 2) * 8;

@@ -21,7 +21,7 @@ union Raw8 {
 // The loads of eight values, `left` of them in the row (none where left <= 0), and the values, zeros
 // past them.  Vec: rows start on 16-byte boundaries; otherwise the values lie in one aligned vector
 // more.  All of a thread's loads are issued before the first value is made.
-template <typename T, bool Vec>
+template <typename T, bool Vec, bool Select = false>
 struct Fetch8 {
   static constexpr int kVectors = sizeof(T) / 2 + (Vec ? 0 : 1);
   uint4 q[kVectors];
@@ -39,7 +39,7 @@ struct Fetch8 {
     } else {
       const unsigned s = low4(at);
 #pragma unroll
-      for (int i = 0; i + 1 < kVectors; ++i) r.q[i] = shift_bytes(q[i], q[i + 1], s);
+      for (int i = 0; i + 1 < kVectors; ++i) r.q[i] = shift_bytes<Select>(q[i], q[i + 1], s);
     }
     if (left < 8)
 #pragma unroll
@@ -255,7 +255,7 @@ struct TileShared {
 // Eight values of each of eight rows (`rows` of them real), `left` of a row's in it.
 template <typename T, bool Vec>
 __device__ __forceinline__ void load_tile(const T* at, size_t pitch, int rows, int left, Raw8<T> (&raw)[8]) {
-  Fetch8<T, Vec> in[8];
+  Fetch8<T, Vec, true> in[8];  // (a warp's lanes are in two rows, which start differently)
 #pragma unroll
   for (int i = 0; i < 8; ++i) in[i].load(at + i * pitch, i < rows ? left : 0);
 #pragma unroll
@@ -278,7 +278,7 @@ __device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
 // CTAs the counting costs more than the launch (8192 x 4096, 2304 CTAs: 26.6 us with the launch,
 // 24.6 without; 32768 x 7168, 15,232 CTAs: 119.5 and 123).
 // (What bounds the kernel is HBM: 5.9 TB/s at the larger size; rows that start anywhere, with a vector more
-// to load for each, 111 us against 72 for 16384 x 7167 and 7168.)
+// to load for each, 94 us against 70 for 16384 x 7167 and 7168.)
 constexpr int kInlineGroups = 256;
 constexpr size_t kInlineCtas = 4096;
 template <typename T, bool Vec, int Fmt, bool Inline>
