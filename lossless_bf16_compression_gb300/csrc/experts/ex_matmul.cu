@@ -718,7 +718,10 @@ struct Shape {
 // Groups of up to 64 rows on average are bound by the weights' bytes: one tile for all of a group's
 // rows where they are no more than half again the average.  Sums of more than kWorthSharing blocks
 // may be shared out (the kernel knows how many tiles there are).  Larger groups are bound by the
-// products: the cut with the least time by the measured cycles of a block, given its waves.
+// products: the cut with the least time by the measured cycles of a block, given its waves, and of
+// the last tile's writing, which decides where all tiles are under way at once (669 rows of four
+// groups, 935 x 166: 10.6 us with tiles of 128 x 128, 12.6 with pairs; 4096 rows of four groups, 4096 x 4096:
+// 51 with pairs, 58 with 128 x 256, 91 with 128 x 128).
 Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool by_blocks) {
   const size_t active = by_blocks ? groups : q_rows < groups ? q_rows : groups;
   const size_t average = by_blocks ? q_rows : ceil_div(q_rows, active);
@@ -727,17 +730,18 @@ Shape shape_of(size_t q_rows, size_t groups, size_t p_rows, size_t blocks, bool 
     while (2 * static_cast<size_t>(t) < 3 * average) t *= 2;
     return {t, false, blocks > kWorthSharing};
   }
+  const double sum = by_blocks ? std::fmax(1.0, static_cast<double>(blocks) / groups) : static_cast<double>(blocks);
   struct {
     Shape shape;
-    double cycles;  // of a block of a tile
-  } const cuts[] = {{{256, true, false}, 545}, {{256, false, false}, 722}, {{128, false, false}, 563}};
+    double cycles, end;  // of a block of a tile, and of writing the last one
+  } const cuts[] = {{{256, true, false}, 545, 5300}, {{256, false, false}, 722, 4300}, {{128, false, false}, 563, 2200}};
   const Shape* best = nullptr;
   double least = 0;
   for (const auto& c : cuts) {
     const size_t g = c.shape.pair ? 2 : 1;
     const double tiles = static_cast<double>(active) * ceil_div(average, c.shape.tile_q) * ceil_div(p_rows, kTileP * g);
     const double waves = std::ceil(tiles / (kSms / g));
-    const double time = waves * c.cycles;
+    const double time = waves * sum * c.cycles + c.end;
     if (best == nullptr || time < least) best = &c.shape, least = time;
   }
   return *best;
