@@ -273,25 +273,38 @@ __device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
   return x % 2 ? make_uint4(v.z, v.w, v.x, v.y) : v;
 }
 
+// 128 rows x 64 columns a CTA, thread (row group tid / 8, column group tid % 8) with 8 x 8 values.  Bound by HBM as
+// long as enough loads are in flight while other CTAs turn their tiles: 32768 x 7168, bf16, takes 115 us (6.2
+// TB/s) with nine CTAs to an SM, 119 with eight, 123 with seven, 121 with ten, which spill, and 123 with CTAs of 128
+// columns; rows that start anywhere, with a vector more to load for each, 90 us for 16384 x 7167 with
+// six (aligned 63).
+//
 // Inline: every CTA counts the blocks before its own, one group a thread, and the first writes
 // block_offsets, which saves a launch; otherwise they come from block_offsets_kernel.  With many
-// CTAs the counting costs more than the launch (8192 x 4096, 2304 CTAs: 26.6 us with the launch,
-// 24.6 without; 32768 x 7168, 15,232 CTAs: 119.5 and 123).
-// (What bounds the kernel is HBM: 5.9 TB/s at the larger size; rows that start anywhere, with a vector more
-// to load for each, 94 us against 70 for 16384 x 7167 and 7168.)
-constexpr int kInlineGroups = 256;
-constexpr size_t kInlineCtas = 4096;
+// CTAs the counting costs more than the launch (8192 x 4096, 4608 CTAs: 26.6 us with the launch,
+// 24.6 without; 32768 x 7168, 30,464 CTAs: 119.5 and 123).
+constexpr int kColumns = 64;  // of a CTA's tile
+constexpr int kColumnThreads = 128;
+constexpr int kInlineGroups = kColumnThreads;
+constexpr size_t kInlineCtas = 8192;
+
+// The tile's transpose by way of shared memory, as for TileShared.
+struct ColumnShared {
+  alignas(16) uint2 turned[kColumns * 16];   // [column][unit of 8 rows], the unit at place unit ^ 2 (column / 8)
+  alignas(16) uint32_t amax[16][kColumns];   // 16-bit types: two columns a word
+  float inverse[kColumns];
+};
 template <typename T, bool Vec, int Fmt, bool Inline>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
+__global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4) : Vec ? 9 : 6) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
                                                                int cols, int groups, const int* __restrict__ offsets,
                                                                int capacity, uint8_t* __restrict__ values,
                                                                uint8_t* __restrict__ scales,
                                                                int* __restrict__ block_offsets, int* status) {
-  __shared__ TileShared s;
+  __shared__ ColumnShared s;
   __shared__ int first, last;  // this block's rows
-  __shared__ int sums[8];
-  const int b = blockIdx.x, tid = threadIdx.x, cg = tid % 16, rg = tid / 16;
-  const int c = blockIdx.y * kBlock + cg * 8;
+  __shared__ int sums[kColumnThreads / 32];
+  const int b = blockIdx.x, tid = threadIdx.x, cg = tid % 8, rg = tid / 8;
+  const int c = blockIdx.y * kColumns + cg * 8;
   if (tid == 0) first = last = 0;
   let_next_start();
   wait_for_previous();
@@ -311,7 +324,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantiz
     }
   } else {
     __syncthreads();
-    for (int g = tid; g < groups; g += 256) {
+    for (int g = tid; g < groups; g += kColumnThreads) {
       const int b0 = block_offsets[g];
       if (b0 <= b && b < block_offsets[g + 1]) take(g, b0);  // (a group with bad starts has no blocks)
     }
@@ -328,14 +341,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantiz
   for (int w = 0; w < words; w += 4)
     *reinterpret_cast<uint4*>(&s.amax[rg][cg * words + w]) = make_uint4(most[w], most[w + 1], most[w + 2], most[w + 3]);
   __syncthreads();
-  if (tid < kBlock) {
+  if (tid < kColumns) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       m = max(m, sizeof(T) == 4 ? s.amax[i][tid] : reinterpret_cast<const unsigned short*>(s.amax[i])[tid]);
     const int e = block_exponent(Bits<T>::fp32(m), Fmt);
     s.inverse[tid] = inverse_scale(e);
-    const size_t row = static_cast<size_t>(blockIdx.y) * kBlock + tid;
+    const size_t row = static_cast<size_t>(blockIdx.y) * kColumns + tid;
     if (row < static_cast<size_t>(cols)) {
       scales[scale_at(row, b, cols)] = static_cast<uint8_t>(e + 127);
       if (b == capacity - 1)
@@ -344,14 +357,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantiz
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) put_column(s, cg * 8 + j, rg, round_column<Fmt>(raw, j, s.inverse[cg * 8 + j], odd));
+  for (int j = 0; j < 8; ++j)
+    s.turned[(cg * 8 + j) * 16 + (rg ^ 2 * cg)] = round_column<Fmt>(raw, j, s.inverse[cg * 8 + j], odd);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int column = i * 32 + tid / 8, part = tid % 8;
-    const size_t row = static_cast<size_t>(blockIdx.y) * kBlock + column;
+    const int column = i * 16 + tid / 8, part = tid % 8;
+    const size_t row = static_cast<size_t>(blockIdx.y) * kColumns + column;
     if (row < static_cast<size_t>(cols))
-      reinterpret_cast<uint4*>(values + (row * capacity + b) * kBlock)[part] = get_column(s, column, part);
+      reinterpret_cast<uint4*>(values + (row * capacity + b) * kBlock)[part] =
+          reinterpret_cast<const uint4*>(s.turned)[column * 8 + (part ^ (column / 8))];
   }
 }
 
@@ -464,18 +479,18 @@ cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_
                                     int* status, cudaStream_t stream) {
   const size_t capacity = column_blocks(rows, groups);
   const bool inline_groups =
-      capacity > 0 && groups <= kInlineGroups && capacity * ceil_div(cols, kBlock) <= kInlineCtas;
+      capacity > 0 && groups <= kInlineGroups && capacity * ceil_div(cols, kColumns) <= kInlineCtas;
   if (!inline_groups) {
     const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, true, offsets, static_cast<int>(rows),
                                    groups, block_offsets, status);
     if (err != cudaSuccess || capacity == 0) return err;
   }
-  const dim3 grid(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, kBlock)));
+  const dim3 grid(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, kColumns)));
   return variant(type, vector_rows(x, pitch, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
     return launch(inline_groups ? quantize_columns_kernel<T, vec(), f(), true>
                                 : quantize_columns_kernel<T, vec(), f(), false>,
-                  grid, 256, 0, stream, true, static_cast<const T*>(x), pitch, static_cast<int>(rows),
+                  grid, kColumnThreads, 0, stream, true, static_cast<const T*>(x), pitch, static_cast<int>(rows),
                   static_cast<int>(cols), groups, offsets, static_cast<int>(capacity), values, scales, block_offsets,
                   status);
   });
