@@ -1,7 +1,6 @@
-"""What the tensor-level calls of ``moe`` and ``fp8`` share: argument checks, streams, the library's calls."""
+"""What the tensor-level calls of ``moe`` and ``fp8`` share: the native calls, streams, the C entry points."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -31,54 +30,27 @@ TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MAX_EXPERTS = 1024
 MAX_K = 64
 
-_fns: dict = {}
 
 
 def fn(name):
-    """An entry point of the library with its argument types set; raises when the library is not built."""
-    f = _fns.get(name)
-    if f is None:
-        handle = binding.lib()
-        f = getattr(handle, name)
-        f.restype, f.argtypes = SIGNATURES[name]
-        _fns[name] = f
+    """An entry point of the library with its argument types set, for callers that have addresses instead of
+    tensors; raises when the library is not built."""
+    f = getattr(binding.lib(), name)
+    f.restype, f.argtypes = SIGNATURES[name]
     return f
 
 
-def call(name, *args):
-    rc = (_fns.get(name) or fn(name))(*args)
-    if rc != binding.ZC_OK:
-        raise binding.ZcError(rc, name)
+def _native():
+    try:
+        from . import _experts
+    except ImportError as e:
+        raise ImportError("the extension module _experts is missing or was built for another torch: build it first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    _experts.bind(binding.lib()._handle, binding.ZcError)
+    return _experts
 
 
-def check(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def on_device(name, t, device, dtypes=None, dim=None):
-    """Checks for a CUDA tensor of device number `device` (None: the current one), of one of `dtypes`, with `dim`
-    dimensions; returns the device number."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {', '.join(str(d) for d in dtypes)}")
-    if dim is not None and t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
-    if device is None:
-        device = torch._C._cuda_getDevice()
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return device
-
-
-def rows_of(t):
-    """(tensor, pitch): `t` as rows of contiguous values a pitch apart (copied when it is not laid out so)."""
-    rows, cols = t.shape
-    pitch, step = t.stride()
-    if (cols > 1 and step != 1) or (rows > 1 and pitch < cols):
-        t, pitch = t.contiguous(), cols
-    return t, (pitch if rows > 1 else cols)
+native = _native()  # the calls on tensors: checks, outputs, launch, on the current device and stream
 
 
 def on(stream, used, f, *args):
@@ -87,10 +59,7 @@ def on(stream, used, f, *args):
     if stream is None:
         return f(*args)
     for t in used:
-        if t is not None:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
     with torch.cuda.stream(stream):
         return f(*args)
-
-
-current = torch._C._cuda_getCurrentRawStream  # (device) -> the handle of its current stream

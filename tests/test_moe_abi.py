@@ -130,3 +130,18 @@ def test_no_gpu_fails_loudly():
         moe.sort(torch.zeros((2, 2), dtype=torch.int32), 4)
     with pytest.raises(TypeError):
         fp8.quantize(torch.zeros((2, 2)))
+
+
+def test_native_calls_refuse():
+    """The calls on tensors, with arguments that never reach the library."""
+    torch = pytest.importorskip("torch")
+    native, x = _tensors.native, torch.zeros((4, 8))
+    for name, args in (("sort", ()), ("sort", (x.int(), 4, 1)), ("sort", (x.int(), 4)), ("sort", ([[0]], 4)), ("sort", (None, 4)),
+                       ("dispatch", (x, x.int(), 4)), ("combine", (x, None, x.int(), x.int())), ("combine", (x,)),
+                       ("combine_grad", (x,) * 5), ("quantize", (x, 0)), ("quantize", ("x", 0)), ("quantize_columns", (x, None, 0)),
+                       ("quantize_weight", (x, 0, True)), ("scale_values", (x.byte(),)), ("values", (3, 0, 8)),
+                       ("matmul", (x.byte(), x.byte(), 0, 8) * 2 + (None, 0)), ("weight_grad", (x.byte(),)), ("bind", ())):
+        with pytest.raises(TypeError):
+            getattr(native, name)(*args)
+    q = native.values(torch.arange(8, dtype=torch.uint8).view(2, 4), 0, 3)
+    assert q.dtype == torch.float8_e4m3fn and q.shape == (2, 3) and q.stride() == (4, 1)
