@@ -31,7 +31,6 @@ MAX_EXPERTS = 1024
 MAX_K = 64
 
 
-
 def fn(name):
     """An entry point of the library with its argument types set, for callers that have addresses instead of
     tensors; raises when the library is not built."""
