@@ -13,6 +13,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+#include <optional>
+#include <string>
+
 #include "zc_moe.h"
 
 namespace {
@@ -46,6 +50,13 @@ constexpr unsigned bit(at::ScalarType t) { return 1u << static_cast<unsigned>(t)
 constexpr unsigned kRows = bit(at::kBFloat16) | bit(at::kHalf) | bit(at::kFloat), kFloats = bit(at::kFloat),
                    kInts = bit(at::kInt), kIds = bit(at::kInt) | bit(at::kLong), kBytes = bit(at::kByte);
 
+std::string names(unsigned types) {
+  std::string s;
+  for (unsigned i = 0; i < 32; ++i)
+    if (types >> i & 1) s += (s.empty() ? "" : ", ") + std::string(c10::toString(static_cast<at::ScalarType>(i)));
+  return s;
+}
+
 // The current device, asked for after the first argument turns out to be on a GPU.
 class Device {
   mutable c10::DeviceIndex n_ = -1;
@@ -60,7 +71,8 @@ const Tensor& tensor(PyObject* o, const char* name, const Device& device, unsign
   const Tensor& t = THPVariable_Unpack(o);
   TORCH_CHECK_TYPE(t.is_cuda(), name, " must be a CUDA tensor");
   const auto type = static_cast<unsigned>(t.scalar_type());
-  TORCH_CHECK_TYPE(type < 32 && (types >> type & 1), name, " has dtype ", t.scalar_type());
+  TORCH_CHECK_TYPE(type < 32 && (types >> type & 1), name, " has dtype ", t.scalar_type(), ", expected one of ",
+                   names(types));
   TORCH_CHECK_VALUE(dim == 0 || t.dim() == dim, name, " must have ", dim, " dimensions, got ", t.sizes());
   TORCH_CHECK_VALUE(t.get_device() == device.number(), name, " is on ", t.device(), ", not on the current device");
   return t;
