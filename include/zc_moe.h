@@ -100,8 +100,8 @@ int zc_fp8_scale_values(const void* scales, size_t words, float* out, cudaStream
  * is the transpose, `cols` rows of 128 * capacity values, capacity = zc_fp8_column_blocks(rows,
  * groups).  Group g (rows offsets[g] .. offsets[g + 1] - 1 of x) starts at block
  * block_offsets[g] and fills ceil of its rows / 128 blocks, the last one padded with zeros
- * (offsets start at 0 and do not decrease); the blocks from block_offsets[groups] on are zeros with scale 1.  offsets null: one group of all
- * the rows.  values: cols x 128 capacity bytes; scales: ceil(capacity / 4) x cols x 4;
+ * (offsets start at 0 and do not decrease); the blocks from block_offsets[groups] on are zeros with
+ * scale 1.  offsets null: one group of all the rows.  values: cols x 128 capacity bytes; scales: ceil(capacity / 4) x cols x 4;
  * block_offsets: groups + 1 int32. */
 size_t zc_fp8_column_blocks(size_t rows, int groups);
 int zc_fp8_quantize_columns(const void* x, size_t pitch, int type, size_t rows, size_t cols, int groups,

@@ -3,7 +3,8 @@
 ``binding`` exposes the C ABI of ``libzc.so`` (``zc_compress``, ``zc_decompress``, ...);
 ``build`` compiles it for sm_103a; ``workloads`` holds the seeded synthetic inputs.  ``moe`` and
 ``fp8`` hold what stands on either side of a compressed expert exchange: tokens sorted by expert
-and back with their gradients, and the experts' products in 8-bit blocks.  The library is loaded on first use and a call fails loudly when it has not been built.
+and back with their gradients, and the experts' products in 8-bit blocks.  The library is loaded
+on first use and a call fails loudly when it has not been built.
 """
 from .binding import (  # noqa: F401
     ZC_BASE_AUTO,

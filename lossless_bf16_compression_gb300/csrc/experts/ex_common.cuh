@@ -101,7 +101,9 @@ __device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, uns
   return s < 12 ? shift_words(a.z, a.w, b.x, b.y, b.z, s) : shift_words(a.w, b.x, b.y, b.z, b.w, s);
 }
 
-__device__ __forceinline__ unsigned low4(const void* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u; }
+__device__ __forceinline__ unsigned low4(const void* p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u;
+}
 
 // Stores bytes from .. from + 15 of a row, an aligned vector, as far as they lie in it; E: bytes of a value.
 template <bool Aligned, int E>

@@ -59,7 +59,9 @@ struct Bits<__nv_bfloat16> {
 template <>
 struct Bits<__half> {
   static constexpr uint32_t kInf = 0x7C00;
-  static __device__ uint32_t fp32(uint32_t m) { return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m)))); }
+  static __device__ uint32_t fp32(uint32_t m) {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+  }
 };
 template <>
 struct Bits<float> {
@@ -295,11 +297,10 @@ struct ColumnShared {
   float inverse[kColumns];
 };
 template <typename T, bool Vec, int Fmt, bool Inline>
-__global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4) : Vec ? 9 : 6) quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows,
-                                                               int cols, int groups, const int* __restrict__ offsets,
-                                                               int capacity, uint8_t* __restrict__ values,
-                                                               uint8_t* __restrict__ scales,
-                                                               int* __restrict__ block_offsets, int* status) {
+__global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4) : Vec ? 9 : 6)
+    quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows, int cols, int groups,
+                            const int* __restrict__ offsets, int capacity, uint8_t* __restrict__ values,
+                            uint8_t* __restrict__ scales, int* __restrict__ block_offsets, int* status) {
   __shared__ ColumnShared s;
   __shared__ int first, last;  // this block's rows
   __shared__ int sums[kColumnThreads / 32];
@@ -373,11 +374,10 @@ __global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4)
 // One scale for the tile; its rows are written from registers, its transpose through shared memory
 // (16 matrices of 4096 x 7168, bf16, both written: 297 us, 6.3 TB/s).
 template <typename T, bool Vec, int Fmt>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3) quantize_weight_kernel(const T* __restrict__ w, int rows, int cols,
-                                                              uint8_t* __restrict__ values,
-                                                              uint8_t* __restrict__ scales,
-                                                              uint8_t* __restrict__ values_t,
-                                                              uint8_t* __restrict__ scales_t) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3)
+    quantize_weight_kernel(const T* __restrict__ w, int rows, int cols, uint8_t* __restrict__ values,
+                           uint8_t* __restrict__ scales, uint8_t* __restrict__ values_t,
+                           uint8_t* __restrict__ scales_t) {
   __shared__ TileShared s;
   let_next_start();
   wait_for_previous();

@@ -183,12 +183,10 @@ __device__ __forceinline__ uint4 vector_at(const uint8_t* row, int from, int byt
 // token has.
 // (Nine CTAs to an SM: 16384 x 8 x 7167 with weights 381 us, without the bound on registers 394, ten 423.)
 template <typename T, bool Aligned, int Tokens, bool Weighted>
-__global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 : 0) combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch,
-                                                                  const float* __restrict__ weights,
-                                                                  uint8_t* __restrict__ out, size_t out_pitch,
-                                                                  int bytes, unsigned parts, size_t tokens, int k,
-                                                                  const int* __restrict__ position,
-                                                                  const int* __restrict__ total, int* status) {
+__global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 : 0)
+    combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch, const float* __restrict__ weights,
+                   uint8_t* __restrict__ out, size_t out_pitch, int bytes, unsigned parts, size_t tokens, int k,
+                   const int* __restrict__ position, const int* __restrict__ total, int* status) {
   // (four tokens of one slot on unaligned rows: 80 us for 16384 x 1 x 5851 by four, 108 by eight)
   constexpr int N = 16 / sizeof(T), kBatch = !Aligned && Tokens == 4 ? 4 : 8, S = kBatch / Tokens;
   let_next_start();
@@ -196,7 +194,8 @@ __global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 :
   const size_t t0 = static_cast<size_t>(blockIdx.x / parts) * Tokens, slots = tokens * k;
   const int thread = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x), lane = threadIdx.x % 32;
   const int c = Aligned ? thread : thread / 32 * kTaking + lane;
-  if (t0 >= tokens || (Aligned ? 16 * c >= bytes : 16 * (c - lane) >= bytes + 16)) return;  // (whole warps of unaligned rows)
+  // (on unaligned rows only whole warps leave)
+  if (t0 >= tokens || (Aligned ? 16 * c >= bytes : 16 * (c - lane) >= bytes + 16)) return;
   const int kept = *total;
   // vector c of each token's row of out: its first byte in the row
   int from[Tokens];
@@ -234,7 +233,8 @@ __global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 :
     Pack<T, 16> o;
 #pragma unroll
     for (int e = 0; e < N; ++e) o.v[e] = from_float<T>(acc[i][e]);
-    if (t0 + i < tokens && (Aligned || lane < kTaking)) put16<Aligned, sizeof(T)>(out + (t0 + i) * out_pitch, from[i], bytes, o.raw);
+    if (t0 + i < tokens && (Aligned || lane < kTaking))
+      put16<Aligned, sizeof(T)>(out + (t0 + i) * out_pitch, from[i], bytes, o.raw);
   }
 }
 

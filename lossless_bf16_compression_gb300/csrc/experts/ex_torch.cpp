@@ -98,7 +98,8 @@ struct Rows {
   const void* data() const { return t.data_ptr(); }
   int type() const { return type_of(t.scalar_type()); }
 };
-Rows rows_of(PyObject* o, const char* name, const Device& device, int64_t rows = -1, int64_t cols = -1, unsigned types = kRows) {
+Rows rows_of(PyObject* o, const char* name, const Device& device, int64_t rows = -1, int64_t cols = -1,
+             unsigned types = kRows) {
   const Tensor& t = tensor(o, name, device, types, 2);
   TORCH_CHECK_VALUE((rows < 0 || t.size(0) == rows) && t.size(1) >= 1 && (cols < 0 || t.size(1) == cols), name,
                     " must be [", rows < 0 ? "rows" : std::to_string(rows), ", ",
