@@ -43,31 +43,14 @@ union Pack {
 };
 
 // A load that happens only where `on` is set, zeros elsewhere: a predicated instruction, not a
-// branch, so that a thread's loads go out together.  For memory no one writes during the kernel.
-template <int B>
-__device__ __forceinline__ typename Bytes<B>::type load_if(const void* p, bool on);
-template <>
-__device__ __forceinline__ uint4 load_if<16>(const void* p, bool on) {
+// branch, so that a thread's loads go out together.  Volatile, so that it stays behind
+// wait_for_previous, and not by the read-only path, which is for memory that no one writes while the
+// kernel is there: a kernel that starts early is there while the one before it writes.
+__device__ __forceinline__ uint4 load_if(const void* p, bool on) {
   uint4 v = make_uint4(0, 0, 0, 0);
-  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(p), "r"(static_cast<int>(on)));
-  return v;
-}
-template <>
-__device__ __forceinline__ uint32_t load_if<4>(const void* p, bool on) {
-  uint32_t v = 0;
-  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}"
-      : "+r"(v)
-      : "l"(p), "r"(static_cast<int>(on)));
-  return v;
-}
-template <>
-__device__ __forceinline__ unsigned short load_if<2>(const void* p, bool on) {
-  unsigned short v = 0;
-  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
-      : "+h"(v)
-      : "l"(p), "r"(static_cast<int>(on)));
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "l"(p), "r"(static_cast<int>(on)));
   return v;
 }
 
@@ -135,7 +118,14 @@ inline bool whole_vectors(size_t element, size_t row_values, std::initializer_li
 inline size_t type_bytes(int type) { return type == ZC_TYPE_FP32 ? 4 : 2; }
 
 // A launch; early: it may start while the kernel before it in the stream still runs (whoever
-// launched that one), so the kernel calls wait_for_previous before it touches memory.
+// launched that one), so the kernel calls wait_for_previous before it touches memory.  Two kernels
+// read before their wait what the kernel before them does not write: place_kernel the ids and
+// dispatch_kernel x.  They are only launched behind count_kernel and place_kernel, which let the next
+// kernel start after their own wait, when all that came earlier in the stream is done.
+//
+// Pointers to global memory are not __restrict__ in kernels that start early: the compiler may take
+// it that nothing but the kernel's own accesses touches such memory, the wait included, and load
+// before it.
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool early,
                    A... args) {
@@ -152,6 +142,7 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// (Clobbers memory: no access that the compiler knows of crosses it.)
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 

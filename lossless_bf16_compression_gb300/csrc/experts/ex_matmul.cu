@@ -255,7 +255,7 @@ __device__ void plan_tiles(const TileParams& p, Shared& s) {
 // The scale words of rows row0 + lane, + 32, + 64, + 96 (1 past the last row).
 __device__ __forceinline__ uint4 scale_words(const uint32_t* words, int row0, int rows) {
   const int r = row0 + static_cast<int>(threadIdx.x % 32);
-  const auto word = [&](int i) { return r + 32 * i < rows ? __ldg(words + r + 32 * i) : 0x7F7F7F7Fu; };
+  const auto word = [&](int i) { return r + 32 * i < rows ? words[r + 32 * i] : 0x7F7F7F7Fu; };
   return make_uint4(word(0), word(1), word(2), word(3));
 }
 

@@ -30,7 +30,7 @@ struct Fetch8 {
     const unsigned s = Vec ? 0 : low4(p);
     const int bytes = min(left, 8) * static_cast<int>(sizeof(T)) + static_cast<int>(s);
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) q[i] = load_if<16>(p - s + 16 * i, left > 0 && 16 * i < bytes);
+    for (int i = 0; i < kVectors; ++i) q[i] = load_if(p - s + 16 * i, left > 0 && 16 * i < bytes);
   }
   __device__ __forceinline__ void values(const T* at, int left, Raw8<T>& r) const {
     if constexpr (Vec) {
@@ -147,10 +147,8 @@ __device__ __forceinline__ uint2 round_column(const Raw8<T> (&r)[8], int j, floa
 // (R = 8, with the registers that takes: 138 us for 102 below).
 constexpr int kRowWarps = 4;  // (32768 x 7168, bf16: 102 us, 6.9 TB/s; 8 warps 108, 16 warps 117)
 template <typename T, bool Vec, int Fmt, int R>
-__global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __restrict__ x, size_t pitch, size_t rows,
-                                                                  int cols, unsigned words,
-                                                                  uint8_t* __restrict__ values,
-                                                                  uint32_t* __restrict__ scales) {
+__global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* x, size_t pitch, size_t rows, int cols,
+                                                                  unsigned words, uint8_t* values, uint32_t* scales) {
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x % 32;
@@ -193,8 +191,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_kernel(const T* __res
 }
 
 // The scales as fp32: 2^(byte - 127), by the bits; byte 0 is the subnormal 2^-127, 255 a NaN.
-__global__ void __launch_bounds__(256) scale_values_kernel(const uint32_t* __restrict__ scales, size_t words,
-                                                           float4* __restrict__ out) {
+__global__ void __launch_bounds__(256) scale_values_kernel(const uint32_t* scales, size_t words, float4* out) {
   let_next_start();
   wait_for_previous();
   const size_t i = blockIdx.x * size_t(256) + threadIdx.x;
@@ -231,8 +228,8 @@ __device__ __forceinline__ int sum_before(int n, int* sums) {
 }
 
 // block_offsets[g] = blocks of the groups before g, by one CTA of 1024 threads.
-__global__ void __launch_bounds__(1024) block_offsets_kernel(const int* __restrict__ offsets, int rows, int groups,
-                                                             int* __restrict__ block_offsets, int* status) {
+__global__ void __launch_bounds__(1024) block_offsets_kernel(const int* offsets, int rows, int groups,
+                                                             int* block_offsets, int* status) {
   __shared__ int sums[32];
   let_next_start();
   wait_for_previous();
@@ -298,9 +295,8 @@ struct ColumnShared {
 };
 template <typename T, bool Vec, int Fmt, bool Inline>
 __global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4) : Vec ? 9 : 6)
-    quantize_columns_kernel(const T* __restrict__ x, size_t pitch, int rows, int cols, int groups,
-                            const int* __restrict__ offsets, int capacity, uint8_t* __restrict__ values,
-                            uint8_t* __restrict__ scales, int* __restrict__ block_offsets, int* status) {
+    quantize_columns_kernel(const T* x, size_t pitch, int rows, int cols, int groups, const int* offsets, int capacity,
+                            uint8_t* values, uint8_t* scales, int* block_offsets, int* status) {
   __shared__ ColumnShared s;
   __shared__ int first, last;  // this block's rows
   __shared__ int sums[kColumnThreads / 32];
@@ -375,9 +371,8 @@ __global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4)
 // (16 matrices of 4096 x 7168, bf16, both written: 297 us, 6.3 TB/s).
 template <typename T, bool Vec, int Fmt>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3)
-    quantize_weight_kernel(const T* __restrict__ w, int rows, int cols, uint8_t* __restrict__ values,
-                           uint8_t* __restrict__ scales, uint8_t* __restrict__ values_t,
-                           uint8_t* __restrict__ scales_t) {
+    quantize_weight_kernel(const T* w, int rows, int cols, uint8_t* values, uint8_t* scales, uint8_t* values_t,
+                           uint8_t* scales_t) {
   __shared__ TileShared s;
   let_next_start();
   wait_for_previous();

@@ -45,7 +45,7 @@ struct Held {
   uint4 before, here;
   __device__ __forceinline__ void load(const uint8_t* row, int c, int bytes) {
     if (Aligned) {
-      here = load_if<16>(row + 16 * c, 16 * c < bytes);
+      here = load_if(row + 16 * c, 16 * c < bytes);
       return;
     }
     const unsigned s = low4(row);
@@ -53,7 +53,7 @@ struct Held {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       const int at = 16 * (c + i - 1) - static_cast<int>(s);
-      v[i] = load_if<16>(row + at, at > -16 && at < bytes && (i < 2 || s));
+      v[i] = load_if(row + at, at > -16 && at < bytes && (i < 2 || s));
     }
     before = shift_bytes<Select>(v[0], v[1], s);
     here = shift_bytes<Select>(v[1], v[2], s);
@@ -76,11 +76,10 @@ struct Held {
 // lose more by giving up uniform registers for a token's positions and addresses, the combine
 // gradient at that size 53 -> 84 us).
 template <bool Aligned, int E>
-__global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __restrict__ x, size_t x_pitch,
-                                                               uint8_t* __restrict__ rows, size_t rows_pitch, int bytes,
-                                                               unsigned parts, size_t tokens, int k,
-                                                               const int* __restrict__ position,
-                                                               const int* __restrict__ total, int* status) {
+__global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* x, size_t x_pitch, uint8_t* rows,
+                                                               size_t rows_pitch, int bytes, unsigned parts,
+                                                               size_t tokens, int k, const int* position,
+                                                               const int* total, int* status) {
   let_next_start();
   const size_t t = static_cast<size_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y, slots = tokens * k;
   const int c = static_cast<int>(blockIdx.x % parts * blockDim.x + threadIdx.x);
@@ -89,8 +88,10 @@ __global__ void __launch_bounds__(kMaxThreads) dispatch_kernel(const uint8_t* __
   held.load(x + t * x_pitch, c, bytes);  // x does not come from the sort
   wait_for_previous();
   const int kept = *total;
+  int next = position[t * k];  // (asked for a slot ahead of the stores)
   for (int j = 0; j < k; ++j) {
-    const int p = position[t * k + j];
+    const int p = next;
+    if (j + 1 < k) next = position[t * k + j + 1];
     if (in_range(p, slots, status)) held.store(rows + p * rows_pitch, c, bytes, p >= kept);
   }
 }
@@ -102,9 +103,8 @@ constexpr size_t kSmallSlots = 1024;
 
 template <typename Id, bool Aligned, int E>
 __global__ void __launch_bounds__(kMaxThreads) small_dispatch_kernel(
-    const Id* __restrict__ ids, int slots, int experts, const uint8_t* __restrict__ x, size_t x_pitch,
-    uint8_t* __restrict__ rows, size_t rows_pitch, int bytes, unsigned parts, int k, int* __restrict__ position,
-    int* __restrict__ offsets) {
+    const Id* ids, int slots, int experts, const uint8_t* x, size_t x_pitch, uint8_t* rows, size_t rows_pitch,
+    int bytes, unsigned parts, int k, int* position, int* offsets) {
   __shared__ short keys[kSmallSlots];
   __shared__ int place[ZC_MOE_MAX_K];
   __shared__ int bins[ZC_MOE_MAX_EXPERTS + 1];
@@ -175,7 +175,7 @@ __device__ __forceinline__ uint4 from_next_lane(const uint4& v) {
 // The aligned vector that holds byte `from` of a row.
 __device__ __forceinline__ uint4 vector_at(const uint8_t* row, int from, int bytes, bool on) {
   const int at = from - static_cast<int>(low4(row + from));
-  return load_if<16>(row + at, on && at > -16 && at < bytes);
+  return load_if(row + at, on && at > -16 && at < bytes);
 }
 
 // out[t] = sum over j of weights[t, j] rows[position[t, j]].  A thread takes Tokens tokens that follow
@@ -184,9 +184,9 @@ __device__ __forceinline__ uint4 vector_at(const uint8_t* row, int from, int byt
 // (Nine CTAs to an SM: 16384 x 8 x 7167 with weights 381 us, without the bound on registers 394, ten 423.)
 template <typename T, bool Aligned, int Tokens, bool Weighted>
 __global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 : 0)
-    combine_kernel(const uint8_t* __restrict__ rows, size_t rows_pitch, const float* __restrict__ weights,
-                   uint8_t* __restrict__ out, size_t out_pitch, int bytes, unsigned parts, size_t tokens, int k,
-                   const int* __restrict__ position, const int* __restrict__ total, int* status) {
+    combine_kernel(const uint8_t* rows, size_t rows_pitch, const float* weights, uint8_t* out, size_t out_pitch,
+                   int bytes, unsigned parts, size_t tokens, int k, const int* position, const int* total,
+                   int* status) {
   // (four tokens of one slot on unaligned rows: 80 us for 16384 x 1 x 5851 by four, 108 by eight)
   constexpr int N = 16 / sizeof(T), kBatch = !Aligned && Tokens == 4 ? 4 : 8, S = kBatch / Tokens;
   let_next_start();
@@ -214,11 +214,12 @@ __global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 :
       at[i] = position[s];
       w[i] = Weighted ? weights[s] : 1.f;
     }
+    // (all reported before the first load, since none crosses an atomic: 16384 x 8 x 7168 298 us, one by one 311)
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kBatch; ++i)
       here[i] = j0 + i % S < k && t0 + i / S < tokens && in_range(at[i], slots, status) && at[i] < kept;
-      l[i] = vector_at(rows + at[i] * rows_pitch, from[i / S], bytes, here[i]);
-    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) l[i] = vector_at(rows + at[i] * rows_pitch, from[i / S], bytes, here[i]);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (!here[i]) continue;
@@ -246,12 +247,12 @@ template <bool Aligned>
 __device__ __forceinline__ Loaded fetch16(const uint8_t* row, int from, int bytes, bool on) {
   Loaded l;
   if (Aligned) {
-    l.a = load_if<16>(row + from, on && from < bytes);
+    l.a = load_if(row + from, on && from < bytes);
   } else {
     const unsigned s = low4(row + from);
     const int at = from - static_cast<int>(s);  // of the first vector, from the row's start
-    l.a = load_if<16>(row + at, on && at > -16 && at < bytes);
-    l.b = load_if<16>(row + at + 16, on && s && at > -32 && at + 16 < bytes);
+    l.a = load_if(row + at, on && at > -16 && at < bytes);
+    l.b = load_if(row + at + 16, on && s && at > -32 && at + 16 < bytes);
   }
   return l;
 }
@@ -264,9 +265,8 @@ __device__ __forceinline__ uint4 settle(const Loaded& l, const uint8_t* row, int
 // CTA a token: each thread sums its vectors' products, then lanes, then warps, in a fixed order.
 template <typename T, bool Aligned, int Batch>
 __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
-    const uint8_t* __restrict__ d_out, size_t d_out_pitch, const uint8_t* __restrict__ rows, size_t rows_pitch,
-    const float* __restrict__ weights, uint8_t* __restrict__ d_rows, size_t d_rows_pitch, float* __restrict__ d_weights,
-    int bytes, size_t tokens, int k, const int* __restrict__ position, const int* __restrict__ total, int* status) {
+    const uint8_t* d_out, size_t d_out_pitch, const uint8_t* rows, size_t rows_pitch, const float* weights,
+    uint8_t* d_rows, size_t d_rows_pitch, float* d_weights, int bytes, size_t tokens, int k, const int* position, const int* total, int* status) {
   constexpr int N = 16 / sizeof(T);
   __shared__ float sums[Batch][kMaxThreads / 32];
   let_next_start();

@@ -30,8 +30,8 @@ __device__ __forceinline__ int key_of(const Id* ids, size_t s, int experts) {
 }
 
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) count_kernel(const Id* __restrict__ ids, int slots, int run,
-                                                             int experts, int* __restrict__ counts) {
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const Id* ids, int slots, int run, int experts,
+                                                             int* counts) {
   extern __shared__ int bins[];
   wait_for_previous();
   let_next_start();
@@ -46,9 +46,9 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const Id* __restric
 
 // counts: [runs][experts + 1] from count_kernel; not read when there is one run.
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) place_kernel(const Id* __restrict__ ids, int slots, int run, int runs,
-                                                             int experts, const int* __restrict__ counts,
-                                                             int* __restrict__ position, int* __restrict__ offsets) {
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const Id* ids, int slots, int run, int runs,
+                                                             int experts, const int* counts, int* position,
+                                                             int* offsets) {
   extern __shared__ int bins[];  // [kSortWarps][experts + 1]
   __shared__ int warp_sums[kSortWarps];
   __shared__ int carry;
