@@ -134,6 +134,22 @@ int zc_fp8_weight_grad(const void* a, const void* a_scales, int a_fmt, const voi
                        size_t capacity, int groups, size_t n, size_t k, const int* block_offsets, void* out,
                        int out_type, cudaStream_t stream);
 
+/* ------------------------------------------------------------------ test hooks */
+
+/* The products with a planted stall, for testing the bounded waits: CTA `stalled_cta` of the launch (-1: none) loads
+ * nothing, so the waits for its operands run out after about wait_us microseconds (those for a whole tile after two
+ * more for each of its blocks), every role gives up and zc_status reports ZC_ERR_TIMEOUT.  What the stalled CTA should
+ * have computed is then missing from `out`.  The other arguments are zc_fp8_matmul's and zc_fp8_weight_grad's, whose
+ * own limit is 4 s. */
+int zc_fp8_matmul_stall_test(const void* a, const void* a_scales, int a_fmt, size_t rows, const void* b,
+                             const void* b_scales, int b_fmt, int groups, size_t n, size_t k, const int* offsets,
+                             void* out, size_t out_pitch, int out_type, void* workspace, cudaStream_t stream,
+                             int stalled_cta, unsigned wait_us);
+int zc_fp8_weight_grad_stall_test(const void* a, const void* a_scales, int a_fmt, const void* b, const void* b_scales,
+                                  int b_fmt, size_t capacity, int groups, size_t n, size_t k,
+                                  const int* block_offsets, void* out, int out_type, cudaStream_t stream,
+                                  int stalled_cta, unsigned wait_us);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,8 @@ SIGNATURES = {
     "zc_fp8_matmul_workspace": (_N, [_N, _I, _N, _N]),
     "zc_fp8_matmul": (_I, [_P, _P, _I, _N, _P, _P, _I, _I, _N, _N, _P, _P, _N, _I, _P, _P]),
     "zc_fp8_weight_grad": (_I, [_P, _P, _I, _P, _P, _I, _N, _I, _N, _N, _P, _P, _I, _P]),
+    "zc_fp8_matmul_stall_test": (_I, [_P, _P, _I, _N, _P, _P, _I, _I, _N, _N, _P, _P, _N, _I, _P, _P, _I, _I]),
+    "zc_fp8_weight_grad_stall_test": (_I, [_P, _P, _I, _P, _P, _I, _N, _I, _N, _N, _P, _P, _I, _P, _I, _I]),
 }
 
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}

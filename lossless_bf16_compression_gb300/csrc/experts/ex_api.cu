@@ -66,6 +66,64 @@ int finish(cudaError_t err) {
   return ZC_ERR_CUDA;
 }
 
+int matmul(const void* a, const void* a_scales, int a_fmt, size_t rows, const void* b, const void* b_scales,
+           int b_fmt, int groups, size_t n, size_t k, const int* offsets, void* out, size_t out_pitch,
+           int out_type, void* workspace, cudaStream_t stream,
+           const ex::Waits& waits) {
+  if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || !matrix_ok(rows, k) || n < 1 || n > kMaxCols ||
+      out_pitch < n || (out_type != ZC_TYPE_BF16 && out_type != ZC_TYPE_FP32) || (!offsets && groups != 1))
+    return ZC_ERR_INVALID_ARG;
+  if (rows == 0) return ZC_OK;
+  const size_t scratch = ex::matmul_workspace(rows, groups, n, k);
+  if (!a || !a_scales || !b || !b_scales || !out || (scratch && !workspace)) return ZC_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16)) return ZC_ERR_MISALIGNED;
+  if (!aligned(a, 128) || !aligned(b, 128) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
+      !aligned(offsets, 4) || !aligned(out, ex::type_bytes(out_type)))
+    return ZC_ERR_MISALIGNED;
+  const size_t g = groups;
+  if (clash({{out, rows_bytes(rows, out_pitch, n, out_type)}, {workspace, scratch}},
+            {{a, values_bytes(rows, k)},
+             {a_scales, scales_bytes(rows, k)},
+             {b, g * values_bytes(n, k)},
+             {b_scales, g * scales_bytes(n, k)},
+             {offsets, offsets ? 4 * (g + 1) : 0}}))
+    return ZC_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
+  const ex::Product p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
+                      static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
+                      a_fmt, b_fmt, groups, out_type, rows, n, k, out_pitch, offsets, out, workspace,
+                      waits};
+  return finish(ex::launch_matmul(p, dev, stream));
+}
+
+int weight_grad(const void* a, const void* a_scales, int a_fmt, const void* b, const void* b_scales, int b_fmt,
+                size_t capacity, int groups, size_t n, size_t k, const int* block_offsets, void* out,
+                int out_type, cudaStream_t stream, const ex::Waits& waits) {
+  if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || capacity > kMaxRows / ZC_FP8_BLOCK || n < 1 ||
+      n > kMaxCols || k < 1 || k > kMaxCols || (out_type != ZC_TYPE_BF16 && out_type != ZC_TYPE_FP32) || !out ||
+      !block_offsets || (capacity && (!a || !a_scales || !b || !b_scales)))
+    return ZC_ERR_INVALID_ARG;
+  if (!aligned(a, 128) || !aligned(b, 128) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
+      !aligned(block_offsets, 4) || !aligned(out, ex::type_bytes(out_type)))
+    return ZC_ERR_MISALIGNED;
+  const size_t g = groups, wide = capacity * ZC_FP8_BLOCK;
+  if (clash({{out, g * n * k * ex::type_bytes(out_type)}},
+            {{a, values_bytes(n, wide)},
+             {a_scales, scales_bytes(n, wide)},
+             {b, values_bytes(k, wide)},
+             {b_scales, scales_bytes(k, wide)},
+             {block_offsets, 4 * (g + 1)}}))
+    return ZC_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
+  const ex::Product p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
+                      static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
+                      a_fmt, b_fmt, groups, out_type, capacity, n, k, k, block_offsets, out, nullptr,
+                      waits};
+  return finish(ex::launch_weight_grad(p, dev, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -237,56 +295,31 @@ size_t zc_fp8_matmul_workspace(size_t rows, int groups, size_t n, size_t k) {
 int zc_fp8_matmul(const void* a, const void* a_scales, int a_fmt, size_t rows, const void* b, const void* b_scales,
                   int b_fmt, int groups, size_t n, size_t k, const int* offsets, void* out, size_t out_pitch,
                   int out_type, void* workspace, cudaStream_t stream) {
-  if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || !matrix_ok(rows, k) || n < 1 || n > kMaxCols ||
-      out_pitch < n || (out_type != ZC_TYPE_BF16 && out_type != ZC_TYPE_FP32) || (!offsets && groups != 1))
-    return ZC_ERR_INVALID_ARG;
-  if (rows == 0) return ZC_OK;
-  const size_t scratch = ex::matmul_workspace(rows, groups, n, k);
-  if (!a || !a_scales || !b || !b_scales || !out || (scratch && !workspace)) return ZC_ERR_INVALID_ARG;
-  if (!aligned(workspace, 16)) return ZC_ERR_MISALIGNED;
-  if (!aligned(a, 128) || !aligned(b, 128) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
-      !aligned(offsets, 4) || !aligned(out, ex::type_bytes(out_type)))
-    return ZC_ERR_MISALIGNED;
-  const size_t g = groups;
-  if (clash({{out, rows_bytes(rows, out_pitch, n, out_type)}, {workspace, scratch}},
-            {{a, values_bytes(rows, k)},
-             {a_scales, scales_bytes(rows, k)},
-             {b, g * values_bytes(n, k)},
-             {b_scales, g * scales_bytes(n, k)},
-             {offsets, offsets ? 4 * (g + 1) : 0}}))
-    return ZC_ERR_INVALID_ARG;
-  DeviceInfo dev;
-  if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
-  const ex::Product p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
-                      static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
-                      a_fmt, b_fmt, groups, out_type, rows, n, k, out_pitch, offsets, out, workspace};
-  return finish(ex::launch_matmul(p, dev, stream));
+  return matmul(a, a_scales, a_fmt, rows, b, b_scales, b_fmt, groups, n, k, offsets, out, out_pitch, out_type,
+                workspace, stream, ex::kWaits);
 }
 
 int zc_fp8_weight_grad(const void* a, const void* a_scales, int a_fmt, const void* b, const void* b_scales, int b_fmt,
                        size_t capacity, int groups, size_t n, size_t k, const int* block_offsets, void* out,
                        int out_type, cudaStream_t stream) {
-  if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || capacity > kMaxRows / ZC_FP8_BLOCK || n < 1 ||
-      n > kMaxCols || k < 1 || k > kMaxCols || (out_type != ZC_TYPE_BF16 && out_type != ZC_TYPE_FP32) || !out ||
-      !block_offsets || (capacity && (!a || !a_scales || !b || !b_scales)))
-    return ZC_ERR_INVALID_ARG;
-  if (!aligned(a, 128) || !aligned(b, 128) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
-      !aligned(block_offsets, 4) || !aligned(out, ex::type_bytes(out_type)))
-    return ZC_ERR_MISALIGNED;
-  const size_t g = groups, wide = capacity * ZC_FP8_BLOCK;
-  if (clash({{out, g * n * k * ex::type_bytes(out_type)}},
-            {{a, values_bytes(n, wide)},
-             {a_scales, scales_bytes(n, wide)},
-             {b, values_bytes(k, wide)},
-             {b_scales, scales_bytes(k, wide)},
-             {block_offsets, 4 * (g + 1)}}))
-    return ZC_ERR_INVALID_ARG;
-  DeviceInfo dev;
-  if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
-  const ex::Product p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
-                      static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
-                      a_fmt, b_fmt, groups, out_type, capacity, n, k, k, block_offsets, out, nullptr};
-  return finish(ex::launch_weight_grad(p, dev, stream));
+  return weight_grad(a, a_scales, a_fmt, b, b_scales, b_fmt, capacity, groups, n, k, block_offsets, out, out_type,
+                     stream, ex::kWaits);
+}
+
+int zc_fp8_matmul_stall_test(const void* a, const void* a_scales, int a_fmt, size_t rows, const void* b,
+                             const void* b_scales, int b_fmt, int groups, size_t n, size_t k, const int* offsets,
+                             void* out, size_t out_pitch, int out_type, void* workspace, cudaStream_t stream,
+                             int stalled_cta, unsigned wait_us) {
+  return matmul(a, a_scales, a_fmt, rows, b, b_scales, b_fmt, groups, n, k, offsets, out, out_pitch, out_type,
+                workspace, stream, {1000ull * wait_us, stalled_cta});
+}
+
+int zc_fp8_weight_grad_stall_test(const void* a, const void* a_scales, int a_fmt, const void* b, const void* b_scales,
+                                  int b_fmt, size_t capacity, int groups, size_t n, size_t k,
+                                  const int* block_offsets, void* out, int out_type, cudaStream_t stream,
+                                  int stalled_cta, unsigned wait_us) {
+  return weight_grad(a, a_scales, a_fmt, b, b_scales, b_fmt, capacity, groups, n, k, block_offsets, out, out_type,
+                     stream, {1000ull * wait_us, stalled_cta});
 }
 
 }  // extern "C"

@@ -180,12 +180,19 @@ cudaError_t launch_quantize_weight(const void* w, int type, int groups, size_t r
                                    uint8_t* values, uint8_t* scales, uint8_t* values_t, uint8_t* scales_t,
                                    cudaStream_t stream);
 
+// A product's waits: how long one may take, and (for their test) the CTA that loads nothing; -1: none.
+struct Waits {
+  unsigned long long limit_ns;
+  int stalled;
+};
+constexpr Waits kWaits = {4000000000ull, -1};
 struct Product {
   const uint8_t *a, *a_scales, *b, *b_scales;
   int a_fmt, b_fmt, groups, out_type;
   size_t rows, n, k, out_pitch;
   const int* offsets;
   void *out, *workspace;
+  Waits waits;
 };
 // rows: the capacity in blocks for weight_grad.
 size_t matmul_workspace(size_t rows, int groups, size_t n, size_t k);

@@ -75,6 +75,8 @@ struct TileParams {
   void* out;
   size_t out_pitch;
   int* status;
+  unsigned long long wait_ns;  // limit of a wait (for a whole tile: and kWaitBlockNs for each of its blocks)
+  int stalled;                 // the CTA that loads nothing, for the test of the waits; -1: none
 };
 
 struct Shared {
@@ -83,6 +85,7 @@ struct Shared {
   uint64_t sum_full[2], sum_empty[2], drained;
   uint32_t tmem;
   unsigned failed;
+  unsigned loads;                            // stages that this CTA has loaded
   int start[ZC_MOE_MAX_EXPERTS + 2];         // first row (or block) of each group
   unsigned tiles[ZC_MOE_MAX_EXPERTS + 2];    // tiles before each group
 };
@@ -356,7 +359,8 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
         for (int c = half; c < columns; c += 2) put(out + c * p.out_pitch, 0u);
       continue;
     }
-    if (!__all_sync(~0u, wait_phase(&s.sum_full[sums % 2], sums / 2 % 2, failed))) break;
+    const unsigned long long limit = p.wait_ns + kWaitBlockNs * (tile.b1 - tile.b0);
+    if (!__all_sync(~0u, wait_phase<G>(&s.sum_full[sums % 2], sums / 2 % 2, failed, limit))) break;
     tcgen05_fence_after();
     const uint32_t from = tmem + (static_cast<uint32_t>(quarter) << 21) + sums % 2 * accumulator;
     if constexpr (G == 1) {
@@ -429,6 +433,22 @@ __device__ __forceinline__ void write_sums(const TileParams& p, Shared& s, uint3
   }
 }
 
+// After the roles gave up: the loads in flight still write the CTA's (or pair's) memory, so wait for
+// the last one of each stage.  In a pair one CTA may have loaded more stages than the other: the leader's
+// barrier expects both's bytes once the leader has loaded, and none before.
+template <int G>
+__device__ __noinline__ void await_loads(const TileParams& p, Shared& s, uint32_t stage_bytes) {
+  const unsigned first = s.loads, second = G == 2 ? seconds_word(&s.loads) : first, all = max(first, second);
+  const unsigned stages = p.stages;
+  for (unsigned n = all > stages ? all - stages : 0; n < all; ++n) {
+    uint64_t* bar = &s.full[n % stages];
+    if (n >= second) mbar_complete_tx(bar, stage_bytes);
+    if (n >= first) mbar_arrive_expect_tx(bar, stage_bytes);
+    const unsigned long long start = now_ns();
+    while (!phase_done(bar, n / stages % 2) && now_ns() - start < kWaits.limit_ns) {}
+  }
+}
+
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ TileParams p,
                                                              const __grid_constant__ CUtensorMap p_map,
@@ -489,10 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     int stage = 0;
     unsigned phase = 0, loads = 0;
     bool ok = true;
-    while (ok && walk.next(&tile)) {
+    while (ok && p.stalled != static_cast<int>(blockIdx.x) && walk.next(&tile)) {
       const int z = p.by_blocks ? 0 : tile.group;
       for (int b = tile.b0; b < tile.b1; ++b) {
-        if (!(ok = __all_sync(~0u, wait_phase(&s.empty[stage], phase ^ 1, failed)))) break;
+        if (!(ok = __all_sync(~0u, wait_phase<G>(&s.empty[stage], phase ^ 1, failed, p.wait_ns)))) break;
         const uint32_t at = smem_u32(tiles) + stage * stage_bytes, bar = leaders<G>(&s.full[stage]);
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], G * stage_bytes);
@@ -503,13 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         if (++stage == p.stages) stage = 0, phase ^= 1;
       }
     }
-    // given up: the loads in flight still write the CTA's (or pair's) memory, so wait for them
-    if (!ok && rank == 0)
-      for (unsigned i = 0; i < loads && i < static_cast<unsigned>(p.stages); ++i) {
-        if (--stage < 0) stage = p.stages - 1, phase ^= 1;
-        const unsigned long long start = now_ns();
-        while (!phase_done(&s.full[stage], phase) && now_ns() - start < kWaitLimitNs) {}
-      }
+    if (lane == 0) s.loads = loads;
   } else if (warp == 1) {
     if (rank == 0) {
       const uint32_t desc = product_desc<G>(p.p_fmt, p.q_fmt, p.tile_q);
@@ -523,14 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         if (tile.b0 == tile.b1) continue;
         if (sums >= lag) {
           const unsigned j = sums - lag;
-          if (!(ok = __all_sync(~0u, wait_phase(&s.sum_empty[j % 2], j / 2 % 2, failed)))) break;
+          if (!(ok = __all_sync(~0u, wait_phase<G>(&s.sum_empty[j % 2], j / 2 % 2, failed, p.wait_ns)))) break;
         }
         const uint32_t d = tmem + sums % 2 * accumulator;
         for (int b = tile.b0; b < tile.b1; ++b) {
           const uint32_t sp = scale_columns + turn * kTurnColumns, sq = sp + 4;
           const bool new_word = b == tile.b0 || b % 4 == 0, last = b == tile.b1 - 1, end_word = b % 4 == 3 || last;
-          if (new_word && !(ok = __all_sync(~0u, wait_phase(&s.scales_full[turn], turn_phase, failed)))) break;
-          if (!(ok = __all_sync(~0u, wait_phase(&s.full[stage], phase, failed)))) break;
+          if (new_word && !(ok = __all_sync(~0u, wait_phase<G>(&s.scales_full[turn], turn_phase, failed, p.wait_ns))))
+            break;
+          if (!(ok = __all_sync(~0u, wait_phase<G>(&s.full[stage], phase, failed, p.wait_ns)))) break;
           tcgen05_fence_after();
           const uint32_t at = smem_u32(tiles) + stage * stage_bytes;
           const uint64_t pd = operand_desc(at), qd = operand_desc(at + kTileP * kBlock);
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       if (!ok) {  // given up: the products in flight end before tensor memory is freed
         if (elect_one()) commit_to<G>(&s.drained);
         const unsigned long long start = now_ns();
-        while (!phase_done(&s.drained, 0) && now_ns() - start < kWaitLimitNs) {}
+        while (!phase_done(&s.drained, 0) && now_ns() - start < kWaits.limit_ns) {}
       }
     }
   } else if (warp < 4 || warp == 8 || warp == 9) {
@@ -586,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     for (bool ok = true; ok;) {
 #pragma unroll
       for (int i = 0; i < kWordsAhead; ++i) {
-        ok = ok && have[i] && __all_sync(~0u, wait_phase(&s.scales_empty[turn], phase ^ 1, failed));
+        ok = ok && have[i] && __all_sync(~0u, wait_phase<G>(&s.scales_empty[turn], phase ^ 1, failed, p.wait_ns));
         if (!ok) break;
         tcgen05_fence_after();
         const uint32_t at = to + turn * kTurnColumns;
@@ -614,7 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     tcgen05_fence_after();
     tmem_free<G>(tmem, kColumns);
   }
-  if (threadIdx.x == 0 && s.failed) set_error(p.status, ZC_ERR_TIMEOUT);
+  if (s.failed) {  // (the same in both CTAs of a pair)
+    if (rank == 0 && threadIdx.x == 0) await_loads<G>(p, s, stage_bytes);
+    if (G == 2) cluster_sync();
+    if (threadIdx.x == 0) set_error(p.status, ZC_ERR_TIMEOUT);
+  }
 }
 
 size_t smem_bytes(int load_q, int stages) {
@@ -672,11 +691,13 @@ cudaError_t allow_shared_memory() {
 
 template <int G>
 cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_t p_matrices, const uint8_t* qv,
-                         size_t q_pitch, const DeviceInfo& dev, cudaStream_t stream) {
+                         size_t q_pitch, const Waits& waits, const DeviceInfo& dev, cudaStream_t stream) {
   const int load_q = t.tile_q / G;
   t.stages = 2;
   while (t.stages < kMaxStages && smem_bytes(load_q, t.stages + 1) <= kSmemLimit) ++t.stages;
   t.status = dev.status;
+  t.wait_ns = waits.limit_ns;
+  t.stalled = waits.stalled;
   t.out_words = reinterpret_cast<uintptr_t>(t.out) % 4 == 0 && t.out_pitch % 2 == 0 && t.p_rows % 2 == 0;
   CUtensorMap p_map, q_map;
   cudaError_t err = tile_map(pv, p_pitch, t.p_rows, p_matrices, 3, kTileP, &p_map);
@@ -753,10 +774,11 @@ size_t parts_bytes(const Shape& shape) {
 }
 
 cudaError_t launch_any(TileParams& t, const Shape& shape, const uint8_t* pv, size_t p_pitch, size_t p_matrices,
-                       const uint8_t* qv, size_t q_pitch, const DeviceInfo& dev, cudaStream_t stream) {
+                       const uint8_t* qv, size_t q_pitch, const Waits& waits, const DeviceInfo& dev,
+                       cudaStream_t stream) {
   t.tile_q = shape.tile_q;
-  return shape.pair ? launch_tiles<2>(t, pv, p_pitch, p_matrices, qv, q_pitch, dev, stream)
-                    : launch_tiles<1>(t, pv, p_pitch, p_matrices, qv, q_pitch, dev, stream);
+  return shape.pair ? launch_tiles<2>(t, pv, p_pitch, p_matrices, qv, q_pitch, waits, dev, stream)
+                    : launch_tiles<1>(t, pv, p_pitch, p_matrices, qv, q_pitch, waits, dev, stream);
 }
 
 }  // namespace
@@ -790,7 +812,7 @@ cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t 
     const cudaError_t err = launch(clear_kernel, 1, kArrivals / 4, 0, stream, true, static_cast<uint4*>(p.workspace));
     if (err != cudaSuccess) return err;
   }
-  return launch_any(t, shape, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, dev, stream);
+  return launch_any(t, shape, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, p.waits, dev, stream);
 }
 
 cudaError_t launch_weight_grad(const Product& p, const DeviceInfo& dev, cudaStream_t stream) {
@@ -813,7 +835,7 @@ cudaError_t launch_weight_grad(const Product& p, const DeviceInfo& dev, cudaStre
   t.out = p.out;
   t.out_pitch = p.k;
   const Shape shape = shape_of(p.n, p.groups, p.k, capacity, true);
-  return launch_any(t, shape, p.b, capacity * kBlock, 1, p.a, capacity * kBlock, dev, stream);
+  return launch_any(t, shape, p.b, capacity * kBlock, 1, p.a, capacity * kBlock, p.waits, dev, stream);
 }
 
 }  // namespace ex

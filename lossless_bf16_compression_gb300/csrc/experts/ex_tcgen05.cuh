@@ -11,8 +11,9 @@ namespace ex {
 
 // ------------------------------------------------------------------ bounded waits
 
-// Nanoseconds after which a wait gives up: far beyond any product's run time.
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+// Nanoseconds that a wait for a whole tile may take longer than another, for each block of its sum: a block takes
+// 0.3 us, but the longest sum, a weight gradient's over 2^31 rows in one group, 4.4 s.
+constexpr unsigned long long kWaitBlockNs = 2000;
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -32,16 +33,43 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, unsigned parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile unsigned* failed) {
+// The flag of having given up, in this CTA and (with G = 2) in the other one of the pair.
+template <int G>
+__device__ __forceinline__ void give_up(volatile unsigned* failed) {
+  *failed = 1;
+  if (G == 2)
+    asm volatile(
+        "{\n\t.reg .b32 r, a;\n\tmov.u32 r, %%cluster_ctarank;\n\txor.b32 r, r, 1;\n\t"
+        "mapa.shared::cluster.u32 a, %0, r;\n\tst.relaxed.cluster.shared::cluster.u32 [a], 1;\n\t}" ::"r"(
+            smem_u32(const_cast<unsigned*>(failed)))
+        : "memory");
+}
+template <int G>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, volatile unsigned* failed,
+                                           unsigned long long limit) {
   if (phase_done(bar, parity)) return true;
   const unsigned long long start = now_ns();
   for (unsigned i = 1;; ++i) {
     if (phase_done(bar, parity)) return true;
-    if (i % 256 == 0 && (*failed || now_ns() - start > kWaitLimitNs)) {
-      *failed = 1;
+    if (i % 256 == 0 && (*failed || now_ns() - start > limit)) {
+      give_up<G>(failed);
       return false;
     }
   }
+}
+// Bytes taken as arrived, of those that a phase of `bar` was told to expect.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, unsigned bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// A word of the second CTA's shared memory, at the place of this CTA's `word`.
+__device__ __forceinline__ unsigned seconds_word(const unsigned* word) {
+  unsigned v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, 1;\n\tld.relaxed.cluster.shared::cluster.u32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"(smem_u32(word))
+      : "memory");
+  return v;
 }
 
 // One lane of a converged warp.  The tensor-core and TMA instructions take uniform operands: a

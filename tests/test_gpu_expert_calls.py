@@ -88,3 +88,82 @@ def test_inputs_written_by_the_kernel_before(tokens, k, hidden):
     together = [step(i, lambda: None) for i in range(rounds)]
     for one, other in zip(apart, together):
         assert all(same_bits(a, b) for a, b in zip(one, other))
+
+
+# ------------------------------------------------------------------ the products' bounded waits
+
+
+def starts(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+
+
+def stalled_matmul(a, b, offsets, cta, wait_us):
+    from lossless_bf16_compression_gb300 import _tensors
+
+    groups, n = b.data.shape[:2]
+    out = torch.zeros((a.rows, n), device="cuda")
+    need = _tensors.fn("zc_fp8_matmul_workspace")(a.rows, groups, n, a.cols)
+    scratch = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    rc = _tensors.fn("zc_fp8_matmul_stall_test")(
+        a.data.data_ptr(), a.scales.data_ptr(), 0, a.rows, b.data.data_ptr(), b.scales.data_ptr(), 0, groups, n, a.cols,
+        offsets.data_ptr(), out.data_ptr(), n, 2, scratch.data_ptr() if need else 0,
+        torch.cuda.current_stream().cuda_stream, cta, wait_us)
+    assert rc == zc.ZC_OK
+    return out, need
+
+
+def stalled_weight_grad(dy, x, cta, wait_us):
+    from lossless_bf16_compression_gb300 import _tensors
+
+    groups = x.offsets.numel() - 1
+    out = torch.zeros((groups, dy.rows, x.rows), device="cuda")
+    rc = _tensors.fn("zc_fp8_weight_grad_stall_test")(
+        dy.data.data_ptr(), dy.scales.data_ptr(), 0, x.data.data_ptr(), x.scales.data_ptr(), 0, x.data.shape[1] // 128,
+        groups, dy.rows, x.rows, x.offsets.data_ptr(), out.data_ptr(), 2, torch.cuda.current_stream().cuda_stream, cta,
+        wait_us)
+    assert rc == zc.ZC_OK
+    return out
+
+
+# single CTAs, pairs (256 x 256 tiles: 16 rounds of them at 4096 x 4096), blocks shared out (a workspace)
+@pytest.mark.parametrize("counts,n,k,shared", [((300,), 200, 640, False), ((4096,), 4096, 700, False),
+                                               ((3, 0, 5), 1000, 7168, True)])
+@pytest.mark.parametrize("cta", [0, 1])
+def test_a_product_whose_loads_never_come_gives_up(counts, n, k, shared, cta):
+    """The waits run out, the status says so, and the call after it is whole."""
+    at = starts(counts)
+    a = fp8.quantize(values((int(at[-1]), k), torch.bfloat16, 1))
+    b, _ = fp8.quantize_weight(values((len(counts), n, k), torch.bfloat16, 2), transposed=False)
+    want = fp8.matmul(a, b, at, torch.float32)
+    for _ in range(2):
+        _, need = stalled_matmul(a, b, at, cta, 20000)
+        assert zc.status(reset=True) == zc.ZC_ERR_TIMEOUT and (need > 0) == shared
+        assert same_bits(fp8.matmul(a, b, at, torch.float32), want)
+        assert same_bits(stalled_matmul(a, b, at, -1, 200000)[0], want)
+        assert zc.status(reset=True) == zc.ZC_OK
+
+
+@pytest.mark.parametrize("counts,n,k", [((100, 0, 30), 200, 130), ((600,) * 8, 2048, 1024)])
+@pytest.mark.parametrize("cta", [0, 1])
+def test_a_weight_gradient_whose_loads_never_come_gives_up(counts, n, k, cta):
+    at = starts(counts)
+    dy = fp8.quantize_columns(values((int(at[-1]), n), torch.bfloat16, 1), at)
+    x = fp8.quantize_columns(values((int(at[-1]), k), torch.bfloat16, 2), at)
+    want = fp8.weight_grad(dy, x, torch.float32)
+    for _ in range(2):
+        stalled_weight_grad(dy, x, cta, 20000)
+        assert zc.status(reset=True) == zc.ZC_ERR_TIMEOUT
+        assert same_bits(fp8.weight_grad(dy, x, torch.float32), want)
+        assert same_bits(stalled_weight_grad(dy, x, -1, 200000), want)
+        assert zc.status(reset=True) == zc.ZC_OK
+
+
+def test_a_sum_longer_than_the_limit_of_a_wait_is_not_given_up():
+    """65,536 blocks in one tile take about 20 ms, ten times the limit given here for any other wait.  Ones far apart,
+    so that the sum is exact."""
+    rows = 1 << 23
+    dy, x = torch.zeros((rows, 1), dtype=torch.bfloat16, device="cuda"), torch.ones((rows, 3), dtype=torch.bfloat16, device="cuda")
+    dy[::65536] = 1
+    got = stalled_weight_grad(fp8.quantize_columns(dy), fp8.quantize_columns(x), -1, 2000)
+    assert zc.status(reset=True) == zc.ZC_OK
+    assert got.flatten().tolist() == [128.0] * 3
