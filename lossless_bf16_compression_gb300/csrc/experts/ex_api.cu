@@ -33,6 +33,7 @@ bool fmt_ok(int fmt) { return fmt == ZC_FP8_E4M3 || fmt == ZC_FP8_E5M2; }
 bool groups_ok(int groups) { return groups >= 1 && groups <= ZC_MOE_MAX_EXPERTS; }
 
 constexpr size_t kMaxRows = 0x7FFFFFFF - 131072;  // rows and row tiles fit in 32 bits with room to spare
+constexpr size_t kMaxBlocks = 0x7FFFFFFF / ZC_FP8_BLOCK;  // of kMaxRows rows in ZC_MOE_MAX_EXPERTS groups
 constexpr size_t kMaxCols = size_t(1) << 20;
 bool matrix_ok(size_t rows, size_t cols) { return rows <= kMaxRows && cols >= 1 && cols <= kMaxCols; }
 
@@ -100,7 +101,7 @@ int matmul(const void* a, const void* a_scales, int a_fmt, size_t rows, const vo
 int weight_grad(const void* a, const void* a_scales, int a_fmt, const void* b, const void* b_scales, int b_fmt,
                 size_t capacity, int groups, size_t n, size_t k, const int* block_offsets, void* out,
                 int out_type, cudaStream_t stream, const ex::Waits& waits) {
-  if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || capacity > kMaxRows / ZC_FP8_BLOCK || n < 1 ||
+  if (!fmt_ok(a_fmt) || !fmt_ok(b_fmt) || !groups_ok(groups) || capacity > kMaxBlocks || n < 1 ||
       n > kMaxCols || k < 1 || k > kMaxCols || (out_type != ZC_TYPE_BF16 && out_type != ZC_TYPE_FP32) || !out ||
       !block_offsets || (capacity && (!a || !a_scales || !b || !b_scales)))
     return ZC_ERR_INVALID_ARG;

@@ -34,3 +34,18 @@ def test_stall_hooks_refuse(name, args, changes):
         assert fn(*bad) == code, (at, value)
     if not os.path.exists("/dev/nvidia0"):
         assert fn(*args) == zc.ZC_ERR_CUDA  # valid arguments reach the runtime, which has no device
+
+
+def test_weight_grad_takes_what_quantize_columns_makes():
+    """The most blocks that quantize_columns fills, of the most rows in the most groups, and not one more."""
+    rows, groups, far = 0x7FFFFFFF - 131072, 1024, 1 << 40
+    most = _tensors.fn("zc_fp8_column_blocks")(rows, groups)
+    assert most == rows // 128 + groups and _tensors.fn("zc_fp8_column_blocks")(rows + 1, groups) == 0
+    fn = _tensors.fn("zc_fp8_weight_grad")
+
+    def rc(capacity):
+        return fn(far, 2 * far, 0, 3 * far, 4 * far, 0, capacity, groups, 1, 1, 5 * far, 6 * far, 2, 0)
+
+    assert rc(most + 1) == INV
+    if not os.path.exists("/dev/nvidia0"):
+        assert rc(most) == zc.ZC_ERR_CUDA == rc(rows // 128 + 1)
