@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <initializer_list>
 
 #include "zc_common.cuh"
@@ -116,6 +117,21 @@ inline bool whole_vectors(size_t element, size_t row_values, std::initializer_li
 }
 
 inline size_t type_bytes(int type) { return type == ZC_TYPE_FP32 ? 4 : 2; }
+
+// Lets a kernel's launches have up to `most` bytes of dynamic shared memory: asked once for each device
+// and never lowered, since another thread may be between asking and launching.
+template <auto Kernel>
+cudaError_t allow_shared_memory(size_t most) {
+  static std::atomic<unsigned long long> done{0};
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (device % 64);
+  if (done.load() & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+  if (err == cudaSuccess) done.fetch_or(bit);
+  return err;
+}
 
 // A launch; early: it may start while the kernel before it in the stream still runs (whoever
 // launched that one), so the kernel calls wait_for_previous before it touches memory.  Two kernels

@@ -24,7 +24,6 @@
 // Scales are kept four blocks to a word, [word][row].  A product's scales lie in tensor memory, row
 // r at lane r % 32 (in each quarter of the lanes) and column r / 32, so a warp reads 32 rows' words
 // as one coalesced load and stores them as one column; byte b % 4 is picked by the instruction.
-#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -675,20 +674,6 @@ cudaError_t tile_map(const uint8_t* base, size_t pitch, size_t rows, size_t matr
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Once for each device.
-template <int G>
-cudaError_t allow_shared_memory() {
-  static std::atomic<unsigned long long> done{0};
-  int device = 0;
-  cudaError_t err = cudaGetDevice(&device);
-  if (err != cudaSuccess) return err;
-  const unsigned long long bit = 1ull << (device % 64);
-  if (done.load() & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(matmul_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemLimit));
-  if (err == cudaSuccess) done.fetch_or(bit);
-  return err;
-}
-
 template <int G>
 cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_t p_matrices, const uint8_t* qv,
                          size_t q_pitch, const Waits& waits, const DeviceInfo& dev, cudaStream_t stream) {
@@ -702,7 +687,7 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
   CUtensorMap p_map, q_map;
   cudaError_t err = tile_map(pv, p_pitch, t.p_rows, p_matrices, 3, kTileP, &p_map);
   if (err == cudaSuccess) err = tile_map(qv, q_pitch, t.q_rows, 1, 2, load_q, &q_map);
-  if (err == cudaSuccess) err = allow_shared_memory<G>();
+  if (err == cudaSuccess) err = allow_shared_memory<matmul_kernel<G>>(kSmemLimit);
   if (err != cudaSuccess) return err;
   const size_t most = ceil_div(t.p_rows, kTileP * G) *
                       (t.by_blocks ? ceil_div(t.q_rows, t.tile_q) * t.groups : t.q_rows / t.tile_q + t.groups + 1);

@@ -18,6 +18,9 @@ constexpr int kSortThreads = 32 * kSortWarps;
 constexpr size_t kRunSlots = 1024;  // slots of a run, while there are at most kMaxRuns
 constexpr size_t kMaxRuns = 128;    // every CTA of the second kernel reads every run's counts
 
+// Dynamic shared memory that needs no asking: 48 KB less what the kernel has itself.
+constexpr size_t kPlainShared = 48 * 1024 - 1024;
+
 size_t runs_of(size_t slots) {
   const size_t r = (slots + kRunSlots - 1) / kRunSlots;
   return r < 1 ? 1 : r > kMaxRuns ? kMaxRuns : r;
@@ -134,9 +137,8 @@ cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts
   const auto go = [&](auto* p) {
     using Id = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
     cudaError_t err = cudaSuccess;
-    if (kSortWarps * row > 48 * 1024)
-      err = cudaFuncSetAttribute(place_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSortWarps * row));
+    if (kSortWarps * row > kPlainShared)
+      err = allow_shared_memory<place_kernel<Id>>(kSortWarps * sizeof(int) * (ZC_MOE_MAX_EXPERTS + 1));
     if (err == cudaSuccess && runs > 1)
       err = launch(count_kernel<Id>, runs, kSortThreads, row, stream, true, p, n, run, experts, counts);
     if (err == cudaSuccess)

@@ -167,3 +167,58 @@ def test_a_sum_longer_than_the_limit_of_a_wait_is_not_given_up():
     got = stalled_weight_grad(fp8.quantize_columns(dy), fp8.quantize_columns(x), -1, 2000)
     assert zc.status(reset=True) == zc.ZC_OK
     assert got.flatten().tolist() == [128.0] * 3
+
+
+# ------------------------------------------------------------------ every number of experts
+
+SORTS = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+from lossless_bf16_compression_gb300 import moe
+experts, wide = int(sys.argv[2]), sys.argv[3] == "wide"
+for slots, k in ((2, 2), (3000, 3)):
+    ids = (torch.arange(slots, device="cuda") * 7 % (experts + 1)).view(-1, k)
+    key = ids.reshape(-1)
+    order = torch.argsort(key, stable=True)
+    want = torch.empty_like(order)
+    want[order] = torch.arange(slots, device="cuda")
+    starts = torch.searchsorted(key[order], torch.arange(experts + 1, device="cuda"))
+    x = torch.arange(slots // k * 4, device="cuda").view(-1, 4).float()
+    for plan in (moe.sort(ids if wide else ids.int(), experts), moe.dispatch(x, ids if wide else ids.int(), experts)[1]):
+        assert torch.equal(plan.position.reshape(-1).long(), want) and torch.equal(plan.offsets.long(), starts)
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("experts,ids", [(765, "int"), (766, "int"), (767, "int"), (767, "wide"), (768, "wide"), (1023, "int")])
+def test_sort_of_as_many_experts_as_the_first_call_asks_for(experts, ids):
+    """In a process of its own: what an earlier call asked of the device does not help this one."""
+    r = subprocess.run([sys.executable, "-c", SORTS, ROOT, str(experts), ids], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr
+
+
+def test_sorts_of_two_threads():
+    """One thread's call does not take back what the other's needs."""
+    import threading
+
+    from lossless_bf16_compression_gb300 import _tensors
+
+    fn, calls, codes = _tensors.fn("zc_moe_sort"), 300, []
+    ids = torch.zeros(2000, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+
+    def work(experts):
+        position, offsets = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (2000, experts + 1))
+        scratch = torch.empty(_tensors.fn("zc_moe_sort_workspace")(2000, experts), dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        codes.extend(fn(ids.data_ptr(), 4, 1000, 2, experts, position.data_ptr(), offsets.data_ptr(), scratch.data_ptr(),
+                        stream.cuda_stream) for _ in range(calls))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(e,)) for e in (1024, 800, 900)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert codes == [zc.ZC_OK] * (3 * calls)
