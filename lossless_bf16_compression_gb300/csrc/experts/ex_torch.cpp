@@ -387,7 +387,7 @@ PyObject* weight_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {  // dy, 
   const at::ScalarType type = out_type(args[9]);
   const Tensor out = empty({groups, dy.data.size(0), x.data.size(0)}, type, x.data);
   call(lib.zc_fp8_weight_grad(dy.data.data_ptr(), dy.scales.data_ptr(), dy.format, x.data.data_ptr(),
-                              x.scales.data_ptr(), x.format, x.cols / kBlock, static_cast<int>(groups), out.size(1),
+                              x.scales.data_ptr(), x.format, ceil_div(x.cols, kBlock), static_cast<int>(groups), out.size(1),
                               out.size(2), at, out.data_ptr(), type_of(type), current(device)),
        "zc_fp8_weight_grad");
   return THPVariable_Wrap(out);

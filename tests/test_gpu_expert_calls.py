@@ -222,3 +222,25 @@ def test_sorts_of_two_threads():
     for t in threads:
         t.join()
     assert codes == [zc.ZC_OK] * (3 * calls)
+
+
+# ------------------------------------------------------------------ matrices of a program's own making
+
+
+def dequantized(m):
+    s = torch.exp2(m.scales.double() - 127).transpose(0, 1).reshape(m.rows, -1)[:, : m.data.shape[1] // 128]
+    return m.values().double() * s.repeat_interleave(128, 1)[:, : m.cols]
+
+
+def test_weight_grad_of_rows_that_end_inside_a_block():
+    """Blocks along the rows of two matrices, with starts of the program's own: the last block counts though it is not full.
+    Sums of 300 terms in fp32 (tolerance as for the products' tests: 300 2^-23 of the terms' magnitudes)."""
+    a, b = fp8.quantize(values((5, 300), torch.float32, 1)), fp8.quantize(values((7, 300), torch.float32, 2))
+    starts_of = torch.tensor([0, 2, 2, 3], dtype=torch.int32, device="cuda")
+    dy, x = (fp8.Matrix(m.data, m.scales, 300, offsets=starts_of) for m in (a, b))
+    got = fp8.weight_grad(dy, x, torch.float32).double()
+    assert zc.status(reset=True) == zc.ZC_OK
+    va, vb = dequantized(a), dequantized(b)
+    for g, (lo, hi) in enumerate(((0, 256), (256, 256), (256, 300))):
+        p, q = va[:, lo:hi], vb[:, lo:hi]
+        assert ((got[g] - p @ q.T).abs() <= 300 * 2.0 ** -23 * (p.abs() @ q.abs().T)).all()
