@@ -322,6 +322,8 @@ PyObject* scale_values(PyObject*, PyObject* const* a, Py_ssize_t n) {  // scales
   expect(n, 1);
   const Device device;
   const Tensor& scales = tensor(a[0], "scales", device, kBytes, 0);
+  TORCH_CHECK_VALUE(scales.is_contiguous() && scales.numel() % 4 == 0, "scales must be contiguous words of four bytes, got ",
+                    scales.sizes());
   const Tensor out = empty(scales.sizes(), at::kFloat, scales);
   call(lib.zc_fp8_scale_values(scales.data_ptr(), static_cast<size_t>(scales.numel()) / 4, out.data_ptr<float>(),
                                current(device)),
@@ -349,7 +351,16 @@ struct Operand {
   int64_t cols;
   Operand(PyObject* const* a, const char* name, const Device& device, int64_t dim)
       : data(tensor(a[0], name, device, kBytes, dim)), scales(tensor(a[1], "scales", device, kBytes, 0)),
-        format(static_cast<int>(number(a[2]))), cols(number(a[3])) {}
+        format(static_cast<int>(number(a[2]))), cols(number(a[3])) {
+    // A Matrix is checked when it is made, but its tensors can be exchanged: what the kernels read is looked at here.
+    const bool grouped = data.dim() == 3;
+    const int64_t blocks = ceil_div(cols, kBlock);
+    TORCH_CHECK_VALUE(cols >= 0 && (grouped || data.dim() == 2) && data.size(-1) == blocks * kBlock &&
+                          scales.numel() == (grouped ? data.size(0) : 1) * data.size(-2) * ceil_div(blocks, 4) * 4 &&
+                          data.is_contiguous() && scales.is_contiguous(),
+                      name, " must hold contiguous rows of ", cols, " values and a scale for each block, got ",
+                      data.sizes(), " and scales ", scales.sizes());
+  }
 };
 at::ScalarType out_type(PyObject* o) { return number(o) == ZC_TYPE_FP32 ? at::kFloat : at::kBFloat16; }
 

@@ -39,6 +39,8 @@ class Matrix:
             raise TypeError("data and scales must be uint8")
         if data.device != scales.device:
             raise ValueError(f"data is on {data.device}, scales on {scales.device}")
+        if offsets is not None and not (isinstance(offsets, torch.Tensor) and offsets.dtype == torch.int32):
+            raise TypeError("offsets must be an int32 tensor")
         if not (data.is_contiguous() and scales.is_contiguous()):
             raise ValueError("data and scales must be contiguous")
         shape, pitch = data.shape, _pitch(cols)

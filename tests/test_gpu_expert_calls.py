@@ -244,3 +244,36 @@ def test_weight_grad_of_rows_that_end_inside_a_block():
     for g, (lo, hi) in enumerate(((0, 256), (256, 256), (256, 300))):
         p, q = va[:, lo:hi], vb[:, lo:hi]
         assert ((got[g] - p @ q.T).abs() <= 300 * 2.0 ** -23 * (p.abs() @ q.abs().T)).all()
+
+
+def test_exchanged_tensors_are_refused():
+    """A Matrix whose tensors were exchanged after it was made: no call reads past them."""
+    at = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+
+    def matrix(rows, cols):
+        m = fp8.quantize(values((rows, cols), torch.float32, rows))
+        return fp8.Matrix(m.data, m.scales, cols, offsets=at)
+
+    good = matrix(40, 300)
+    for change in (lambda m: setattr(m, "scales", m.scales[:, :39]), lambda m: setattr(m, "scales", m.scales[:0]),
+                   lambda m: setattr(m, "scales", m.scales.expand(2, 40, 4)[:, ::2]),
+                   lambda m: setattr(m, "data", matrix(41, 300).data), lambda m: setattr(m, "data", m.data[:, :256]),
+                   lambda m: setattr(m, "data", matrix(40, 500).data[:, :384]), lambda m: setattr(m, "data", m.data[0]),
+                   lambda m: setattr(m, "cols", 385), lambda m: setattr(m, "cols", 0), lambda m: setattr(m, "cols", -5)):
+        bad = matrix(40, 300)
+        change(bad)
+        for call in (lambda: fp8.matmul(good, bad), lambda: fp8.matmul(bad, good), lambda: fp8.weight_grad(good, bad),
+                     lambda: fp8.weight_grad(bad, good)):
+            with pytest.raises(ValueError):
+                call()
+    bad = matrix(40, 300)
+    bad.scales = torch.zeros((1, 40, 8), dtype=torch.uint8, device="cuda")[:, :, ::2]
+    with pytest.raises(ValueError):
+        bad.scale_values()
+    bad.scales = torch.zeros(7, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        bad.scale_values()
+    for offsets in ([0, 1], at.long(), at.tolist()):
+        with pytest.raises(TypeError):
+            fp8.Matrix(good.data, good.scales, 300, offsets=offsets)
+    assert fp8.matmul(good, good).shape == (40, 40) and fp8.weight_grad(good, good).shape == (2, 40, 40)
