@@ -7,6 +7,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -65,7 +66,8 @@ class Device {
   c10::DeviceIndex number() const { return n_ < 0 ? n_ = c10::cuda::current_device() : n_; }
 };
 
-// A tensor on the current device, of one of the types, with `dim` dimensions (0: any).
+// A tensor on the current device, of one of the types, with `dim` dimensions (0: any).  One that requires a
+// gradient is refused while gradients are recorded: results have no history, so training would lose it unseen.
 const Tensor& tensor(PyObject* o, const char* name, const Device& device, unsigned types, int64_t dim) {
   TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a CUDA tensor");
   const Tensor& t = THPVariable_Unpack(o);
@@ -75,6 +77,10 @@ const Tensor& tensor(PyObject* o, const char* name, const Device& device, unsign
                    names(types));
   TORCH_CHECK_VALUE(dim == 0 || t.dim() == dim, name, " must have ", dim, " dimensions, got ", t.sizes());
   TORCH_CHECK_VALUE(t.get_device() == device.number(), name, " is on ", t.device(), ", not on the current device");
+  // (asked in this order, since few tensors require a gradient)
+  TORCH_CHECK(!t.requires_grad() || !c10::GradMode::is_enabled(), name, " requires a gradient, which this call would not "
+              "pass on: its gradient is a call of its own (detach the tensor, or call under torch.no_grad or in a "
+              "torch.autograd.Function)");
   return t;
 }
 int64_t number(PyObject* o) {

@@ -9,6 +9,9 @@
 A scale is the smallest power of two that brings its block's largest finite magnitude into the format's range, so
 scaling is exact and only the rounding to 8 bits loses anything.  Sums are taken in float32.  Every call runs on
 ``stream`` (default: the current one) and does not synchronize.
+
+Results have no autograd history: the gradients are the calls above.  A tensor that requires a gradient is refused while
+gradients are recorded; use these calls under ``torch.no_grad``, on detached tensors or in a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 

@@ -9,6 +9,9 @@
 or one that another rank holds): its row lies behind all experts' rows, holds zeros and adds nothing.  Values are
 bfloat16, float16 or float32; sums are taken in float32, in slot order, and rounded once.  Tensors may have any row
 stride.  Every call runs on ``stream`` (default: the current one) and does not synchronize.
+
+Results have no autograd history: the gradients are the calls above.  A tensor that requires a gradient is refused while
+gradients are recorded; use these calls under ``torch.no_grad``, on detached tensors or in a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 

@@ -277,3 +277,40 @@ def test_exchanged_tensors_are_refused():
         with pytest.raises(TypeError):
             fp8.Matrix(good.data, good.scales, 300, offsets=offsets)
     assert fp8.matmul(good, good).shape == (40, 40) and fp8.weight_grad(good, good).shape == (2, 40, 40)
+
+
+# ------------------------------------------------------------------ tensors that require a gradient
+
+
+def test_a_gradient_is_not_lost_unseen():
+    """A result would have no history, so an input that requires a gradient is refused where gradients are recorded, and
+    taken where they are not: under no_grad, detached, in a function's forward."""
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    x = values((4, 256), torch.float32, 1).requires_grad_()
+    w = values((4, 2), torch.float32, 2).requires_grad_()
+    rows, plan = moe.dispatch(x.detach(), ids, 3)
+    calls = [lambda t: moe.dispatch(t(x), ids, 3), lambda t: moe.combine(rows, t(w), plan),
+             lambda t: moe.combine(t(rows.clone().requires_grad_()), w.detach(), plan),
+             lambda t: moe.combine_grad(t(x), rows, w.detach(), plan), lambda t: moe.dispatch_grad(t(rows.clone().requires_grad_()), plan),
+             lambda t: fp8.quantize(t(x)), lambda t: fp8.quantize_columns(t(x)), lambda t: fp8.quantize_weight(t(x))]
+    for call in calls:
+        with pytest.raises(RuntimeError, match="requires a gradient"):
+            call(lambda v: v)
+        call(lambda v: v.detach())
+        with torch.no_grad():
+            call(lambda v: v)
+        with torch.inference_mode():
+            call(lambda v: v)
+
+    class Dispatch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, t):
+            r, ctx.plan = moe.dispatch(t, ids, 3)
+            return r
+
+        @staticmethod
+        def backward(ctx, d):
+            return moe.dispatch_grad(d, ctx.plan)
+
+    Dispatch.apply(x).sum().backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2.0))
