@@ -196,7 +196,7 @@ int zc_status(cudaStream_t stream, int reset);
 #define ZC_KERNEL_REFIT_ENCODE 9 /* ... and the encode kernel again, after it */
 
 /* enable != 0: bracket every kernel the library launches from now on with CUDA events on the
- * kernel's own stream.  enable == 0: stop recording.  Returns ZC_OK or ZC_ERR_CUDA. */
+ * kernel's own stream (those of zc_moe.h have their ids there).  enable == 0: stop recording.  Returns ZC_OK or ZC_ERR_CUDA. */
 int zc_timing_enable(int enable);
 
 /* Wait for the recorded events, write up to `max` (kernel id, milliseconds) pairs, oldest

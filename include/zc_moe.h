@@ -38,6 +38,20 @@ extern "C" {
 #define ZC_MOE_MAX_SLOTS ((size_t)1 << 30)
 #define ZC_FP8_BLOCK 128
 
+/* ------------------------------------------------------------------ kernel timing
+ *
+ * The kernels' ids in the records of zc_timing_collect (zc.h). */
+
+#define ZC_KERNEL_MOE_SORT 16         /* both kernels of a sort */
+#define ZC_KERNEL_MOE_DISPATCH 17     /* with the sort, where one launch does both */
+#define ZC_KERNEL_MOE_COMBINE 18      /* and the gradient of dispatch */
+#define ZC_KERNEL_MOE_COMBINE_GRAD 19
+#define ZC_KERNEL_FP8_ROWS 20         /* zc_fp8_quantize */
+#define ZC_KERNEL_FP8_COLUMNS 21      /* and the block starts, where they take a launch of their own */
+#define ZC_KERNEL_FP8_WEIGHT 22
+#define ZC_KERNEL_FP8_SCALES 23       /* zc_fp8_scale_values */
+#define ZC_KERNEL_FP8_PRODUCT 24      /* both products, and the clearing of a workspace */
+
 /* ------------------------------------------------------------------ tokens sorted by expert
  *
  * T tokens with k slots each; slot s = t k + j asks for expert ids[s].  An id outside

@@ -32,6 +32,15 @@ ZC_KERNEL_MEDIUM = 6
 ZC_KERNEL_FUSED = 7
 ZC_KERNEL_REFIT_STATS = 8
 ZC_KERNEL_REFIT_ENCODE = 9
+ZC_KERNEL_MOE_SORT = 16
+ZC_KERNEL_MOE_DISPATCH = 17
+ZC_KERNEL_MOE_COMBINE = 18
+ZC_KERNEL_MOE_COMBINE_GRAD = 19
+ZC_KERNEL_FP8_ROWS = 20
+ZC_KERNEL_FP8_COLUMNS = 21
+ZC_KERNEL_FP8_WEIGHT = 22
+ZC_KERNEL_FP8_SCALES = 23
+ZC_KERNEL_FP8_PRODUCT = 24
 
 ERROR_NAMES = {
     ZC_OK: "ZC_OK",

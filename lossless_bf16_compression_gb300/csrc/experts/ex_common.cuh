@@ -133,8 +133,9 @@ cudaError_t allow_shared_memory(size_t most) {
   return err;
 }
 
-// A launch; early: it may start while the kernel before it in the stream still runs (whoever
-// launched that one), so the kernel calls wait_for_previous before it touches memory.  Two kernels
+// A launch, with CUDA events around it under the kernel's id while timing is enabled (zc_timing_enable).
+// It may start while the kernel before it in the stream still runs (whoever launched that one), so the
+// kernel calls wait_for_previous before it touches memory.  Two kernels
 // read before their wait what the kernel before them does not write: place_kernel the ids and
 // dispatch_kernel x.  They are only launched behind count_kernel and place_kernel, which let the next
 // kernel start after their own wait, when all that came earlier in the stream is done.
@@ -143,8 +144,7 @@ cudaError_t allow_shared_memory(size_t most) {
 // it that nothing but the kernel's own accesses touches such memory, the wait included, and load
 // before it.
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool early,
-                   A... args) {
+cudaError_t launch(int id, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -154,8 +154,11 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cud
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  cfg.numAttrs = 1;
+  TimingRecord t = timing_begin(id, stream);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  timing_end(t, stream);
+  return err;
 }
 
 // (Clobbers memory: no access that the compiler knows of crosses it.)

@@ -706,7 +706,10 @@ cudaError_t launch_tiles(TileParams& t, const uint8_t* pv, size_t p_pitch, size_
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<G>, t, p_map, q_map);
+  TimingRecord rec = timing_begin(ZC_KERNEL_FP8_PRODUCT, stream);
+  err = cudaLaunchKernelEx(&cfg, matmul_kernel<G>, t, p_map, q_map);
+  timing_end(rec, stream);
+  return err;
 }
 
 __global__ void __launch_bounds__(1024) clear_kernel(uint4* to) {
@@ -794,7 +797,8 @@ cudaError_t launch_matmul(const Product& p, const DeviceInfo& dev, cudaStream_t 
   if (shape.share) {
     t.arrivals = static_cast<unsigned*>(p.workspace);
     t.parts = reinterpret_cast<float*>(t.arrivals + kArrivals);
-    const cudaError_t err = launch(clear_kernel, 1, kArrivals / 4, 0, stream, true, static_cast<uint4*>(p.workspace));
+    const cudaError_t err = launch(ZC_KERNEL_FP8_PRODUCT, clear_kernel, 1, kArrivals / 4, 0, stream,
+                                   static_cast<uint4*>(p.workspace));
     if (err != cudaSuccess) return err;
   }
   return launch_any(t, shape, p.b, blocks * kBlock, p.groups, p.a, blocks * kBlock, p.waits, dev, stream);

@@ -454,9 +454,10 @@ cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, 
     using T = decltype(t);
     const auto go = [&](auto per_warp) {
       constexpr int R = per_warp();
-      return launch(quantize_kernel<T, vec(), f(), R>, static_cast<unsigned>(ceil_div(rows, kRowWarps * R) * words),
-                    32 * kRowWarps, 0, stream, true, static_cast<const T*>(x), pitch, rows, static_cast<int>(cols),
-                    static_cast<unsigned>(words), values, reinterpret_cast<uint32_t*>(scales));
+      return launch(ZC_KERNEL_FP8_ROWS, quantize_kernel<T, vec(), f(), R>,
+                    static_cast<unsigned>(ceil_div(rows, kRowWarps * R) * words), 32 * kRowWarps, 0, stream,
+                    static_cast<const T*>(x), pitch, rows, static_cast<int>(cols), static_cast<unsigned>(words), values,
+                    reinterpret_cast<uint32_t*>(scales));
     };
     // four rows a warp once that still gives every SM a few CTAs; one row a warp below
     return ceil_div(rows, kRowWarps * 4) * words >= 2048 ? go(std::integral_constant<int, vec() ? 4 : 2>{})
@@ -465,7 +466,7 @@ cudaError_t launch_quantize(const void* x, size_t pitch, int type, size_t rows, 
 }
 
 cudaError_t launch_scale_values(const void* scales, size_t words, float* out, cudaStream_t stream) {
-  return launch(scale_values_kernel, static_cast<unsigned>(ceil_div(words, 256)), 256, 0, stream, true,
+  return launch(ZC_KERNEL_FP8_SCALES, scale_values_kernel, static_cast<unsigned>(ceil_div(words, 256)), 256, 0, stream,
                 static_cast<const uint32_t*>(scales), words, reinterpret_cast<float4*>(out));
 }
 
@@ -476,16 +477,17 @@ cudaError_t launch_quantize_columns(const void* x, size_t pitch, int type, size_
   const bool inline_groups =
       capacity > 0 && groups <= kInlineGroups && capacity * ceil_div(cols, kColumns) <= kInlineCtas;
   if (!inline_groups) {
-    const cudaError_t err = launch(block_offsets_kernel, 1, 1024, 0, stream, true, offsets, static_cast<int>(rows),
-                                   groups, block_offsets, status);
+    const cudaError_t err = launch(ZC_KERNEL_FP8_COLUMNS, block_offsets_kernel, 1, 1024, 0, stream, offsets,
+                                   static_cast<int>(rows), groups, block_offsets, status);
     if (err != cudaSuccess || capacity == 0) return err;
   }
   const dim3 grid(static_cast<unsigned>(capacity), static_cast<unsigned>(ceil_div(cols, kColumns)));
   return variant(type, vector_rows(x, pitch, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(inline_groups ? quantize_columns_kernel<T, vec(), f(), true>
+    return launch(ZC_KERNEL_FP8_COLUMNS,
+                  inline_groups ? quantize_columns_kernel<T, vec(), f(), true>
                                 : quantize_columns_kernel<T, vec(), f(), false>,
-                  grid, kColumnThreads, 0, stream, true, static_cast<const T*>(x), pitch, static_cast<int>(rows),
+                  grid, kColumnThreads, 0, stream, static_cast<const T*>(x), pitch, static_cast<int>(rows),
                   static_cast<int>(cols), groups, offsets, static_cast<int>(capacity), values, scales, block_offsets,
                   status);
   });
@@ -498,8 +500,9 @@ cudaError_t launch_quantize_weight(const void* w, int type, int groups, size_t r
                   static_cast<unsigned>(groups));
   return variant(type, vector_rows(w, cols, type), fmt, [&](auto t, auto vec, auto f) {
     using T = decltype(t);
-    return launch(quantize_weight_kernel<T, vec(), f()>, grid, 256, 0, stream, true, static_cast<const T*>(w),
-                  static_cast<int>(rows), static_cast<int>(cols), values, scales, values_t, scales_t);
+    return launch(ZC_KERNEL_FP8_WEIGHT, quantize_weight_kernel<T, vec(), f()>, grid, 256, 0, stream,
+                  static_cast<const T*>(w), static_cast<int>(rows), static_cast<int>(cols), values, scales, values_t,
+                  scales_t);
   });
 }
 

@@ -266,7 +266,8 @@ __device__ __forceinline__ uint4 settle(const Loaded& l, const uint8_t* row, int
 template <typename T, bool Aligned, int Batch>
 __global__ void __launch_bounds__(kMaxThreads) combine_grad_kernel(
     const uint8_t* d_out, size_t d_out_pitch, const uint8_t* rows, size_t rows_pitch, const float* weights,
-    uint8_t* d_rows, size_t d_rows_pitch, float* d_weights, int bytes, size_t tokens, int k, const int* position, const int* total, int* status) {
+    uint8_t* d_rows, size_t d_rows_pitch, float* d_weights, int bytes, size_t tokens, int k, const int* position,
+    const int* total, int* status) {
   constexpr int N = 16 / sizeof(T);
   __shared__ float sums[Batch][kMaxThreads / 32];
   let_next_start();
@@ -357,8 +358,9 @@ cudaError_t launch_dispatch(const RowShape& s, const void* x, size_t x_pitch, vo
   const Cut cut = cut_row(row_vectors(s.hidden * b, aligned), kMaxThreads);
   return by_size(s.type, aligned, [&](auto a, auto e) {
     const unsigned together = kMaxThreads / cut.threads;  // tokens of a CTA
-    return launch(dispatch_kernel<a(), e()>, static_cast<unsigned>((s.tokens + together - 1) / together) * cut.parts,
-                  dim3(cut.threads, together), 0, stream, true, static_cast<const uint8_t*>(x), x_pitch * b,
+    return launch(ZC_KERNEL_MOE_DISPATCH, dispatch_kernel<a(), e()>,
+                  static_cast<unsigned>((s.tokens + together - 1) / together) * cut.parts,
+                  dim3(cut.threads, together), 0, stream, static_cast<const uint8_t*>(x), x_pitch * b,
                   static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(s.hidden * b), cut.parts, s.tokens,
                   s.k, position, offsets + s.experts, status);
   });
@@ -375,10 +377,11 @@ cudaError_t launch_small_dispatch(const RowShape& s, const void* ids, int id_byt
   return by_size(s.type, aligned, [&](auto a, auto e) {
     const auto go = [&](auto* p) {
       using Id = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
-      return launch(small_dispatch_kernel<Id, a(), e()>, static_cast<unsigned>(s.tokens) * cut.parts, threads, 0,
-                    stream, true, p, static_cast<int>(s.tokens * s.k), s.experts, static_cast<const uint8_t*>(x),
-                    x_pitch * b, static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(s.hidden * b),
-                    cut.parts, s.k, position, offsets);
+      return launch(ZC_KERNEL_MOE_DISPATCH, small_dispatch_kernel<Id, a(), e()>,
+                    static_cast<unsigned>(s.tokens) * cut.parts, threads, 0, stream, p,
+                    static_cast<int>(s.tokens * s.k), s.experts, static_cast<const uint8_t*>(x), x_pitch * b,
+                    static_cast<uint8_t*>(rows), rows_pitch * b, static_cast<int>(s.hidden * b), cut.parts, s.k,
+                    position, offsets);
     };
     return id_bytes == 8 ? go(static_cast<const long long*>(ids)) : go(static_cast<const int*>(ids));
   });
@@ -392,9 +395,10 @@ cudaError_t launch_combine(const RowShape& s, const void* rows, size_t rows_pitc
   const size_t vecs = row_vectors(s.hidden * b, aligned);
   const Cut cut = cut_row(aligned ? vecs : (vecs + kTaking - 1) / kTaking * 32, kCombineThreads);
   const auto go = [&](auto type, auto a, auto tokens) {
-    return launch(weights ? combine_kernel<decltype(type), a(), tokens(), true>
+    return launch(ZC_KERNEL_MOE_COMBINE,
+                  weights ? combine_kernel<decltype(type), a(), tokens(), true>
                           : combine_kernel<decltype(type), a(), tokens(), false>,
-                  static_cast<unsigned>((s.tokens + tokens() - 1) / tokens()) * cut.parts, cut.threads, 0, stream, true,
+                  static_cast<unsigned>((s.tokens + tokens() - 1) / tokens()) * cut.parts, cut.threads, 0, stream,
                   static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(out),
                   out_pitch * b, static_cast<int>(s.hidden * b), cut.parts, s.tokens, s.k, position,
                   offsets + s.experts, status);
@@ -421,8 +425,9 @@ cudaError_t launch_combine_grad(const RowShape& s, const void* d_out, size_t d_o
   // 7168: 582 and 576).
   const unsigned most = s.tokens < 2048 ? 256 : vecs <= 256 ? 64 : 128;
   const auto go = [&](auto type, auto a, auto batch) {
-    return launch(combine_grad_kernel<decltype(type), a(), batch()>, static_cast<unsigned>(s.tokens),
-                  cut_row(vecs, most).threads, 0, stream, true, static_cast<const uint8_t*>(d_out), d_out_pitch * b,
+    return launch(ZC_KERNEL_MOE_COMBINE_GRAD, combine_grad_kernel<decltype(type), a(), batch()>,
+                  static_cast<unsigned>(s.tokens),
+                  cut_row(vecs, most).threads, 0, stream, static_cast<const uint8_t*>(d_out), d_out_pitch * b,
                   static_cast<const uint8_t*>(rows), rows_pitch * b, weights, static_cast<uint8_t*>(d_rows),
                   d_rows_pitch * b, d_weights, static_cast<int>(s.hidden * b), s.tokens, s.k, position,
                   offsets + s.experts, status);

@@ -140,10 +140,10 @@ cudaError_t launch_sort(const void* ids, int id_bytes, size_t slots, int experts
     if (kSortWarps * row > kPlainShared)
       err = allow_shared_memory<place_kernel<Id>>(kSortWarps * sizeof(int) * (ZC_MOE_MAX_EXPERTS + 1));
     if (err == cudaSuccess && runs > 1)
-      err = launch(count_kernel<Id>, runs, kSortThreads, row, stream, true, p, n, run, experts, counts);
+      err = launch(ZC_KERNEL_MOE_SORT, count_kernel<Id>, runs, kSortThreads, row, stream, p, n, run, experts, counts);
     if (err == cudaSuccess)
-      err = launch(place_kernel<Id>, runs, kSortThreads, kSortWarps * row, stream, true, p, n, run, runs, experts,
-                   counts, position, offsets);
+      err = launch(ZC_KERNEL_MOE_SORT, place_kernel<Id>, runs, kSortThreads, kSortWarps * row, stream, p, n, run, runs,
+                   experts, counts, position, offsets);
     return err;
   };
   return id_bytes == 8 ? go(static_cast<const long long*>(ids)) : go(static_cast<const int*>(ids));

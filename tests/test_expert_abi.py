@@ -49,3 +49,15 @@ def test_weight_grad_takes_what_quantize_columns_makes():
     assert rc(most + 1) == INV
     if not os.path.exists("/dev/nvidia0"):
         assert rc(most) == zc.ZC_ERR_CUDA == rc(rows // 128 + 1)
+
+
+def test_kernel_ids_match_the_header():
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    found = {}
+    for name in ("zc.h", "zc_moe.h"):
+        found |= dict(re.findall(r"^#define\s+(ZC_KERNEL_\w+)\s+(\d+)", open(os.path.join(root, "include", name)).read(), flags=re.M))
+    assert len(set(found.values())) == len(found) == 18
+    for name, value in found.items():
+        assert getattr(zc, name) == int(value), name

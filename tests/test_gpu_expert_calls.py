@@ -314,3 +314,58 @@ def test_a_gradient_is_not_lost_unseen():
 
     Dispatch.apply(x).sum().backward()
     assert torch.equal(x.grad, torch.full_like(x, 2.0))
+
+
+# ------------------------------------------------------------------ kernel timing
+
+
+def test_every_kernel_is_timed():
+    """zc_timing_enable brackets every kernel that the library launches, the experts' among them."""
+    x, w = values((1000, 256), torch.bfloat16, 1), values((1000, 4), torch.float32, 2)
+    ids = routing(1000, 4, 9, 3)
+    few = starts((3, 0, 5))
+    a = fp8.quantize(values((8, 7168), torch.bfloat16, 4))
+
+    def step():
+        """The calls, and the ids of the kernels that each launches."""
+        s, d, c, cg = zc.ZC_KERNEL_MOE_SORT, zc.ZC_KERNEL_MOE_DISPATCH, zc.ZC_KERNEL_MOE_COMBINE, zc.ZC_KERNEL_MOE_COMBINE_GRAD
+        q, col, wt, sc, p = (zc.ZC_KERNEL_FP8_ROWS, zc.ZC_KERNEL_FP8_COLUMNS, zc.ZC_KERNEL_FP8_WEIGHT, zc.ZC_KERNEL_FP8_SCALES,
+                             zc.ZC_KERNEL_FP8_PRODUCT)
+        out, kernels = [], []
+
+        def take(values_, *names):
+            out.extend(v for v in values_ if isinstance(v, torch.Tensor))
+            kernels.extend(names)
+            return values_
+
+        rows, plan = take(moe.dispatch(x, ids, 9), s, s, d)
+        take([rows, *plan])
+        take(moe.dispatch(x[:7], ids[:7], 9), d)
+        take(moe.sort(ids[:7], 9), s)
+        back = take([moe.combine(rows, w, plan)], c)[0]
+        take(moe.combine_grad(back, rows, w, plan), cg)
+        take([moe.dispatch_grad(rows, plan)], c)
+        m = take([fp8.quantize(rows)], q)[0]
+        take([m.data, m.scales, m.scale_values()], sc)
+        b, b_t = take(fp8.quantize_weight(values((9, 96, 256), torch.bfloat16, 5)), wt)
+        y = take([fp8.matmul(m, b, plan.offsets)], p)[0]
+        dy, xc = take([fp8.quantize_columns(y, plan.offsets), fp8.quantize_columns(rows, plan.offsets)], col, col)
+        take([fp8.weight_grad(dy, xc), b_t.data], p)
+        v = take(fp8.quantize_weight(values((2, 1000, 7168), torch.bfloat16, 6), transposed=False), wt)[0]
+        v3 = fp8.Matrix(torch.cat([v.data, v.data[:1]]), torch.cat([v.scales, v.scales[:1]]), 7168)
+        take([fp8.matmul(a, v3, few)], p, p)  # shared out: its workspace is cleared first
+        return out, kernels
+
+    want, _ = step()
+    zc.zc_timing_enable(1)
+    zc.zc_timing_collect()
+    try:
+        got, kernels = step()
+        records = zc.zc_timing_collect()
+    finally:
+        zc.zc_timing_enable(0)
+    assert [k for k, _ in records] == kernels
+    assert all(0 < ms < 1000 for _, ms in records)
+    assert all(same_bits(p, q) for p, q in zip(want, got)) and len(want) == len(got)
+    step()
+    assert zc.zc_timing_collect() == []
