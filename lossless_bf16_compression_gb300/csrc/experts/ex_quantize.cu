@@ -247,8 +247,7 @@ __global__ void __launch_bounds__(1024) block_offsets_kernel(const int* offsets,
 
 struct TileShared {
   alignas(16) uint2 turned[kBlock * 16];  // [column][unit of 8 rows], the unit at place unit ^ (column / 8)
-  alignas(16) uint32_t amax[16][kBlock];  // 16-bit types: two columns a word
-  float inverse[kBlock];
+  uint32_t amax[8];                       // of each warp's values
 };
 
 // Eight values of each of eight rows (`rows` of them real), `left` of a row's in it.
@@ -388,10 +387,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3)
   bool odd;
   magnitudes<T, 8>(raw, words, odd);
   uint32_t m = __reduce_max_sync(~0u, largest<T>(words));
-  if (tid % 32 == 0) s.amax[0][tid / 32] = m;
+  if (tid % 32 == 0) s.amax[tid / 32] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, s.amax[0][i]);
+  for (int i = 0; i < 8; ++i) m = max(m, s.amax[i]);
   const int e = block_exponent(Bits<T>::fp32(m), Fmt);
   const float f = inverse_scale(e);
 #pragma unroll
