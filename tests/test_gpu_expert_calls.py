@@ -42,6 +42,11 @@ def values(shape, dtype, seed):
     return torch.randn(shape, generator=g, device="cuda").to(dtype)
 
 
+def two(s):
+    """2^s in 64 bits, by the bits."""
+    return ((s + 1023) << 52).view(torch.float64)
+
+
 def same_bits(a, b):
     return a.shape == b.shape and a.dtype == b.dtype and torch.equal(
         a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
@@ -228,7 +233,7 @@ def test_sorts_of_two_threads():
 
 
 def dequantized(m):
-    s = torch.exp2(m.scales.double() - 127).transpose(0, 1).reshape(m.rows, -1)[:, : m.data.shape[1] // 128]
+    s = two(m.scales.long() - 127).transpose(0, 1).reshape(m.rows, -1)[:, : m.data.shape[1] // 128]
     return m.values().double() * s.repeat_interleave(128, 1)[:, : m.cols]
 
 
@@ -369,3 +374,157 @@ def test_every_kernel_is_timed():
     assert all(same_bits(p, q) for p, q in zip(want, got)) and len(want) == len(got)
     step()
     assert zc.zc_timing_collect() == []
+
+
+# ------------------------------------------------------------------ sizes at which a call takes another kernel
+
+
+def check_rows(x, fmt):
+    """quantize(x) against the definition in 64 bits, on the GPU: each scale the smallest power of two that brings the
+    block's largest value into the format, each value one of the two neighbours on the format's grid, the nearer one, at
+    a tie the one with the even last bit."""
+    from moe_oracle import grid_values
+
+    top = {"e4m3": 448.0, "e5m2": 57344.0}[fmt]
+    grid = torch.from_numpy(grid_values(fmt)).cuda()
+    m = fp8.quantize(x, fmt)
+    r, c = x.shape
+    blocks = -(-c // 128)
+    for a in range(0, r, 4096):
+        wide = torch.zeros((min(4096, r - a), blocks * 128), dtype=torch.float64, device="cuda")
+        wide[:, :c] = x[a:a + 4096].double()
+        wide = wide.view(wide.shape[0], blocks, 128)
+        amax = wide.abs().amax(2)
+        words = m.scales[:, a:a + 4096].permute(1, 0, 2).reshape(wide.shape[0], -1).long() - 127
+        assert not words[:, blocks:].any()
+        s = words[:, :blocks]
+        scale = two(s)
+        zero = amax == 0
+        assert (amax <= top * scale).all() and ((amax > top * scale / 2) | (s == -127) | zero).all() and not s[zero].any()
+        v = wide / scale[..., None]
+        got = m.data[a:a + 4096].view(torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2).double().view(v.shape)
+        hi = torch.searchsorted(grid, v.abs().contiguous()).clamp(max=grid.numel() - 1)
+        lo = (hi - 1).clamp(min=0)
+        up, down = grid[hi] - v.abs(), v.abs() - grid[lo]
+        want = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), grid[hi], grid[lo])
+        assert torch.equal(got, torch.copysign(want, v))
+
+
+# from 2048 CTAs of four rows a warp on, a warp takes four rows (two where rows start anywhere): sizes on either side,
+# a last warp and a last CTA that are not full, and a last word of scales that is not
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(32768, 300), (32749, 296), (32751, 301), (8195, 2048), (8197, 1999), (6000, 2504)])
+def test_quantize_many_rows(rows, cols, dtype, fmt):
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randn((rows, cols), generator=g, device="cuda").mul_(1.5).sub_(3).exp_()
+    x *= torch.where(torch.rand((rows, cols), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    x[torch.rand((rows, cols), generator=g, device="cuda") < 0.01] = 0
+    x[rows // 2, :] = 0
+    check_rows(x.to(dtype), fmt)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,k,hidden,shift", [(600, 3, 7001, 0), (600, 3, 4600, 3), (2100, 2, 2055, 1), (2100, 3, 7168, 0),
+                                                   (2049, 5, 4099, 1), (2050, 1, 8200, 0)])
+def test_rows_of_several_parts(tokens, k, hidden, shift, dtype):
+    """Rows of more than one CTA's or one warp's vectors, aligned or starting anywhere, in calls of more than 1024 slots and
+    on either side of 2048 tokens.  Sums: k products of fp32, or hidden of them, and a rounding (test_gpu_moe.py)."""
+    experts = 11
+    wide = values((tokens, hidden + shift), dtype, 1)
+    x, d_out = wide[:, shift:], values((tokens, hidden + 2 * shift), dtype, 2)[:, shift:shift + hidden]
+    ids, w = routing(tokens, k, experts, 3, dropped=0.2), values((tokens, k), torch.float32, 4)
+    rows, plan = moe.dispatch(x, ids, experts)
+    at, kept = plan.position.long(), (ids >= 0)[..., None]
+    assert same_bits(rows[at], torch.where(kept, x[:, None, :], torch.zeros((), dtype=dtype, device="cuda")))
+    assert plan.offsets[-1].item() == int(kept.sum())
+
+    eps, last = 2.0 ** -24, {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}[dtype]
+    sources = values((tokens * k, hidden + shift), dtype, 5)[:, shift:]
+    r = torch.where(kept, sources.double()[at], 0.0)
+
+    def close(got, want, size, count, rounding):
+        err = count * eps * size
+        assert ((got.double() - want).abs() <= err + rounding * (want.abs() + err)).all()
+
+    p = r * w.double()[..., None]
+    close(moe.combine(sources, w, plan), p.sum(1), p.abs().sum(1), k, last)
+    close(moe.dispatch_grad(sources, plan), r.sum(1), r.abs().sum(1), k, last)
+    d_rows, d_w = moe.combine_grad(d_out, sources, w, plan)
+    want = torch.where(kept, d_out.double()[:, None, :] * w.double()[..., None], 0.0)
+    close(d_rows[at], want, want.abs(), 1, last)
+    p = r * d_out.double()[:, None, :]
+    close(d_w, p.sum(2), p.abs().sum(2), hidden + 1, eps)
+
+
+@pytest.mark.parametrize("counts,n,k", [((1,) * 40 + (1500,) + (0,) * 10, 260, 300), ((2, 900) + (0,) * 60, 140, 6000),
+                                        ((0,) * 5 + (3000,) + (1,) * 7, 700, 520), ((1000,) + (0,) * 1000, 130, 129)])
+def test_products_of_a_group_with_most_of_the_rows(counts, n, k):
+    """Tiles are cut for the average group: one group of many times as many rows, products and weight gradient (tolerances
+    as in test_gpu_fp8.py: the number of terms times 2^-23 of their magnitudes)."""
+    at = starts(counts)
+    rows, e = int(at[-1]), len(counts)
+    a, (b, _) = fp8.quantize(values((rows, k), torch.bfloat16, 1)), fp8.quantize_weight(values((e, n, k), torch.bfloat16, 2))
+    got, av = fp8.matmul(a, b, at, torch.float32).double(), dequantized(a)
+    dy, x = fp8.quantize_columns(values((rows, n), torch.bfloat16, 3), at), fp8.quantize_columns(values((rows, k), torch.bfloat16, 4), at)
+    dw, yv, xv, blocks = fp8.weight_grad(dy, x, torch.float32).double(), dequantized(dy), dequantized(x), dy.offsets.tolist()
+    assert zc.status(reset=True) == zc.ZC_OK
+    for g in range(e):
+        if counts[g] == 0:
+            assert not dw[g].any()
+            continue
+        s = slice(at[g].item(), at[g + 1].item())
+        bv = dequantized(fp8.Matrix(b.data[g], b.scales[g], k))
+        assert ((got[s] - av[s] @ bv.T).abs() <= k * 2.0 ** -23 * (av[s].abs() @ bv.abs().T)).all()
+        s = slice(128 * blocks[g], 128 * blocks[g + 1])
+        p, q = yv[:, s], xv[:, s]
+        assert ((dw[g] - p @ q.T).abs() <= p.shape[1] * 2.0 ** -23 * (p.abs() @ q.abs().T)).all()
+
+
+# ------------------------------------------------------------------ NaN, infinities, subnormals, the largest values
+
+
+def patterns(dtype):
+    """[512, 128]: every pattern of a 16-bit type, or 65,536 of 32 bits over all exponents and both signs, shuffled."""
+    g = torch.Generator().manual_seed(3)
+    bits = torch.arange(1 << 16, dtype=torch.int64)
+    if dtype == torch.float32:
+        low = torch.randint(0, 1 << 16, (1 << 16,), generator=g)
+        low[::5] = 0  # (so that infinities are among them)
+        bits = bits << 16 | low
+        bits = torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(torch.int32)
+    else:
+        bits = torch.where(bits >= 1 << 15, bits - (1 << 16), bits).to(torch.int16)
+    return bits[torch.randperm(1 << 16, generator=g)].view(dtype).view(512, 128)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("ordered", [False, True])
+def test_every_quantization_of_every_value(dtype, fmt, ordered):
+    """Rows, columns and weights against the 64-bit statements, values and scales for equality: blocks of values of all
+    magnitudes with NaN and infinities among them, and (ordered) blocks of neighbours, finite or not as a whole."""
+    from moe_oracle import doubles, quantize, quantize_blocks, quantize_columns, unpack_scales
+
+    x = patterns(dtype)
+    if ordered:
+        key = x.view(torch.int16 if dtype != torch.float32 else torch.int32).reshape(-1)
+        x = key.sort().values.view(dtype).view(512, 128)
+    x = x.cuda()
+
+    def check(m, v, s):
+        got = m.values().float().cpu().numpy().astype(np.float64)
+        assert np.array_equal(got, v, equal_nan=True) and np.array_equal(np.signbit(got[v == 0]), np.signbit(v[v == 0]))
+        assert np.array_equal(unpack_scales(m.scales.cpu().numpy(), s.shape[1]), s)
+
+    check(fp8.quantize(x, fmt), *quantize(doubles(x), fmt))
+    turned = x.t().contiguous()  # a column of 128 x 512 is a row of x
+    check(fp8.quantize_columns(turned, None, fmt), *quantize_columns(doubles(turned), np.array([0, 128]), fmt)[:2])
+    w = x.reshape(4, 128, 128)
+    m, t = fp8.quantize_weight(w, fmt)
+    v, s = quantize_blocks(doubles(w).reshape(1, 4, 128 * 128), fmt)
+    for e in range(4):
+        ve, se = v[0, e].reshape(128, 128), np.full((128, 1), s[0, e])
+        check(fp8.Matrix(m.data[e], m.scales[e], 128, fmt), ve, se)
+        check(fp8.Matrix(t.data[e], t.scales[e], 128, fmt), ve.T, se)
+
