@@ -272,10 +272,10 @@ __device__ __forceinline__ uint4 get_column(const TileShared& s, int c, int i) {
 }
 
 // 128 rows x 64 columns a CTA, thread (row group tid / 8, column group tid % 8) with 8 x 8 values.  Bound by HBM as
-// long as enough loads are in flight while other CTAs turn their tiles: 32768 x 7168, bf16, takes 115 us (6.2
+// long as enough loads are in flight while other CTAs turn their tiles: 32768 x 7168, bf16, takes 113 us (6.3
 // TB/s) with nine CTAs to an SM, 119 with eight, 123 with seven, 121 with ten, which spill, and 123 with CTAs of 128
-// columns; rows that start anywhere, with a vector more to load for each, 90 us for 16384 x 7167 with
-// six (aligned 63).
+// columns; rows that start anywhere, with a vector more to load for each, 88 us for 16384 x 7167 with
+// six (aligned 63; six spill 8 to 16 bytes, and five CTAs of fp32 12 to 28).
 //
 // Inline: every CTA counts the blocks before its own, one group a thread, and the first writes
 // block_offsets, which saves a launch; otherwise they come from block_offsets_kernel.  With many
@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(kColumnThreads, sizeof(T) == 4 ? (Vec ? 5 : 4)
 }
 
 // One scale for the tile; its rows are written from registers, its transpose through shared memory
-// (16 matrices of 4096 x 7168, bf16, both written: 297 us, 6.3 TB/s).
+// (16 matrices of 4096 x 7168, bf16, both written: 297 us, 6.3 TB/s).  Of the tile's 64 values a thread, aligned
+// 16-bit ones spill 8 bytes at four CTAs to an SM, unaligned ones 88 to 116 at three, unaligned fp32 16 to 20 at two.
 template <typename T, bool Vec, int Fmt>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : Vec ? 4 : 3)
     quantize_weight_kernel(const T* w, int rows, int cols, uint8_t* values, uint8_t* scales, uint8_t* values_t,

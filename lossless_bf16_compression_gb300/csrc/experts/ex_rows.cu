@@ -4,8 +4,8 @@
 // the traffic there is, and every sum over j runs inside one thread in slot order (no atomics).
 // Bound by HBM when there are many tokens, by two dependent loads (position, then row) when there
 // are few; so a thread asks for the rows of eight slots before it uses the first.  16384 tokens x 8 x
-// 7168, bf16: dispatch 320 us (6.6 TB/s), combine 317 (6.7), combine's gradient 576 (7.3, part of it from the
-// L2); one token 8, 8 and 13 us with the launches, of which the sort's part is in dispatch.
+// 7168, bf16: dispatch 321 us (6.6 TB/s; with the sort), combine 298 (7.1), combine's gradient 578 (6.9, part of
+// it from the L2); one token, calls from Python back to back: 5.5, 3.8 and 6.6 us.
 #include <initializer_list>
 
 #include "ex_common.cuh"
@@ -181,7 +181,8 @@ __device__ __forceinline__ uint4 vector_at(const uint8_t* row, int from, int byt
 // out[t] = sum over j of weights[t, j] rows[position[t, j]].  A thread takes Tokens tokens that follow
 // one another, with a share of each one's slots at a time: as many rows in flight however few slots a
 // token has.
-// (Nine CTAs to an SM: 16384 x 8 x 7167 with weights 381 us, without the bound on registers 394, ten 423.)
+// (Nine CTAs to an SM, with weights spilling 32 to 48 bytes: 16384 x 8 x 7167 with weights 374 us; measured before
+// the positions were checked ahead of the loads: nine 381, without the bound on registers 394, ten 423.)
 template <typename T, bool Aligned, int Tokens, bool Weighted>
 __global__ void __launch_bounds__(kCombineThreads, !Aligned && Tokens == 1 ? 9 : 0)
     combine_kernel(const uint8_t* rows, size_t rows_pitch, const float* weights, uint8_t* out, size_t out_pitch,
