@@ -41,7 +41,7 @@ def fn(name):
     return f
 
 
-def _native():
+def _load():
     try:
         from . import _experts
     except ImportError as e:
@@ -51,7 +51,19 @@ def _native():
     return _experts
 
 
-native = _native()  # the calls on tensors: checks, outputs, launch, on the current device and stream
+class _NotBuilt:
+    """Stands for the extension module in a checkout that is not built yet: a call loads it, or says what is missing."""
+
+    def __getattr__(self, name):
+        module = _load()
+        self.__dict__.update((k, v) for k, v in vars(module).items() if not k.startswith("__"))
+        return getattr(module, name)
+
+
+try:
+    native = _load()  # the calls on tensors: checks, outputs, launch, on the current device and stream
+except (ImportError, RuntimeError):
+    native = _NotBuilt()
 
 
 def on(stream, used, f, *args):

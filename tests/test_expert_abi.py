@@ -61,3 +61,33 @@ def test_kernel_ids_match_the_header():
     assert len(set(found.values())) == len(found) == 18
     for name, value in found.items():
         assert getattr(zc, name) == int(value), name
+
+
+def test_a_checkout_that_is_not_built_says_so_on_first_use():
+    """moe and fp8 import without the extension module (a checkout that is not built yet); their first call says what is
+    missing."""
+    import subprocess
+    import sys
+
+    code = """
+import sys
+name = "lossless_bf16_compression_gb300._experts"
+sys.modules[name] = None  # as if it were not there
+import torch
+from lossless_bf16_compression_gb300 import fp8, moe
+for call in (lambda: moe.sort(torch.zeros((2, 2), dtype=torch.int32), 4), lambda: fp8.quantize(torch.zeros((2, 2)))) * 2:
+    try:
+        call()
+    except ImportError as e:
+        assert "build" in str(e), e
+    else:
+        raise SystemExit("no error")
+del sys.modules[name]
+try:
+    moe.sort(torch.zeros((2, 2), dtype=torch.int32), 4)  # built by now: refused for the tensor
+except TypeError:
+    print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr
