@@ -1,4 +1,4 @@
-"""What the tensor-level calls of ``moe`` and ``fp8`` share: the native calls, streams, the C entry points."""
+""": the native calls, streams, the C entry points."""
 from __future__ import annotations
 
 import ctypes
@@ -7,7 +7,7 @@ import torch
 
 from . import binding
 
-_P, _N, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_P, _N, _I, _F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 
 # (restype, argtypes) of every entry point of zc_moe.h.
 SIGNATURES = {
@@ -28,6 +28,19 @@ SIGNATURES = {
     "zc_fp8_weight_grad_stall_test": (_I, [_P, _P, _I, _P, _P, _I, _N, _I, _N, _N, _P, _P, _I, _P, _I, _I]),
 }
 
+# Those of zc_router.h and zc_int4.h.
+ROUTER_SIGNATURES = {
+    "zc_moe_route": (_I, [_P, _N, _I, _N, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "zc_moe_balance_workspace": (_N, [_N, _I]),
+    "zc_moe_balance": (_I, [_P, _N, _I, _P, _N, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "zc_moe_route_grad": (_I, [_P, _P, _P, _P, _P, _N, _I, _N, _I, _I, _I, _I, _F, _P, _N, _P]),
+}
+INT4_SIGNATURES = {
+    "zc_int4_quantize": (_I, [_P, _I, _I, _N, _N, _P, _P, _P]),
+    "zc_int4_values": (_I, [_P, _P, _I, _N, _N, _I, _P, _P]),
+    "zc_int4_matmul": (_I, [_P, _N, _I, _N, _P, _P, _I, _N, _N, _P, _P, _N, _I, _P]),
+}
+
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MAX_EXPERTS = 1024
 MAX_K = 64
@@ -37,7 +50,7 @@ def fn(name):
     """An entry point of the library with its argument types set, for callers that have addresses instead of
     tensors; raises when the library is not built."""
     f = getattr(binding.lib(), name)
-    f.restype, f.argtypes = SIGNATURES[name]
+    f.restype, f.argtypes = (SIGNATURES | ROUTER_SIGNATURES | INT4_SIGNATURES)[name]
     return f
 
 

@@ -41,6 +41,12 @@ ZC_KERNEL_FP8_COLUMNS = 21
 ZC_KERNEL_FP8_WEIGHT = 22
 ZC_KERNEL_FP8_SCALES = 23
 ZC_KERNEL_FP8_PRODUCT = 24
+ZC_KERNEL_MOE_ROUTE = 25
+ZC_KERNEL_MOE_ROUTE_GRAD = 26
+ZC_KERNEL_MOE_BALANCE = 27
+ZC_KERNEL_INT4_WEIGHT = 28
+ZC_KERNEL_INT4_VALUES = 29
+ZC_KERNEL_INT4_PRODUCT = 30
 
 ERROR_NAMES = {
     ZC_OK: "ZC_OK",

@@ -1,7 +1,8 @@
-// ex_api.cu -- the entry points of zc_moe.h: argument checks and launches.
+// ex_api.cu -- the entry points of zc_moe.h, zc_router.h and zc_int4.h: argument checks and launches.
 #include <initializer_list>
 
-#include "ex_common.cuh"
+#include "ex_int4.cuh"
+#include "ex_router.cuh"
 
 using namespace zc;
 
@@ -46,6 +47,17 @@ size_t scales_bytes(size_t rows, size_t cols) { return rows * ((blocks_of(cols) 
 
 bool slots_ok(size_t tokens, int k, int experts) {
   return k >= 1 && k <= ZC_MOE_MAX_K && groups_ok(experts) && tokens <= ZC_MOE_MAX_SLOTS / static_cast<size_t>(k);
+}
+
+bool score_ok(int score) { return score == ZC_SCORE_SOFTMAX || score == ZC_SCORE_SIGMOID; }
+bool router_ok(size_t tokens, int experts, int k, int type, int score) {
+  return slots_ok(tokens, k, experts) && k <= experts && type_ok(type) && score_ok(score);
+}
+
+constexpr size_t kMaxRecords = size_t(1) << 31;  // 2 TB
+bool int4_ok(int groups, size_t n, size_t k) {
+  return groups_ok(groups) && n >= 1 && n <= kMaxCols && k >= 1 && k <= kMaxCols &&
+         static_cast<size_t>(groups) * ex::Int4Shape{n, k}.records() <= kMaxRecords;
 }
 
 int check_sort(const void* ids, int id_bytes, size_t tokens, int k, int experts, const int* position,
@@ -321,6 +333,121 @@ int zc_fp8_weight_grad_stall_test(const void* a, const void* a_scales, int a_fmt
                                   int stalled_cta, unsigned wait_us) {
   return weight_grad(a, a_scales, a_fmt, b, b_scales, b_fmt, capacity, groups, n, k, block_offsets, out, out_type,
                      stream, {1000ull * wait_us, stalled_cta});
+}
+
+// ------------------------------------------------------------------ zc_router.h
+
+int zc_moe_route(const void* logits, size_t pitch, int type, size_t tokens, int experts, int k, int score,
+                 int normalize, float scale, float* weights, int* ids, cudaStream_t stream) {
+  if (!router_ok(tokens, experts, k, type, score) || pitch < static_cast<size_t>(experts)) return ZC_ERR_INVALID_ARG;
+  if (tokens == 0) return ZC_OK;
+  if (!logits || !weights || !ids) return ZC_ERR_INVALID_ARG;
+  if (!aligned(logits, ex::type_bytes(type)) || !aligned(weights, 4) || !aligned(ids, 4)) return ZC_ERR_MISALIGNED;
+  const size_t slots = tokens * k;
+  if (clash({{weights, 4 * slots}, {ids, 4 * slots}}, {{logits, rows_bytes(tokens, pitch, experts, type)}}))
+    return ZC_ERR_INVALID_ARG;
+  return finish(ex::launch_route({tokens, experts, k, type, score, normalize, scale}, logits, pitch, weights, ids, stream));
+}
+
+size_t zc_moe_balance_workspace(size_t tokens, int experts) {
+  return groups_ok(experts) && tokens <= ZC_MOE_MAX_SLOTS ? ex::balance_workspace(tokens, experts) : 0;
+}
+
+int zc_moe_balance(const void* logits, size_t pitch, int type, const int* ids, size_t tokens, int experts, int k,
+                   int score, float* loss, int* counts, float* slope, void* workspace, cudaStream_t stream) {
+  if (!slots_ok(tokens, k, experts) || !type_ok(type) || !score_ok(score) || pitch < static_cast<size_t>(experts) || !loss ||
+      !counts || !slope || (tokens && (!logits || !ids)))
+    return ZC_ERR_INVALID_ARG;
+  const size_t scratch = ex::balance_workspace(tokens, experts), e = experts;
+  if (scratch && !workspace) return ZC_ERR_INVALID_ARG;
+  if (!aligned(logits, ex::type_bytes(type)) || !aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
+      !aligned(slope, 4) || !aligned(workspace, 16))
+    return ZC_ERR_MISALIGNED;
+  if (clash({{loss, 4}, {counts, 4 * e}, {slope, 4 * e}, {workspace, scratch}},
+            {{logits, rows_bytes(tokens, pitch, experts, type)}, {ids, 4 * tokens * k}}))
+    return ZC_ERR_INVALID_ARG;
+  return finish(ex::launch_balance({tokens, experts, k, type, score, 0, 1.0f}, logits, pitch, ids, loss, counts, slope,
+                                   workspace, stream));
+}
+
+int zc_moe_route_grad(const float* d_weights, const int* ids, const float* d_loss, const float* slope,
+                      const void* logits, size_t pitch, int type, size_t tokens, int experts, int k, int score,
+                      int normalize, float scale, void* d_logits, size_t d_pitch, cudaStream_t stream) {
+  if (!slots_ok(tokens, k, experts) || !type_ok(type) || !score_ok(score) || pitch < static_cast<size_t>(experts) ||
+      d_pitch < static_cast<size_t>(experts) || !d_loss != !slope)
+    return ZC_ERR_INVALID_ARG;
+  if (tokens == 0) return ZC_OK;
+  if (!logits || !d_logits || !d_weights != !ids || (!d_weights && !slope)) return ZC_ERR_INVALID_ARG;
+  const size_t b = ex::type_bytes(type), slots = tokens * k, e = experts;
+  if (!aligned(logits, b) || !aligned(d_logits, b) || !aligned(d_weights, 4) || !aligned(ids, 4) || !aligned(d_loss, 4) ||
+      !aligned(slope, 4))
+    return ZC_ERR_MISALIGNED;
+  if (clash({{d_logits, rows_bytes(tokens, d_pitch, experts, type)}},
+            {{logits, rows_bytes(tokens, pitch, experts, type)},
+             {d_weights, d_weights ? 4 * slots : 0},
+             {ids, ids ? 4 * slots : 0},
+             {d_loss, d_loss ? size_t(4) : 0},
+             {slope, slope ? 4 * e : 0}}))
+    return ZC_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
+  return finish(ex::launch_route_grad({tokens, experts, k, type, score, normalize, scale}, d_weights, ids, d_loss, slope,
+                                      logits, pitch, d_logits, d_pitch, dev, stream));
+}
+
+// ------------------------------------------------------------------ zc_int4.h
+
+int zc_int4_quantize(const void* w, int type, int groups, size_t n, size_t k, void* values, void* scales,
+                     cudaStream_t stream) {
+  if (!type_ok(type) || !int4_ok(groups, n, k) || !w || !values || !scales) return ZC_ERR_INVALID_ARG;
+  if (!aligned(w, ex::type_bytes(type)) || !aligned(values, 16) || !aligned(scales, 16)) return ZC_ERR_MISALIGNED;
+  const size_t g = groups;
+  const ex::Int4Shape s{n, k};
+  if (clash({{values, g * s.records() * ex::kInt4Record}, {scales, g * s.records() * 2 * ex::kInt4Rows}},
+            {{w, g * n * k * ex::type_bytes(type)}}))
+    return ZC_ERR_INVALID_ARG;
+  return finish(ex::launch_int4_quantize(w, type, g, s, static_cast<uint8_t*>(values),
+                                         static_cast<__nv_bfloat16*>(scales), stream));
+}
+
+int zc_int4_values(const void* values, const void* scales, int groups, size_t n, size_t k, int type, void* out,
+                   cudaStream_t stream) {
+  if (!type_ok(type) || !int4_ok(groups, n, k) || !values || !scales || !out) return ZC_ERR_INVALID_ARG;
+  if (!aligned(out, ex::type_bytes(type)) || !aligned(values, 16) || !aligned(scales, 16)) return ZC_ERR_MISALIGNED;
+  const size_t g = groups;
+  const ex::Int4Shape s{n, k};
+  if (clash({{out, g * n * k * ex::type_bytes(type)}},
+            {{values, g * s.records() * ex::kInt4Record}, {scales, g * s.records() * 2 * ex::kInt4Rows}}))
+    return ZC_ERR_INVALID_ARG;
+  return finish(ex::launch_int4_values(static_cast<const uint8_t*>(values), static_cast<const __nv_bfloat16*>(scales), g, s,
+                                       type, out, stream));
+}
+
+int zc_int4_matmul(const void* x, size_t x_pitch, int type, size_t rows, const void* values, const void* scales,
+                   int groups, size_t n, size_t k, const int* offsets, void* out, size_t out_pitch, int out_type,
+                   cudaStream_t stream) {
+  if (!type_ok(type) || !type_ok(out_type) || !int4_ok(groups, n, k) || rows > kMaxRows || x_pitch < k || out_pitch < n ||
+      (!offsets && groups != 1))
+    return ZC_ERR_INVALID_ARG;
+  if (rows == 0) return ZC_OK;
+  if (!x || !values || !scales || !out) return ZC_ERR_INVALID_ARG;
+  if (!aligned(x, ex::type_bytes(type)) || !aligned(out, ex::type_bytes(out_type)) || !aligned(values, 16) ||
+      !aligned(scales, 16) || !aligned(offsets, 4))
+    return ZC_ERR_MISALIGNED;
+  const size_t g = groups;
+  const ex::Int4Shape s{n, k};
+  if (clash({{out, rows_bytes(rows, out_pitch, n, out_type)}},
+            {{x, rows_bytes(rows, x_pitch, k, type)},
+             {values, g * s.records() * ex::kInt4Record},
+             {scales, g * s.records() * 2 * ex::kInt4Rows},
+             {offsets, offsets ? 4 * (g + 1) : 0}}))
+    return ZC_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (const cudaError_t err = device_info(&dev); err != cudaSuccess) return finish(err);
+  return finish(ex::launch_int4_matmul({x, x_pitch, type, rows, static_cast<const uint8_t*>(values),
+                                        static_cast<const __nv_bfloat16*>(scales), groups, s, offsets, out, out_pitch,
+                                        out_type},
+                                       dev, stream));
 }
 
 }  // extern "C"

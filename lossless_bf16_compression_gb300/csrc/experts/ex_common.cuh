@@ -144,21 +144,28 @@ cudaError_t allow_shared_memory(size_t most) {
 // it that nothing but the kernel's own accesses touches such memory, the wait included, and load
 // before it.
 template <typename... P, typename... A>
-cudaError_t launch(int id, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch_clusters(int id, int cluster, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   TimingRecord t = timing_begin(id, stream);
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
   timing_end(t, stream);
   return err;
+}
+template <typename... P, typename... A>
+cudaError_t launch(int id, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  return launch_clusters(id, 1, kernel, grid, block, smem, stream, args...);
 }
 
 // (Clobbers memory: no access that the compiler knows of crosses it.)

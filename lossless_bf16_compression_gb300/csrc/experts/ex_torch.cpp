@@ -1,4 +1,5 @@
-// ex_torch.cpp -- the Python module _experts: the entry points of zc_moe.h on torch tensors.
+// ex_torch.cpp -- the Python module _experts: the entry points of zc_moe.h, zc_router.h and zc_int4.h on torch
+// tensors.
 //
 // What a call from Python costs is its checks, its outputs and its launch.  Here they take 4 us (8-bit
 // blocks of 777 x 1000); the same steps made from Python one by one took 14, more than most kernels of a
@@ -14,11 +15,13 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <optional>
 #include <string>
 
-#include "zc_moe.h"
+#include "zc_int4.h"
+#include "zc_router.h"
 
 namespace {
 
@@ -27,7 +30,9 @@ using at::Tensor;
 #define FUNCTIONS(X)                                                                                        \
   X(zc_moe_sort_workspace) X(zc_moe_sort) X(zc_moe_dispatch) X(zc_moe_combine) X(zc_moe_combine_grad)       \
   X(zc_fp8_quantize) X(zc_fp8_scale_values) X(zc_fp8_column_blocks) X(zc_fp8_quantize_columns)              \
-  X(zc_fp8_quantize_weight) X(zc_fp8_matmul_workspace) X(zc_fp8_matmul) X(zc_fp8_weight_grad)
+  X(zc_fp8_quantize_weight) X(zc_fp8_matmul_workspace) X(zc_fp8_matmul) X(zc_fp8_weight_grad)             \
+  X(zc_moe_route) X(zc_moe_balance_workspace) X(zc_moe_balance) X(zc_moe_route_grad)                        \
+  X(zc_int4_quantize) X(zc_int4_values) X(zc_int4_matmul)
 struct {
 #define MEMBER(f) decltype(&::f) f;
   FUNCTIONS(MEMBER)
@@ -411,6 +416,179 @@ PyObject* weight_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {  // dy, 
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------------ the router
+
+struct Logits : Rows {
+  Logits(PyObject* o, const Device& device, int64_t tokens = -1) : Rows(rows_of(o, "logits", device, tokens)) {
+    TORCH_CHECK_VALUE(cols <= ZC_MOE_MAX_EXPERTS, "logits must have 1 to ", ZC_MOE_MAX_EXPERTS, " columns, got ", cols);
+  }
+};
+// What a routing chose: int32 (that is what moe.route returns), rows of k.
+Tensor chosen(PyObject* o, const Device& device) {
+  const Tensor& t = tensor(o, "experts_of", device, kInts, 2);
+  TORCH_CHECK_VALUE(t.size(1) >= 1 && t.size(1) <= ZC_MOE_MAX_K, "experts_of must have 1 to ", ZC_MOE_MAX_K,
+                    " columns, got ", t.size(1));
+  return t.contiguous();
+}
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return static_cast<float>(v);
+}
+
+PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {  // logits, k, score, normalize, scale
+  HANDLE_TH_ERRORS
+  expect(n, 5);
+  const Device device;
+  const Logits x(a[0], device);
+  const int64_t k = number(a[1]);
+  TORCH_CHECK_VALUE(k >= 1 && k <= ZC_MOE_MAX_K && k <= x.cols, "k must be 1 to ",
+                    std::min<int64_t>(ZC_MOE_MAX_K, x.cols), ", got ", k);
+  const Tensor weights = empty({x.rows, k}, at::kFloat, x.t), ids = empty({x.rows, k}, at::kInt, x.t);
+  call(lib.zc_moe_route(x.data(), x.pitch, x.type(), x.rows, static_cast<int>(x.cols), static_cast<int>(k),
+                        static_cast<int>(number(a[2])), a[3] == Py_True, real(a[4]), weights.data_ptr<float>(),
+                        ids.data_ptr<int>(), current(device)),
+       "zc_moe_route");
+  return results({&weights, &ids});
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* balance(PyObject*, PyObject* const* a, Py_ssize_t n) {  // logits, experts_of, score
+  HANDLE_TH_ERRORS
+  expect(n, 3);
+  const Device device;
+  const Tensor ids = chosen(a[1], device);
+  const Logits x(a[0], device, ids.size(0));
+  const Tensor loss = empty({}, at::kFloat, x.t), counts = empty({x.cols}, at::kInt, x.t),
+               slope = empty({x.cols}, at::kFloat, x.t);
+  const size_t need = lib.zc_moe_balance_workspace(x.rows, static_cast<int>(x.cols));
+  const Tensor scratch = need ? empty({static_cast<int64_t>(need)}, at::kByte, x.t) : Tensor();
+  call(lib.zc_moe_balance(x.data(), x.pitch, x.type(), ids.data_ptr<int>(), x.rows, static_cast<int>(x.cols),
+                          static_cast<int>(ids.size(1)), static_cast<int>(number(a[2])), loss.data_ptr<float>(),
+                          counts.data_ptr<int>(), slope.data_ptr<float>(), need ? scratch.data_ptr() : nullptr,
+                          current(device)),
+       "zc_moe_balance");
+  return results({&loss, &counts, &slope});
+  END_HANDLE_TH_ERRORS
+}
+
+// logits, d_weights or None, experts_of or None, d_loss or None, slope or None, score, normalize, scale
+PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 8);
+  const Device device;
+  const Logits x(a[0], device);
+  Tensor d_weights, ids, slope, d_loss;
+  if (a[1] != Py_None) {
+    ids = chosen(a[2], device);
+    d_weights = tensor(a[1], "d_weights", device, kFloats, 2).contiguous();
+    TORCH_CHECK_VALUE(ids.size(0) == x.rows, "experts_of must have ", x.rows, " rows, got ", ids.size(0));
+    TORCH_CHECK_VALUE(d_weights.sizes() == ids.sizes(), "d_weights must have the shape ", ids.sizes(), ", got ",
+                      d_weights.sizes());
+  }
+  if (a[3] != Py_None) {
+    d_loss = tensor(a[3], "d_loss", device, kFloats, 0);
+    TORCH_CHECK_VALUE(d_loss.numel() == 1, "d_loss must have one element, got ", d_loss.sizes());
+    slope = tensor(a[4], "slope", device, kFloats, 1).contiguous();
+    TORCH_CHECK_VALUE(slope.size(0) == x.cols, "slope must have ", x.cols, " elements, got ", slope.sizes());
+  }
+  const Tensor d = empty({x.rows, x.cols}, x.t.scalar_type(), x.t);
+  call(lib.zc_moe_route_grad(ids.defined() ? d_weights.data_ptr<float>() : nullptr,
+                             ids.defined() ? ids.data_ptr<int>() : nullptr,
+                             slope.defined() ? d_loss.data_ptr<float>() : nullptr,
+                             slope.defined() ? slope.data_ptr<float>() : nullptr, x.data(), x.pitch, x.type(), x.rows,
+                             static_cast<int>(x.cols), ids.defined() ? static_cast<int>(ids.size(1)) : 1,
+                             static_cast<int>(number(a[5])), a[6] == Py_True, real(a[7]), d.data_ptr(), x.cols,
+                             current(device)),
+       "zc_moe_route_grad");
+  return THPVariable_Wrap(d);
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------------ 4-bit weights
+
+// Records and scales of n x k weights, or of one such matrix for each group; checked at every call, since a Matrix's
+// tensors can be exchanged.
+struct Weights4 {
+  const Tensor &data, &scales;
+  int64_t n, k, groups;
+  Weights4(PyObject* const* a, const Device& device)
+      : data(tensor(a[0], "data", device, kBytes, 0)), scales(tensor(a[1], "scales", device, bit(at::kBFloat16), 0)),
+        n(number(a[2])), k(number(a[3])) {
+    const int64_t dim = data.dim();
+    groups = dim == 4 ? data.size(0) : 1;
+    const int64_t tiles = ceil_div(n, ZC_INT4_ROWS), blocks = ceil_div(k, ZC_INT4_GROUP);
+    TORCH_CHECK_VALUE(n >= 1 && k >= 1 && (dim == 3 || dim == 4) && data.size(dim - 3) == tiles &&
+                          data.size(dim - 2) == blocks && data.size(dim - 1) == ZC_INT4_GROUP * ZC_INT4_ROWS / 2 &&
+                          scales.numel() == groups * tiles * blocks * ZC_INT4_ROWS && data.is_contiguous() &&
+                          scales.is_contiguous(),
+                      "the records and scales of ", n, " x ", k, " weights do not have the shapes ", data.sizes(), " and ",
+                      scales.sizes());
+    TORCH_CHECK_VALUE(groups >= 1 && groups <= ZC_MOE_MAX_EXPERTS, "1 to ", ZC_MOE_MAX_EXPERTS, " experts, got ", groups);
+  }
+};
+
+PyObject* quantize4(PyObject*, PyObject* const* a, Py_ssize_t n) {  // w
+  HANDLE_TH_ERRORS
+  expect(n, 1);
+  const Device device;
+  Tensor w = tensor(a[0], "w", device, kRows, 0);
+  const int64_t dim = w.dim();
+  TORCH_CHECK_VALUE((dim == 2 || dim == 3) && w.numel() > 0, "w must be [n, k] or [experts, n, k], got ", w.sizes());
+  const int64_t groups = dim == 3 ? w.size(0) : 1, rows = w.size(dim - 2), cols = w.size(dim - 1);
+  TORCH_CHECK_VALUE(groups <= ZC_MOE_MAX_EXPERTS, "at most ", ZC_MOE_MAX_EXPERTS, " experts");
+  w = w.contiguous();
+  const int64_t tiles = ceil_div(rows, ZC_INT4_ROWS), blocks = ceil_div(cols, ZC_INT4_GROUP), skip = dim == 3 ? 0 : 1;
+  const int64_t d[4] = {groups, tiles, blocks, ZC_INT4_GROUP * ZC_INT4_ROWS / 2}, s[4] = {groups, tiles, blocks, ZC_INT4_ROWS};
+  const Tensor data = empty(at::IntArrayRef(d + skip, 4 - skip), at::kByte, w),
+               scales = empty(at::IntArrayRef(s + skip, 4 - skip), at::kBFloat16, w);
+  call(lib.zc_int4_quantize(w.data_ptr(), type_of(w.scalar_type()), static_cast<int>(groups), rows, cols, data.data_ptr(),
+                            scales.data_ptr(), current(device)),
+       "zc_int4_quantize");
+  return results({&data, &scales});
+  END_HANDLE_TH_ERRORS
+}
+
+constexpr at::ScalarType kTypes[] = {at::kBFloat16, at::kHalf, at::kFloat};  // by ZC_TYPE_*
+at::ScalarType type_at(PyObject* o) {
+  const int64_t i = number(o);
+  TORCH_CHECK_VALUE(i >= 0 && i < 3, "no such type: ", i);
+  return kTypes[i];
+}
+
+PyObject* values4(PyObject*, PyObject* const* a, Py_ssize_t n) {  // data, scales, n, k, type
+  HANDLE_TH_ERRORS
+  expect(n, 5);
+  const Device device;
+  const Weights4 w(a, device);
+  const at::ScalarType type = type_at(a[4]);
+  const int64_t d[3] = {w.groups, w.n, w.k}, skip = w.data.dim() == 4 ? 0 : 1;
+  const Tensor out = empty(at::IntArrayRef(d + skip, 3 - skip), type, w.data);
+  call(lib.zc_int4_values(w.data.data_ptr(), w.scales.data_ptr(), static_cast<int>(w.groups), w.n, w.k, type_of(type),
+                          out.data_ptr(), current(device)),
+       "zc_int4_values");
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* matmul4(PyObject*, PyObject* const* a, Py_ssize_t n) {  // x, data, scales, n, k, offsets or None, type or None
+  HANDLE_TH_ERRORS
+  expect(n, 7);
+  const Device device;
+  const Weights4 w(a + 1, device);
+  const Rows x = rows_of(a[0], "x", device, -1, w.k);
+  int64_t groups;
+  const int* at = starts(a[5], device, &groups);
+  TORCH_CHECK_VALUE(w.groups == groups, "the weights must be of ", groups, " experts, got ", w.data.sizes());
+  const at::ScalarType type = a[6] == Py_None ? x.t.scalar_type() : type_at(a[6]);
+  const Tensor out = empty({x.rows, w.n}, type, x.t);
+  call(lib.zc_int4_matmul(x.data(), x.pitch, x.type(), x.rows, w.data.data_ptr(), w.scales.data_ptr(),
+                          static_cast<int>(groups), w.n, w.k, at, out.data_ptr(), w.n, type_of(type), current(device)),
+       "zc_int4_matmul");
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 // ------------------------------------------------------------------ the module
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {  // the loaded library's handle, the class of its errors
@@ -444,6 +622,12 @@ PyMethodDef methods[] = {method("bind", bind),
                          method("values", values),
                          method("matmul", matmul),
                          method("weight_grad", weight_grad),
+                         method("route", route),
+                         method("balance", balance),
+                         method("route_grad", route_grad),
+                         method("quantize4", quantize4),
+                         method("values4", values4),
+                         method("matmul4", matmul4),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_experts", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
