@@ -15,28 +15,13 @@ namespace zc {
 namespace ex {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kTile = kWarps * kInt4Rows;  // weight rows of a CTA
-constexpr int kChunk = 8;                  // blocks of x in shared memory at a time
-constexpr int kAhead = 4;                  // blocks of weights in flight for each warp
-constexpr int kPitch = kTile + 4;          // of a column of partial sums (in fp32), free of bank conflicts
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kColumnPitch = 20;  // of 16 partial sums (in fp32), free of bank conflicts
+constexpr size_t kShared = 226 * 1024;
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A value in the same place of another CTA's shared memory.
-__device__ __forceinline__ float peer_value(uint32_t address, int rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
-               : "r"(address), "r"(rank)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void multiply(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -44,12 +29,45 @@ __device__ __forceinline__ void multiply(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Weights 2 p and 2 p + 1 of a word as two bfloat16 values.
-template <int P>
-__device__ __forceinline__ uint32_t pair(uint32_t word) {
-  const uint32_t v = (word >> 4 * P & 0x000F000Fu) | 0x43004300u;
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.0f));
-  return *reinterpret_cast<uint32_t*>(&r);
+__device__ __forceinline__ void multiply_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Two times 16 bytes, 512 apart, where `on` is set; else they are as they were, and not used.
+__device__ __forceinline__ void fetch_record(uint4& a, uint4& b, const void* p, int on) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+               "@q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%8];\n\t"
+               "@q ld.global.L1::no_allocate.v4.u32 {%4, %5, %6, %7}, [%8 + 512];\n\t}"
+               : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w), "+r"(b.x), "+r"(b.y), "+r"(b.z), "+r"(b.w)
+               : "l"(p), "r"(on));
+}
+// 16 bits where `on` is set; else `v` is as it was.
+__device__ __forceinline__ void fetch_scale(uint32_t& v, const void* p, int on) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
+               : "+r"(v)
+               : "l"(p), "r"(on));
+}
+
+
+// The eight weights of a word as pairs of bfloat16 values, weights 2 p and 2 p + 1 in the p-th, each q / 64.  The bits of
+// a nibble alone, in the low eight bits of a bfloat16, are a number too small to be normal, u 2^-133 or 16 u 2^-133,
+// and one fused multiply-add makes u / 64 - 8 / 64 of either, exactly.
+constexpr float kWeightUnit = 64.0f;
+__device__ __forceinline__ uint32_t fma_pair(uint32_t v, uint32_t times, uint32_t plus) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(times), "r"(plus));
+  return r;
+}
+struct Four {
+  uint32_t v[4];
+};
+__device__ __forceinline__ Four four(uint32_t word) {
+  const uint32_t up = word >> 8;
+  constexpr uint32_t k2_127 = 0x7F007F00u, k2_123 = 0x7D007D00u, kMinus = 0xBE00BE00u;
+  return {fma_pair(word & 0x000F000Fu, k2_127, kMinus), fma_pair(word & 0x00F000F0u, k2_123, kMinus),
+          fma_pair(up & 0x000F000Fu, k2_127, kMinus), fma_pair(up & 0x00F000F0u, k2_123, kMinus)};
 }
 
 // ------------------------------------------------------------------ rows of x as columns of bfloat16
@@ -94,80 +112,46 @@ __device__ __forceinline__ void split(const T (&v)[8], uint4 (&out)[Parts<T>::n]
   }
 }
 
-// Puts blocks first .. first + count - 1 of `rows` rows of x where the products read them: for each block and eight
-// columns 4 x 512 bytes, in the c-th of which lane 4 g + t finds values 32 t + 8 c .. + 7 of column g.
-template <typename T, int NT>
-__device__ __forceinline__ void stage(const T* x, size_t pitch, int rows, size_t first, int count, size_t k, bool aligned,
-                                      uint8_t* to) {
+// Puts `count` blocks of `rows` rows of x, from block `first` on, where the products read them: for each block and
+// eight columns 4 x 512 bytes, in the c-th of which lane 4 g + t finds values 32 t + 8 c .. + 7 of column g.  bfloat16 on
+// whole vectors is copied asynchronously: staged() waits for it.
+template <typename T>
+__device__ __forceinline__ void stage(const T* x, size_t pitch, int rows, int first, int count, size_t k, bool aligned,
+                                      int tiles, uint4* to) {
   const int vectors = count * (kInt4Group / 8);
-  for (int i = threadIdx.x; i < rows * vectors; i += kThreads) {
-    const int r = i / vectors, v = i % vectors;
-    const size_t col = first * kInt4Group + 8 * static_cast<size_t>(v);
-    const T* from = x + r * pitch + col;
-    alignas(16) T in[8];
-    if (aligned) {
+  for (int r = 0; r < rows; ++r) {
+    for (int v = threadIdx.x; v < vectors; v += kThreads) {
+      const size_t col = static_cast<size_t>(first) * kInt4Group + 8 * v;
+      const T* from = x + r * pitch + col;
+      const int block = v / 16, t = v % 16 / 4, c = v % 4;
+      const auto place = [&](int column) { return to + ((block * tiles + column / 8) * 4 + c) * 32 + column % 8 * 4 + t; };
+      if constexpr (Parts<T>::n == 1) {
+        if (aligned) {  // (past the end of the row: zeros)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(place(r))), "l"(col < k ? from : x),
+                       "r"(col < k ? 16 : 0)
+                       : "memory");
+          continue;
+        }
+      }
+      alignas(16) T in[8];
+      if (aligned) {
 #pragma unroll
-      for (int j = 0; j < 8; j += 16 / sizeof(T))
-        *reinterpret_cast<uint4*>(in + j) = load_if(from + j, col + j < k);
-    } else {
+        for (int j = 0; j < 8; j += 16 / sizeof(T)) *reinterpret_cast<uint4*>(in + j) = load_if(from + j, col + j < k);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) in[j] = col + j < k ? from[j] : from_float<T>(0.0f);
-    }
-    uint4 out[Parts<T>::n];
-    split<T>(in, out);
-    const int block = v / 16, t = v % 16 / 4, c = v % 4;
+        for (int j = 0; j < 8; ++j) in[j] = col + j < k ? from[j] : from_float<T>(0.0f);
+      }
+      uint4 out[Parts<T>::n];
+      split<T>(in, out);
 #pragma unroll
-    for (int p = 0; p < Parts<T>::n; ++p) {
-      const int column = r * Parts<T>::n + p;
-      reinterpret_cast<uint4*>(to)[((block * NT + column / 8) * 4 + c) * 32 + column % 8 * 4 + t] = out[p];
+      for (int p = 0; p < Parts<T>::n; ++p) *place(r * Parts<T>::n + p) = out[p];
     }
   }
 }
-
-// ------------------------------------------------------------------ groups
-
-struct Span {
-  int group, begin, end;
-};
-
-// The index-th group that has rows (group -1: there are not so many), found by the whole CTA.
-__device__ __forceinline__ Span find_group(const int* offsets, int groups, int rows, int index, int* status) {
-  __shared__ Span found;
-  __shared__ int counts[kWarps];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int each = (groups + kThreads - 1) / kThreads, first = threadIdx.x * each;
-  int mine = 0;
-  bool bad = false;
-  for (int i = 0; i < each; ++i) {
-    const int g = first + i;
-    if (g >= groups) break;
-    const int a = offsets[g], z = offsets[g + 1];
-    bad |= a < 0 || z < a || z > rows || (g == 0 && a != 0);
-    mine += min(max(z, 0), rows) > min(max(a, 0), rows);
-  }
-  if (bad) set_error(status, ZC_ERR_CORRUPT);
-  int before = mine;
-  for (int d = 1; d < 32; d *= 2) {
-    const int v = __shfl_up_sync(~0u, before, d);
-    if (lane >= d) before += v;
-  }
-  if (lane == 31) counts[warp] = before;
-  if (threadIdx.x == 0) found.group = -1;
+__device__ __forceinline__ void staged() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  before -= mine;
-  for (int w = 0; w < warp; ++w) before += counts[w];
-  if (index >= before && index < before + mine) {
-    for (int i = 0; i < each; ++i) {
-      const int g = first + i;
-      const int a = min(max(offsets[g], 0), rows), z = min(max(offsets[g + 1], 0), rows);
-      if (z > a && before++ == index) found = {g, a, z};
-    }
-  }
-  __syncthreads();
-  return found;
 }
-
-// ------------------------------------------------------------------ the product
 
 struct Job {
   const void* x;
@@ -179,7 +163,8 @@ struct Job {
   size_t out_pitch;
   int* status;
   Int4Shape w;
-  int rows, groups, out_type, slices;
+  int rows, groups, out_type;
+  int room;  // for x in shared memory: blocks of eight columns
   bool aligned;
 };
 
@@ -190,154 +175,371 @@ __device__ __forceinline__ void put(const Job& p, size_t row, size_t col, float 
   else static_cast<float*>(p.out)[at] = v;
 }
 
-template <int NT>
-constexpr size_t shared_bytes() {
-  const size_t x = static_cast<size_t>(kChunk) * NT * 2048, sums = sizeof(float) * 8 * NT * kPitch;
-  return x > sums ? x : sums;
+// ------------------------------------------------------------------ passes
+//
+// A pass is up to `each` rows of one group, the columns that the products take at once.  A pass of more columns takes
+// longer on the same weights (measured: by a third for sixteen instead of eight), so CTAs share the work by cost: 2 and
+// 1 for each eight columns begun.
+
+constexpr int cost_of(int columns) { return 2 + (columns + 7) / 8; }
+
+struct Pass {
+  int group, row, rows;
+};
+// In shared memory, of each group and past the last: its first row, first pass, and the cost before it.
+struct Passes {
+  int *start, *first, *cost;
+};
+
+template <int kEach, int kParts>
+__device__ __forceinline__ void find_passes(const Job& p, const Passes& s) {
+  __shared__ int2 sums[kWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  constexpr int kGroups = (ZC_MOE_MAX_EXPERTS + kThreads - 1) / kThreads;  // of a thread
+  int begin[kGroups], rows[kGroups];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const int g = threadIdx.x * kGroups + i;
+    begin[i] = rows[i] = 0;
+    if (g < p.groups) {
+      const int a = p.offsets ? p.offsets[g] : 0, z = p.offsets ? p.offsets[g + 1] : p.rows;
+      bad |= a < 0 || z < a || z > p.rows || (g == 0 && a != 0);
+      begin[i] = a;
+      rows[i] = z - a;
+    }
+  }
+  if (bad) set_error(p.status, ZC_ERR_CORRUPT);
+  bad = __syncthreads_or(bad);  // (then there are no passes: their rows could be anywhere)
+  const auto passes = [&](int i) { return (rows[i] + kEach - 1) / kEach; };
+  const auto cost = [&](int i) {
+    const int rest = rows[i] % kEach;
+    return rows[i] / kEach * cost_of(kEach * kParts) + (rest ? cost_of(rest * kParts) : 0);
+  };
+  int2 upto = make_int2(0, 0);
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    if (bad) begin[i] = rows[i] = 0;
+    upto.x += passes(i);
+    upto.y += cost(i);
+  }
+  const int2 mine = upto;
+  for (int d = 1; d < 32; d *= 2) {
+    const int x = __shfl_up_sync(~0u, upto.x, d), y = __shfl_up_sync(~0u, upto.y, d);
+    if (lane >= d) upto.x += x, upto.y += y;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  upto.x -= mine.x;
+  upto.y -= mine.y;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) upto.x += sums[w].x, upto.y += sums[w].y;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const int g = threadIdx.x * kGroups + i;
+    if (g < p.groups) s.start[g] = begin[i], s.first[g] = upto.x, s.cost[g] = upto.y;
+    upto.x += passes(i);
+    upto.y += cost(i);
+    if (g == p.groups - 1) s.start[g + 1] = bad ? p.rows : begin[i] + rows[i], s.first[g + 1] = upto.x, s.cost[g + 1] = upto.y;
+  }
+  __syncthreads();
+}
+// The last group whose entry is at most `value` (a group without passes has the next one's entry).
+__device__ __forceinline__ int group_of(const int* table, int groups, int value) {
+  int lo = 0, hi = groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (table[mid] <= value) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ Pass pass_at(const Passes& s, int groups, int each, int index) {
+  const int g = group_of(s.first, groups, index), row = s.start[g] + (index - s.first[g]) * each;
+  return {g, row, min(each, s.start[g + 1] - row)};
+}
+// The place, counted in lines of all passes, of a point of the total cost (`lines` times a pass's, line after line).
+template <int kEach, int kParts>
+__device__ __forceinline__ size_t line_at(const Passes& s, int groups, int lines, size_t point) {
+  const int g = group_of(s.cost, groups, static_cast<int>(point / lines));
+  if (point >= static_cast<size_t>(s.cost[groups]) * lines) return static_cast<size_t>(s.first[groups]) * lines;
+  const size_t in = point - static_cast<size_t>(s.cost[g]) * lines;
+  constexpr int kFull = cost_of(kEach * kParts);
+  const int rows = s.start[g + 1] - s.start[g], full = rows / kEach;
+  const size_t before = static_cast<size_t>(full) * kFull * lines;  // of the group's whole passes
+  const size_t line = in < before ? in / kFull : static_cast<size_t>(full) * lines + (in - before) / cost_of(rows % kEach * kParts);
+  return static_cast<size_t>(s.first[g]) * lines + line;
 }
 
+// ------------------------------------------------------------------ the product
+//
+// The work is a list of record rows, pass after pass, of which each CTA takes a run of equal length.  It goes through
+// them in rounds of up to a record row for each warp, of one pass; where fewer are left the warps share the blocks of
+// each, and their sums are added in their order.  The pass's x lies in shared memory, all of it where it fits, else
+// in chunks of k, one read while the next one comes in.  A warp asks for the first blocks of its next record row (or
+// chunk) while it works on the last ones of this.
+
+struct Phase {  // what a warp reads next: `count` records from this one on, and as many `apart` further on
+  uint32_t record, apart;
+  int count;
+};
+// Record rows side by side that a warp takes: with two, each fragment of x serves twice.
+template <int NT>
+constexpr int tiles_of_warp() { return NT <= 2 ? 2 : 1; }
+template <int NT>
+struct Sums {
+  float of[kWarps][tiles_of_warp<NT>()][8 * NT][kColumnPitch];
+};
+
 template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads) int4_product_kernel(const __grid_constant__ Job p) {
+__global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_constant__ Job p) {
   extern __shared__ __align__(16) uint8_t shared[];
-  constexpr int kParts = Parts<T>::n, kRowsAtOnce = 8 * NT / kParts;
+  constexpr int kParts = Parts<T>::n, kEach = 8 * NT / kParts;
+  constexpr int kTiles = tiles_of_warp<NT>(), kAhead = 4 / kTiles;  // blocks in flight for each warp: 4 KB
+  Sums<NT>& sums = *reinterpret_cast<Sums<NT>*>(shared);
+  uint4* xs = reinterpret_cast<uint4*>(shared + sizeof(Sums<NT>));
+  int* tables = reinterpret_cast<int*>(xs + p.room * 128);
+  const Passes passes{tables, tables + p.groups + 1, tables + 2 * (p.groups + 1)};
   wait_for_previous();
   let_next_start();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
-  const int rank = blockIdx.x % p.slices;
-  const size_t column0 = static_cast<size_t>(blockIdx.x / p.slices) * kTile;
-  Span span{0, 0, p.rows};
-  if (p.offsets != nullptr) {
-    if (blockIdx.y == gridDim.y - 1) {  // the rows behind the last group
-      const int end = min(max(p.offsets[p.groups], 0), p.rows);
-      if (rank == 0)
-        for (size_t i = threadIdx.x; i < static_cast<size_t>(p.rows - end) * kTile; i += kThreads)
-          if (column0 + i % kTile < p.w.n) put(p, end + i / kTile, column0 + i % kTile, 0.0f);
-      return;
-    }
-    span = find_group(p.offsets, p.groups, p.rows, blockIdx.y, p.status);
-    if (span.group < 0) return;
-  }
-  const size_t tiles = p.w.tiles(), blocks = p.w.blocks(), tile = column0 / kInt4Rows + warp;
-  const int per = static_cast<int>((blocks + p.slices - 1) / p.slices);
-  const size_t begin = min(blocks, static_cast<size_t>(rank) * per);
-  const int count = tile < tiles ? static_cast<int>(min(blocks, begin + per) - begin) : 0;  // of this warp
-  const int staged = static_cast<int>(min(blocks, begin + per) - begin);
-  const size_t record0 = (span.group * tiles + tile) * blocks + begin;
-  const uint8_t* values = p.values + record0 * kInt4Record + 16 * lane;
-  const __nv_bfloat16* scales = p.scales + record0 * kInt4Rows + g;
 
-  for (int row = span.begin; row < span.end; row += kRowsAtOnce) {
-    const int rows = min(kRowsAtOnce, span.end - row), columns = rows * kParts;
-    uint4 a[kAhead], b[kAhead];
-    float sa[kAhead], sb[kAhead];
-    const auto fetch = [&](int i, int block) {
-      const bool on = block < count;
-      a[i] = load_if(values + static_cast<size_t>(block) * kInt4Record, on);
-      b[i] = load_if(values + static_cast<size_t>(block) * kInt4Record + 512, on);
-      sa[i] = on ? __bfloat162float(scales[static_cast<size_t>(block) * kInt4Rows]) : 0.0f;
-      sb[i] = on ? __bfloat162float(scales[static_cast<size_t>(block) * kInt4Rows + 8]) : 0.0f;
-    };
+  find_passes<kEach, kParts>(p, passes);
+  // The rows behind the last group.
+  if (const int end = passes.start[p.groups]; end < p.rows) {
+    const size_t step = static_cast<size_t>(gridDim.x) * kThreads, last = static_cast<size_t>(p.rows - end) * p.w.n;
+    for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < last; i += step)
+      put(p, end + i / p.w.n, i % p.w.n, 0.0f);
+  }
+  // A line: kTiles record rows.
+  const int record_rows = static_cast<int>(p.w.tiles()), blocks = static_cast<int>(p.w.blocks());
+  const int lines_each = (record_rows + kTiles - 1) / kTiles;  // of a pass
+  const size_t all = static_cast<size_t>(passes.cost[p.groups]) * lines_each;
+  // (Lanes 0 and 1 look up this CTA's first line and the next one's.)
+  const size_t bound = line_at<kEach, kParts>(passes, p.groups, lines_each, all * (blockIdx.x + (lane & 1)) / gridDim.x);
+  const size_t begin = __shfl_sync(~0u, bound, 0);
+  int left = static_cast<int>(__shfl_sync(~0u, bound, 1) - begin);
+  if (left == 0) return;
+
+  int index = static_cast<int>(begin / lines_each);  // of the pass
+  int line = static_cast<int>(begin - static_cast<size_t>(index) * lines_each);
+  Pass pass = pass_at(passes, p.groups, kEach, index);
+
+  // What is in flight, and the scales, in the lanes: lane 4 g + t holds those of rows g and g + 8 of record
+  // t % kTiles of block t / kTiles.
+  uint4 a[kAhead][kTiles], b[kAhead][kTiles];
+  uint32_t scale_a = 0, scale_b = 0;
+  const auto fetch = [&](int i, const Phase& f) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i, i);
-    float sum[NT][4];
+    for (int h = 0; h < kTiles; ++h)
+      fetch_record(a[i][h], b[i][h],
+                   p.values + static_cast<size_t>(f.record + h * f.apart) * kInt4Record + i * kInt4Record + 16 * lane, i < f.count);
+  };
+  const auto fetch_scales = [&](const Phase& f) {  // (as they come: a warp would wait here for anything done with them)
+    const __nv_bfloat16* s = p.scales + static_cast<size_t>(f.record + t % kTiles * f.apart + t / kTiles) * kInt4Rows + g;
+    fetch_scale(scale_a, s, t / kTiles < f.count);
+    fetch_scale(scale_b, s + 8, t / kTiles < f.count);
+  };
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+  for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[n][i] = 0;
-    const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(row) * p.x_pitch;
-    for (int base = 0; base < staged; base += kAhead) {
-      if (base % kChunk == 0) {
-        __syncthreads();
-        stage<T, NT>(x, p.x_pitch, rows, begin + base, min(kChunk, staged - base), p.w.k, p.aligned, shared);
-        __syncthreads();
-      }
+    for (int h = 0; h < kTiles; ++h) a[i][h] = b[i][h] = make_uint4(0, 0, 0, 0);
+
+  // How a pass's x lies in shared memory: eight columns to a tile, and as many blocks at a time as there is room for.
+  const auto tiles_of = [&](const Pass& of) { return (of.rows * kParts + 7) / 8; };
+  const auto chunk_of = [&](const Pass& of) {
+    const int room = p.room / tiles_of(of);
+    return blocks <= room ? blocks : room / 2;
+  };
+  const auto length = [&](int chunk, int c) { return min(chunk, blocks - c * chunk); };
+  const auto lines_of = [&](int at) {  // of a round: a few are left over where that keeps more warps at work
+    const int most = min(kWarps, min(left, lines_each - at));
+    return most > kWarps / 2 && most < kWarps * 3 / 4 ? kWarps / 2 : most;
+  };
+  const auto phase = [&](const Pass& of, int first, int lines, int c) {
+    const int chunk = chunk_of(of), sharing = kWarps / lines, part = warp / lines, len = length(chunk, c);
+    const int sub = (len + sharing - 1) / sharing, at = part * sub, row = (first + warp % lines) * kTiles;
+    // (A record row past the last one: the first of the warp again, for sums that no one reads.)
+    return Phase{static_cast<uint32_t>((static_cast<size_t>(of.group) * record_rows + row) * blocks + c * chunk + at),
+                 row + 1 < record_rows ? static_cast<uint32_t>(blocks) : 0u, part < sharing ? max(0, min(sub, len - at)) : 0};
+  };
+  int half = 0;  // of the x in shared memory, where it is read in chunks
+  const auto bring = [&](const Pass& of, int c, int into) {
+    const int chunk = chunk_of(of), tiles = tiles_of(of);
+    stage<T>(static_cast<const T*>(p.x) + static_cast<size_t>(of.row) * p.x_pitch, p.x_pitch, of.rows, c * chunk,
+             length(chunk, c), p.w.k, p.aligned, tiles, xs + into * (p.room / 2 * 128));
+  };
+
+  int lines = lines_of(line);
+  Phase now = phase(pass, line, lines, 0);
+  fetch_scales(now);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (base + i < count) {
-          const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-          const uint4* at = reinterpret_cast<const uint4*>(shared) + (base + i) % kChunk * (NT * 128) + lane;
-          float part[NT][4];
+  for (int i = 0; i < kAhead; ++i) fetch(i, now);
+  bring(pass, 0, 0);
+  staged();
+
+  for (;;) {
+    // The round after this one.
+    Pass next_pass = pass;
+    int next_line = line + lines, next_lines = 0;
+    left -= lines;
+    if (next_line == lines_each) {
+      next_line = 0;
+      if (left > 0) next_pass = pass_at(passes, p.groups, kEach, ++index);
+    }
+    if (left > 0) next_lines = lines_of(next_line);
+    const int sharing = kWarps / lines, part = warp / lines, tiles = tiles_of(pass), chunk = chunk_of(pass);
+    const int chunks = (blocks + chunk - 1) / chunk;
+    const bool resident = chunks == 1;
+
+    float sum[kTiles][NT][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+    for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[n][j] = 0;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t a0 = pair<0>(wa[c]), a1 = pair<1>(wa[c]), a2 = pair<2>(wa[c]), a3 = pair<3>(wa[c]);
-            const uint32_t b0 = pair<0>(wb[c]), b1 = pair<1>(wb[c]), b2 = pair<2>(wb[c]), b3 = pair<3>(wb[c]);
+        for (int i = 0; i < 4; ++i) sum[h][n][i] = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const bool last = c + 1 == chunks;
+      Phase next{0, 0, 0};
+      if (!last) next = phase(pass, line, lines, c + 1);
+      else if (next_lines > 0) next = phase(next_pass, next_line, next_lines, 0);
+      // The chunk after this one, into the other half: of this pass, in this round or the next.
+      if (!resident && (!last || (next_lines > 0 && next_line > 0))) bring(pass, last ? 0 : c + 1, half ^ 1);
+      // (Columns past the pass's hold whatever was there: they only reach sums that no one reads.)
+      const auto blocks_of = [&](auto column_tiles) {
+        constexpr int N = decltype(column_tiles)::value;
+        const uint4* x = xs + half * (p.room / 2 * 128) + part * ((length(chunk, c) + sharing - 1) / sharing) * (N * 128) + lane;
+        for (bool more = true; more;) {
+          more = now.count > kAhead;
+          const Phase then = more ? Phase{now.record + kAhead, now.apart, now.count - kAhead} : next;
+          const uint32_t scales = scale_a | scale_b << 16;
+          fetch_scales(then);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (8 * n + g < columns) v = at[(n * 4 + c) * 32];
-              multiply(part[n], a0, b0, a1, b1, v.x, v.y);
-              multiply(part[n], a2, b2, a3, b3, v.z, v.w);
+          for (int i = 0; i < kAhead; ++i) {
+            if (i < now.count) {
+              float block_sum[kTiles][N][4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint4 v[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] = x[i * (N * 128) + (n * 4 + q) * 32];
+#pragma unroll
+                for (int h = 0; h < kTiles; ++h) {
+                  const uint32_t wa = q == 0 ? a[i][h].x : q == 1 ? a[i][h].y : q == 2 ? a[i][h].z : a[i][h].w;
+                  const uint32_t wb = q == 0 ? b[i][h].x : q == 1 ? b[i][h].y : q == 2 ? b[i][h].z : b[i][h].w;
+                  const Four fa = four(wa), fb = four(wb);
+#pragma unroll
+                  for (int n = 0; n < N; ++n) {
+                    if (q == 0) multiply_first(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
+                    else multiply(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
+                  }
+#pragma unroll
+                  for (int n = 0; n < N; ++n) multiply(block_sum[h][n], fa.v[2], fb.v[2], fa.v[3], fb.v[3], v[n].z, v[n].w);
+                }
+              }
+#pragma unroll
+              for (int h = 0; h < kTiles; ++h) {
+                const uint32_t both = __shfl_sync(~0u, scales, (lane & 28) + i * kTiles + h);
+                const float fa = __uint_as_float(both << 16), fb = __uint_as_float(both & 0xFFFF0000u);
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) sum[h][n][j] = fmaf(j < 2 ? fa : fb, block_sum[h][n][j], sum[h][n][j]);
+              }
             }
+            fetch(i, then);
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            sum[n][0] = fmaf(sa[i], part[n][0], sum[n][0]);
-            sum[n][1] = fmaf(sa[i], part[n][1], sum[n][1]);
-            sum[n][2] = fmaf(sb[i], part[n][2], sum[n][2]);
-            sum[n][3] = fmaf(sb[i], part[n][3], sum[n][3]);
-          }
+          x += kAhead * N * 128;
+          now = then;
         }
-        fetch(i, base + i + kAhead);
+      };
+      if (NT == 1 || tiles == 1) blocks_of(std::integral_constant<int, 1>());
+      else if (NT == 2 || tiles == 2) blocks_of(std::integral_constant<int, NT < 2 ? NT : 2>());
+      else if (tiles == 3) blocks_of(std::integral_constant<int, NT < 3 ? NT : 3>());
+      else blocks_of(std::integral_constant<int, NT>());
+      if (!last) {
+        staged();
+        half ^= 1;
       }
     }
-    // The CTA's sums, column after column, then those of the slices of k added in their order.
-    __syncthreads();
-    float* sums = reinterpret_cast<float*>(shared);
+
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sums[(8 * n + 2 * t + i % 2) * kPitch + warp * kInt4Rows + g + i / 2 * 8] = sum[n][i];
-    cluster_sync();
-    const uint32_t at = shared_address(sums);
-    for (int i = rank * kThreads + threadIdx.x; i < rows * kTile; i += p.slices * kThreads) {
-      const int r = i / kTile, c = i % kTile;
-      if (column0 + c >= p.w.n) continue;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums.of[warp][h][8 * n + 2 * t + i % 2][g + i / 2 * 8] = sum[h][n][i];
+    const auto result = [&](int at, int r, int c) {  // row r of the pass, weight row c of the at-th line
       float v = 0;
-      for (int s = 0; s < p.slices; ++s)
+      for (int h = 0; h < sharing; ++h)
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          v += peer_value(at + sizeof(float) * ((r * kParts + q) * kPitch + c), s);
-      put(p, row + r, column0 + c, v);
+        for (int q = 0; q < kParts; ++q) v += sums.of[h * lines + at][c / kInt4Rows][r * kParts + q][c % kInt4Rows];
+      const size_t column = static_cast<size_t>(line + at) * (kTiles * kInt4Rows) + c;
+      if (column < p.w.n) put(p, pass.row + r, column, kWeightUnit * v);
+    };
+    constexpr int kWide = kTiles * kInt4Rows;
+    if (sharing == 1) {  // a warp's own
+      __syncwarp();
+      if (warp < lines)
+        for (int i = lane; i < pass.rows * kWide; i += 32) result(warp, i / kWide, i % kWide);
+      __syncwarp();
+    } else {
+      __syncthreads();
+      for (int i = threadIdx.x; i < pass.rows * lines * kWide; i += kThreads)
+        result(i / kWide % lines, i / kWide / lines, i % kWide);
     }
-    cluster_sync();
+    if (next_lines == 0) return;
+    if (next_line == 0) {  // another pass's x
+      __syncthreads();
+      half = 0;
+      bring(next_pass, 0, 0);
+      staged();
+    } else if (!resident) {  // on its way
+      staged();
+      half ^= 1;
+    } else if (sharing > 1) {
+      __syncthreads();
+    }
+    pass = next_pass;
+    line = next_line;
+    lines = next_lines;
   }
 }
 
+// ------------------------------------------------------------------ the launch
+
 template <typename T, int NT>
-cudaError_t run(const Job& p, int jobs, cudaStream_t stream) {
-  cudaError_t err = cudaSuccess;
-  if (shared_bytes<NT>() > 48 * 1024) err = allow_shared_memory<int4_product_kernel<T, NT>>(shared_bytes<NT>());
+cudaError_t run(Job p, const DeviceInfo& dev, cudaStream_t stream) {
+  const size_t tables = 3 * sizeof(int) * (p.groups + 1);
+  const int most_room = static_cast<int>((kShared - sizeof(Sums<NT>) - tables) / 2048) / (2 * NT) * (2 * NT);
+  const cudaError_t err = allow_shared_memory<int4_product_kernel<T, NT>>(kShared);
   if (err != cudaSuccess) return err;
-  const auto tiles = static_cast<unsigned>((p.w.n + kTile - 1) / kTile);
-  return launch_clusters(ZC_KERNEL_INT4_PRODUCT, p.slices, int4_product_kernel<T, NT>,
-                         dim3(tiles * p.slices, static_cast<unsigned>(jobs)), kThreads, shared_bytes<NT>(), stream, p);
+  const int wanted = static_cast<int>(p.w.blocks()) * NT;
+  p.room = wanted < most_room ? wanted : most_room;
+  const size_t passes = (static_cast<size_t>(p.rows) * Parts<T>::n + 8 * NT - 1) / (8 * NT) + (p.groups < p.rows ? p.groups : p.rows);
+  const size_t most = passes * p.w.tiles(), sms = static_cast<size_t>(dev.sm_count);
+  return launch(ZC_KERNEL_INT4_PRODUCT, int4_product_kernel<T, NT>, static_cast<unsigned>(most < sms ? most : sms), kThreads,
+                sizeof(Sums<NT>) + static_cast<size_t>(p.room) * 2048 + tables, stream, p);
 }
 
 template <typename T>
-cudaError_t by_rows(const Job& p, int jobs, cudaStream_t stream) {
-  // Columns at a time: what an average group has, and some more.
-  const int groups = p.groups < p.rows ? p.groups : p.rows;
-  const int columns = (p.rows + groups - 1) / groups * Parts<T>::n;
-  if (columns <= 8) return run<T, 1>(p, jobs, stream);
-  if (columns <= 16) return run<T, 2>(p, jobs, stream);
-  return run<T, 4>(p, jobs, stream);
+cudaError_t by_rows(const Job& p, const DeviceInfo& dev, cudaStream_t stream) {
+  const size_t all = static_cast<size_t>(p.rows) * Parts<T>::n;
+  if (all <= 8) return run<T, 1>(p, dev, stream);
+  if (all <= 8 * static_cast<size_t>(p.groups)) return run<T, 2>(p, dev, stream);
+  return run<T, 4>(p, dev, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_int4_matmul(const Int4Product& p, const DeviceInfo& dev, cudaStream_t stream) {
-  Job q{p.x, p.x_pitch, p.values, p.scales, p.offsets, p.out, p.out_pitch, dev.status, p.w,
-            static_cast<int>(p.rows), p.groups, p.out_type, 1, whole_vectors(type_bytes(p.type), p.w.k, {p.x}, {p.x_pitch})};
-  while (q.slices < 8 && q.slices * kChunk < static_cast<int>(p.w.blocks())) q.slices *= 2;
-  const int jobs = p.offsets == nullptr ? 1 : (q.groups < q.rows ? q.groups : q.rows) + 1;
-  if (p.type == ZC_TYPE_BF16) return by_rows<__nv_bfloat16>(q, jobs, stream);
-  if (p.type == ZC_TYPE_FP16) return by_rows<__half>(q, jobs, stream);
-  return by_rows<float>(q, jobs, stream);
+  const Job q{p.x, p.x_pitch, p.values, p.scales, p.offsets, p.out, p.out_pitch, dev.status, p.w,
+              static_cast<int>(p.rows), p.groups, p.out_type, 0, whole_vectors(type_bytes(p.type), p.w.k, {p.x}, {p.x_pitch})};
+  if (p.type == ZC_TYPE_BF16) return by_rows<__nv_bfloat16>(q, dev, stream);
+  if (p.type == ZC_TYPE_FP16) return by_rows<__half>(q, dev, stream);
+  return by_rows<float>(q, dev, stream);
 }
 
 }  // namespace ex
