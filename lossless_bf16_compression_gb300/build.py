@@ -23,7 +23,8 @@ MODULE_PATH = os.path.join(PKG, "_experts.so")
 MODULE_SOURCE = os.path.join(CSRC, "experts", "ex_torch.cpp")
 SOURCES = ["zc_api.cu", "zc_stats.cu", "zc_encode.cu", "zc_decode.cu", "zc_static.cu", "zc_small.cu", "zc_fused.cu",
            "experts/ex_api.cu", "experts/ex_sort.cu", "experts/ex_rows.cu", "experts/ex_quantize.cu",
-           "experts/ex_matmul.cu", "experts/ex_router.cu", "experts/ex_int4.cu", "experts/ex_int4_matmul.cu"]
+           "experts/ex_matmul.cu", "experts/ex_route.cu", "experts/ex_route_grad.cu", "experts/ex_balance.cu",
+           "experts/ex_int4.cu", "experts/ex_int4_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

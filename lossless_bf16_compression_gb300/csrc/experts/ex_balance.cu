@@ -1,0 +1,250 @@
+// ex_balance.cu -- the balance loss of a router, its counts and slopes.
+//
+// Each lane keeps the sums of its columns' probabilities in registers over all of its tokens; the warps' are added in
+// shared memory in their order, the CTAs' by a second kernel, in theirs, so nothing depends on timing.  The counts are
+// whole numbers, for which order does not matter.
+#include "ex_router.cuh"
+
+namespace zc {
+namespace ex {
+namespace {
+
+// Rows that a warp takes at a time, so that their loads are in flight together, and warps of a CTA: what registers allow.
+template <typename R>
+constexpr int rows_at_once() { return R::N <= 8 ? 4 : 1; }
+template <typename R>
+constexpr int balance_warps() { return R::N <= 8 ? 32 : 16; }
+constexpr int kSums = 8;  // rows of sums in shared memory
+constexpr size_t kMaxParts = 152;
+
+struct Parts {  // of each CTA: sums, counts, tokens
+  float* sums;
+  int *counts, *tokens;
+};
+__host__ __device__ inline Parts parts_of(void* workspace, size_t ctas, size_t experts) {
+  float* s = static_cast<float*>(workspace);
+  int* c = reinterpret_cast<int*>(s + ctas * experts);
+  return {s, c, c + ctas * experts};
+}
+
+// Counts and slopes of experts begin .. end - 1 from their sums and counts (of `tokens` tokens), and in thread 0 the CTA's
+// part of the loss.  Slopes are rounded once: one division in 64 bits, which is slow, for all.
+__device__ __forceinline__ float settle(const float* sums, const int* totals, int tokens, int begin, int end, int experts,
+                                        int k, int* counts, float* slope) {
+  __shared__ double unit;
+  __shared__ float parts[ZC_MOE_MAX_EXPERTS / 32];
+  if (threadIdx.x == 0) unit = tokens > 0 ? experts / (static_cast<double>(k) * tokens * tokens) : 0.0;
+  __syncthreads();
+  const int warps = (end - begin + 31) / 32;
+  for (int w = threadIdx.x / 32; w < warps; w += blockDim.x / 32) {
+    const int e = w * 32 + threadIdx.x % 32;
+    float mine = 0;
+    if (begin + e < end) {
+      const float s = static_cast<float>(unit * totals[e]);
+      counts[begin + e] = totals[e];
+      slope[begin + e] = s;
+      mine = s * sums[e];
+    }
+    mine = row_sum<32>(mine);
+    if (threadIdx.x % 32 == 0) parts[w] = mine;
+  }
+  __syncthreads();
+  float all = 0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < warps; ++w) all += parts[w];
+  return all;
+}
+
+template <typename R>
+__global__ void __launch_bounds__(32 * balance_warps<R>())
+    balance_kernel(const typename R::T* logits, size_t pitch, const int* ids, size_t tokens, int experts, int k, int score, float* loss,
+                   int* counts, float* slope, void* workspace) {
+  constexpr int N = R::N, W = R::W;
+  constexpr int kRows = rows_at_once<R>(), kBalanceWarps = balance_warps<R>(), kBalanceThreads = 32 * kBalanceWarps;
+  constexpr int kTokens = kBalanceThreads / W;  // side by side
+  extern __shared__ float sums[];  // [kSums][experts], then experts counts
+  __shared__ int live_of[kBalanceWarps];
+  int* found = reinterpret_cast<int*>(sums + kSums * experts);
+  wait_for_previous();
+  let_next_start();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int e = threadIdx.x; e < experts; e += kBalanceThreads) found[e] = 0;
+  __syncthreads();
+  const size_t each = (tokens + gridDim.x - 1) / gridDim.x;
+  const size_t begin = min(tokens, blockIdx.x * each), end = min(tokens, begin + each);
+  float sum[N];
+  int live = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = 0;
+  for (size_t first = begin; first < end; first += kTokens * kRows) {
+    R r[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const size_t t = first + threadIdx.x / W + u * kTokens;
+      r[u].load(logits + t * pitch, t < end ? experts : 0);  // (behind the last: a row of nothing)
+    }
+    // The slots of these tokens.
+    const size_t slots = min(end - first, static_cast<size_t>(kTokens * kRows)) * k;
+    for (size_t s = threadIdx.x; s < slots; s += kBalanceThreads) {
+      const int e = ids[first * k + s];
+      if (e >= 0 && e < experts) atomicAdd(&found[e], 1);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (first + u * kTokens + warp * (32 / W) >= end) break;  // none of the warp's is left
+      float p[N], top = -kInf;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        p[i] = to_float(r[u].v[i]);
+        top = larger(top, p[i]);
+      }
+      top = row_max<W>(top);
+      if (W == 32 && top == -kInf) continue;
+      live += top != -kInf;
+      const float m = top == -kInf ? 0.0f : score == ZC_SCORE_SOFTMAX ? top : fminf(top, 0.0f);
+      float total = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        p[i] = score == ZC_SCORE_SOFTMAX ? expf(p[i] - m) : scaled_sigmoid(p[i], m).s;
+        total += p[i];
+      }
+      total = row_sum<W>(total);
+      const float f = total == 0 ? 0.0f : __fdividef(1.0f, total);  // (0: a row of padding)
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum[i] += p[i] * f;
+    }
+  }
+  // The tokens of a warp.
+#pragma unroll
+  for (int d = W; d < 32; d *= 2) {
+    live += __shfl_xor_sync(~0u, live, d);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] += __shfl_xor_sync(~0u, sum[i], d);
+  }
+  if (lane == 0) live_of[warp] = live;
+#pragma unroll
+  for (int round = 0; round < kBalanceWarps / kSums; ++round) {
+    if (warp / kSums == round) {
+      float* to = sums + warp % kSums * experts;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = R::column(i);
+        if (lane < W && c < experts) to[c] = round == 0 ? sum[i] : to[c] + sum[i];
+      }
+    }
+    __syncthreads();
+  }
+  int rows = 0;
+  for (int w = 0; w < kBalanceWarps; ++w) rows += live_of[w];
+  const bool alone = gridDim.x == 1;
+  const Parts parts = parts_of(workspace, gridDim.x, experts);
+  for (int e = threadIdx.x; e < experts; e += kBalanceThreads) {
+    float s = 0;
+    for (int w = 0; w < kSums; ++w) s += sums[w * experts + e];
+    if (alone) {
+      sums[e] = s;  // (read by this thread only: row 0 of column e)
+    } else {
+      parts.sums[blockIdx.x * static_cast<size_t>(experts) + e] = s;
+      parts.counts[blockIdx.x * static_cast<size_t>(experts) + e] = found[e];
+    }
+  }
+  if (alone) {
+    __syncthreads();
+    const float all = settle(sums, found, rows, 0, experts, experts, k, counts, slope);
+    if (threadIdx.x == 0) *loss = all;
+  } else if (threadIdx.x == 0) {
+    parts.tokens[blockIdx.x] = rows;
+  }
+}
+
+// The CTAs' parts added: one cluster, each of its CTAs a share of the experts, for every expert several threads that
+// read at the same time.
+constexpr int kSettleThreads = 1024, kSettleCtas = 8;
+__global__ void __launch_bounds__(kSettleThreads) __cluster_dims__(kSettleCtas, 1, 1)
+    settle_kernel(void* workspace, int ctas, int experts, int k, float* loss, int* counts, float* slope) {
+  __shared__ float sums[kSettleThreads];
+  __shared__ int totals[kSettleThreads], live[32];
+  __shared__ float losses[kSettleCtas];
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // (waited for before the first CTA's memory is used)
+  wait_for_previous();
+  let_next_start();
+  const Parts parts = parts_of(workspace, ctas, experts);
+  const int each = (experts + kSettleCtas - 1) / kSettleCtas, rank = blockIdx.x;
+  const int begin = min(experts, rank * each), end = min(experts, begin + each);
+  const int readers = min(32, kSettleThreads / each), reader = threadIdx.x / each, e = begin + threadIdx.x % each;
+  float s = 0;
+  int c = 0, n = 0;
+  if (reader < readers && e < end) {
+#pragma unroll 8
+    for (int b = reader; b < ctas; b += readers) {
+      s += parts.sums[static_cast<size_t>(b) * experts + e];
+      c += parts.counts[static_cast<size_t>(b) * experts + e];
+    }
+  }
+  if (threadIdx.x < ctas) n = parts.tokens[threadIdx.x];
+  sums[threadIdx.x] = s;
+  totals[threadIdx.x] = c;
+  n = __reduce_add_sync(~0u, n);
+  if (threadIdx.x % 32 == 0) live[threadIdx.x / 32] = n;
+  __syncthreads();
+  int tokens = 0;
+  for (int w = 0; w < kSettleThreads / 32; ++w) tokens += live[w];
+  if (threadIdx.x < each) {
+    for (int r = 1; r < readers; ++r) {
+      s += sums[r * each + threadIdx.x];
+      c += totals[r * each + threadIdx.x];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < each) {
+    sums[threadIdx.x] = s;
+    totals[threadIdx.x] = c;
+  }
+  __syncthreads();
+  const float all = settle(sums, totals, tokens, begin, end, experts, k, counts, slope);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (threadIdx.x == 0) {  // into the first CTA
+    const auto at = static_cast<uint32_t>(__cvta_generic_to_shared(&losses[rank]));
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.f32 [a], %1;\n\t}" ::"r"(at),
+                 "f"(all)
+                 : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0 && threadIdx.x == 0) {
+    float sum = 0;
+    for (int i = 0; i < kSettleCtas; ++i) sum += losses[i];
+    *loss = sum;
+  }
+}
+
+// CTAs for a call: one, which needs no second kernel, while its warps have two rows each at most; else as many as
+// SMs, while each warp has a row.
+size_t balance_ctas(size_t tokens, int experts) {
+  const size_t side = 32 * (experts <= 256 ? 32 : 16) / lanes_of(experts);  // tokens side by side in a CTA
+  const size_t n = tokens <= 2 * side ? 1 : (tokens + side - 1) / side;
+  return n > kMaxParts ? kMaxParts : n;
+}
+
+}  // namespace
+
+size_t balance_workspace(size_t tokens, int experts) {
+  const size_t n = balance_ctas(tokens, experts);
+  return n > 1 ? n * (2 * static_cast<size_t>(experts) + 1) * 4 : 0;
+}
+
+cudaError_t launch_balance(const RouterShape& s, const void* logits, size_t pitch, const int* ids, float* loss, int* counts,
+                           float* slope, void* workspace, cudaStream_t stream) {
+  const int ctas = static_cast<int>(balance_ctas(s.tokens, s.experts));
+  const cudaError_t err = by_row(s.type, s.experts, true, {logits}, {pitch}, [&](auto row) {
+    using R = decltype(row);
+    return launch(ZC_KERNEL_MOE_BALANCE, balance_kernel<R>, ctas, 32 * balance_warps<R>(),
+                  sizeof(float) * (kSums + 1) * s.experts, stream, static_cast<const typename R::T*>(logits), pitch, ids,
+                  s.tokens, s.experts, s.k, s.score, loss, counts, slope, workspace);
+  });
+  if (err != cudaSuccess || ctas == 1) return err;
+  return launch(ZC_KERNEL_MOE_BALANCE, settle_kernel, kSettleCtas, kSettleThreads, 0, stream, workspace, ctas, s.experts, s.k,
+                loss, counts, slope);
+}
+
+}  // namespace ex
+}  // namespace zc

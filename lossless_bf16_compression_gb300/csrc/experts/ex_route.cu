@@ -1,0 +1,200 @@
+// ex_route.cu -- a router's choice: the k largest logits of each token, and their weights.
+//
+// The largest of a row is found k times: each lane offers the largest of its own that is left, the row's largest wins,
+// and the lane that had it looks for its next one.  Bound by instructions: comparisons of every lane's values, k times.
+#include "ex_router.cuh"
+
+namespace zc {
+namespace ex {
+namespace {
+
+constexpr int kWarps = 8;
+
+// ------------------------------------------------------------------ the order of logits
+//
+// A logit as an unsigned integer in its own order: a NaN of either sign above all, -0 equal to 0 (an addition of 0 makes
+// them one), -infinity below all.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
+}
+constexpr uint32_t kNone = 0x007FFFFFu;  // of -infinity
+
+// The keys that are searched for a row's largest logits.
+//   16 bits: the logit's order above 0xFFFF - column: no two are equal, and equal logits go by column.
+//   fp32: the order with its last bits given to the number of the lane's register, N - 1 - i.  Two logits that differ in
+//   those bits alone, or not at all, may come in the wrong order: that is seen, and the row is searched again.
+template <typename R>
+struct Keys {
+  using T = typename R::T;
+  static constexpr int N = R::N;
+  static constexpr bool kUnique = sizeof(T) == 2;
+  static constexpr uint32_t kLow = kUnique ? 0xFFFFu : N - 1;
+  static constexpr uint32_t kLeast = sizeof(T) == 2 && std::is_same_v<T, __half> ? 0x03FFFFFFu : kNone;
+  uint32_t k[N];
+
+  __device__ __forceinline__ explicit Keys(const R& row) {
+    if constexpr (kUnique) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        uint32_t w = pair_plus_zero(row.v[i], row.v[i + 1]), sign;
+        asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(sign) : "r"(w));  // each half's sign, all over it
+        w ^= sign | 0x80008000u;
+        k[i] = w << 16 | (0xFFFFu - R::column(i));
+        k[i + 1] = (w & 0xFFFF0000u) | (0xFFFFu - R::column(i + 1));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) k[i] = (ordered(row.v[i]) & ~kLow) | (N - 1 - i);
+    }
+  }
+  __device__ __forceinline__ static uint32_t pair_plus_zero(__nv_bfloat16 a, __nv_bfloat16 b) {
+    const __nv_bfloat162 r = __hadd2(__nv_bfloat162(a, b), __float2bfloat162_rn(0.0f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  __device__ __forceinline__ static uint32_t pair_plus_zero(__half a, __half b) {
+    const __half2 r = __hadd2(__half2(a, b), __float2half2_rn(0.0f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t best = k[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = max(best, k[i]);
+    return best;
+  }
+  // The largest below m; 0: there is none.  (Distances from m - 1 wrap around for the others.)
+  __device__ __forceinline__ uint32_t below(uint32_t m) const {
+    uint32_t least = m - 1 - k[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) least = min(least, m - 1 - k[i]);
+    return least < m ? m - 1 - least : 0u;
+  }
+};
+
+// ------------------------------------------------------------------ the choice
+
+// The k largest of a row whose search by keys was not sure, one after the other by value and column: slot lane (and
+// lane + 32) gets its column.
+template <typename R>
+__device__ __noinline__ int2 search_again(const typename R::T* logits, int experts, int k) {
+  constexpr int N = R::N;
+  const int lane = R::lane();
+  R row;
+  row.load(logits, experts);
+  uint32_t key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) key[i] = ordered(to_float(row.v[i]));
+  int2 e = make_int2(-1, -1);
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] > best) best = key[i], at = R::column(i);
+    const uint32_t m = row_max<R::W>(best);
+    const int first = row_min<R::W>(best == m ? at : experts);
+    if (lane == j % R::W && m > kNone) {
+      if (j >= R::W) e.y = first;
+      else e.x = first;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (R::column(i) == first) key[i] = 0;
+  }
+  return e;
+}
+
+// Slots: lane j of a token's has slot j, and slot j + 32 where a token has a whole warp.
+template <typename R>
+__global__ void __launch_bounds__(32 * kWarps)
+    route_kernel(const typename R::T* logits, size_t pitch, size_t tokens, int experts, int k, int score, int normalize,
+                 float scale, float* weights, int* ids) {
+  using K = Keys<R>;
+  constexpr int N = R::N, W = R::W;
+  wait_for_previous();
+  let_next_start();
+  const int lane = R::lane();
+  const size_t t = (static_cast<size_t>(blockIdx.x) * (32 * kWarps) + threadIdx.x) / W;
+  const bool real = t < tokens;  // (the others of a warp take part in its exchanges)
+  const typename R::T* from = logits + (real ? t : 0) * pitch;
+  R row;
+  row.load(from, real ? experts : 0);
+  const K keys(row);
+
+  int e[2] = {-1, -1};  // the columns in this lane's slots
+  uint32_t best = keys.largest(), before = 0;
+  bool unsure = false;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = row_max<W>(best);
+    if (W == 32 && m <= K::kLeast) break;
+    int column;
+    if (K::kUnique) {
+      column = 0xFFFF - static_cast<int>(m & 0xFFFFu);
+    } else {
+      const unsigned who = __ballot_sync(~0u, best == m) >> (threadIdx.x % 32 / W * W) & (W == 32 ? ~0u : (1u << W % 32) - 1);
+      const int i = N - 1 - static_cast<int>(m & K::kLow);
+      column = (i / R::V * W + __ffs(who) - 1) * R::V + i % R::V;
+      unsure |= m > K::kLeast && ((who & (who - 1)) != 0 || (m ^ before) <= K::kLow);
+      before = m;
+    }
+    if (m > K::kLeast && lane == (j & (W - 1))) {
+      if (W == 32 && j >= 32) e[1] = column;
+      else e[0] = column;
+    }
+    if (best == m) best = keys.below(m);
+  }
+  if (!K::kUnique) {
+    const uint32_t m = row_max<W>(best);  // what is left may have been as large
+    unsure |= m > K::kLeast && (m ^ before) <= K::kLow;
+    if (__any_sync(~0u, unsure)) {
+      const int2 again = search_again<R>(from, real ? experts : 0, k);
+      e[0] = again.x;
+      e[1] = again.y;
+    }
+  }
+
+  // (The chosen logits again, from the L1.)
+  const bool many = W == 32 && k > 32, softmax = score == ZC_SCORE_SOFTMAX;
+  float x[2] = {-kInf, -kInf};
+  if (e[0] >= 0) x[0] = to_float(from[e[0]]);
+  if (many && e[1] >= 0) x[1] = to_float(from[e[1]]);
+  const float top = __shfl_sync(~0u, x[0], 0, W);
+  const auto value = [&](int h) {
+    return e[h] < 0 ? 0.0f : softmax ? expf(x[h] - top) : scaled_sigmoid(x[h], normalize ? fminf(top, 0.0f) : 0.0f).s;
+  };
+  const float w0 = value(0), w1 = many ? value(1) : 0.0f;
+  float total = 1.0f;
+  if (normalize) {
+    total = slots_sum<W>(w0 + w1, k);
+  } else if (softmax) {
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) total += expf(to_float(row.v[i]) - top);
+    total = row_sum<W>(total);
+  }
+  const float f = scale * __fdividef(1.0f, total);
+  if (real && lane < k) {
+    weights[t * k + lane] = e[0] < 0 ? 0.0f : f * w0;
+    ids[t * k + lane] = e[0];
+  }
+  if (many && real && lane + 32 < k) {
+    weights[t * k + lane + 32] = e[1] < 0 ? 0.0f : f * w1;
+    ids[t * k + lane + 32] = e[1];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouterShape& s, const void* logits, size_t pitch, float* weights, int* ids,
+                         cudaStream_t stream) {
+  return by_row(s.type, s.experts, s.k <= lanes_of(s.experts), {logits}, {pitch}, [&](auto row) {
+    using R = decltype(row);
+    const size_t tokens = 32 / R::W * kWarps;  // of a CTA
+    return launch(ZC_KERNEL_MOE_ROUTE, route_kernel<R>, static_cast<unsigned>((s.tokens + tokens - 1) / tokens), 32 * kWarps, 0,
+                  stream, static_cast<const typename R::T*>(logits), pitch, s.tokens, s.experts, s.k, s.score, s.normalize,
+                  s.scale, weights, ids);
+  });
+}
+
+}  // namespace ex
+}  // namespace zc
