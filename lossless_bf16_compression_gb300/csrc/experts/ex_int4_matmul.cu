@@ -70,6 +70,10 @@ __device__ __forceinline__ Four four(uint32_t word) {
           fma_pair(up & 0x000F000Fu, k2_127, kMinus), fma_pair(up & 0x00F000F0u, k2_123, kMinus)};
 }
 
+// a / b of whole numbers, 0 <= a < 2^20, without the long division: the quotient's error is below a / b 2^-21, the distance
+// of (a + 1/2) / b from a whole number at least 1 / 2b.
+__device__ __forceinline__ int divide(int a, int b) { return static_cast<int>((a + 0.5f) * __fdividef(1.0f, b)); }
+
 // ------------------------------------------------------------------ rows of x as columns of bfloat16
 
 template <typename T>
@@ -113,18 +117,24 @@ __device__ __forceinline__ void split(const T (&v)[8], uint4 (&out)[Parts<T>::n]
 }
 
 // Puts `count` blocks of `rows` rows of x, from block `first` on, where the products read them: for each block and
-// eight columns 4 x 512 bytes, in the c-th of which lane 4 g + t finds values 32 t + 8 c .. + 7 of column g.  bfloat16 on
-// whole vectors is copied asynchronously: staged() waits for it.
+// eight columns 4 x 512 bytes, in the c-th of which lane 4 g + t finds values 32 t + 8 c .. + 7 of column g (in the place of
+// lane 4 (g ^ 1) + t for odd c, so that the rows that come in meet in half as many banks).  bfloat16 on whole vectors is
+// copied asynchronously: staged() waits for it.
 template <typename T>
 __device__ __forceinline__ void stage(const T* x, size_t pitch, int rows, int first, int count, size_t k, bool aligned,
                                       int tiles, uint4* to) {
+  // A thread takes a vector of eight values of one row, or of each.
   const int vectors = count * (kInt4Group / 8);
-  for (int r = 0; r < rows; ++r) {
-    for (int v = threadIdx.x; v < vectors; v += kThreads) {
-      const size_t col = static_cast<size_t>(first) * kInt4Group + 8 * v;
+  const int side = vectors < kThreads ? divide(kThreads, vectors) : 1;  // rows side by side
+  const int row0 = side > 1 ? divide(threadIdx.x, vectors) : 0;
+  for (int v = threadIdx.x - row0 * vectors; v < vectors && row0 < side; v += kThreads) {
+    const size_t col = static_cast<size_t>(first) * kInt4Group + 8 * v;
+    const int block = v / 16, t = v % 16 / 4, c = v % 4;
+    const auto place = [&](int column) {
+      return to + ((block * tiles + column / 8) * 4 + c) * 32 + ((column % 8 * 4 + t) ^ (c & 1) * 4);
+    };
+    for (int r = row0; r < rows; r += side) {
       const T* from = x + r * pitch + col;
-      const int block = v / 16, t = v % 16 / 4, c = v % 4;
-      const auto place = [&](int column) { return to + ((block * tiles + column / 8) * 4 + c) * 32 + column % 8 * 4 + t; };
       if constexpr (Parts<T>::n == 1) {
         if (aligned) {  // (past the end of the row: zeros)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(place(r))), "l"(col < k ? from : x),
@@ -133,13 +143,24 @@ __device__ __forceinline__ void stage(const T* x, size_t pitch, int rows, int fi
           continue;
         }
       }
+      // Whole vectors, or each put together from the two aligned ones that hold it; zeros past the row's end.
+      constexpr int kVectors = 8 * sizeof(T) / 16, kEach = 16 / sizeof(T);
       alignas(16) T in[8];
+      uint4* whole = reinterpret_cast<uint4*>(in);
       if (aligned) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 16 / sizeof(T)) *reinterpret_cast<uint4*>(in + j) = load_if(from + j, col + j < k);
+        for (int j = 0; j < kVectors; ++j) whole[j] = load_if(from + j * kEach, col + j * kEach < k);
       } else {
+        const unsigned shift = low4(from);
+        const uint8_t *at = reinterpret_cast<const uint8_t*>(from) - shift, *end = reinterpret_cast<const uint8_t*>(x + r * pitch + k);
+        uint4 w[kVectors + 1];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) in[j] = col + j < k ? from[j] : from_float<T>(0.0f);
+        for (int j = 0; j <= kVectors; ++j) w[j] = load_if(at + 16 * j, at + 16 * j < end && (j < kVectors || shift != 0));
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) whole[j] = shift_bytes<true>(w[j], w[j + 1], shift);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j >= k) in[j] = from_float<T>(0.0f);
       }
       uint4 out[Parts<T>::n];
       split<T>(in, out);
@@ -192,18 +213,34 @@ struct Passes {
 };
 
 template <int kEach, int kParts>
+__device__ __forceinline__ int cost_of_rows(int rows) {
+  const int rest = rows % kEach;
+  return rows / kEach * cost_of(kEach * kParts) + (rest ? cost_of(rest * kParts) : 0);
+}
+template <int kEach, int kParts>
 __device__ __forceinline__ void find_passes(const Job& p, const Passes& s) {
+  if (p.offsets == nullptr) {  // one group
+    if (threadIdx.x < 2) {
+      const int rows = threadIdx.x ? p.rows : 0;
+      s.start[threadIdx.x] = rows;
+      s.first[threadIdx.x] = (rows + kEach - 1) / kEach;
+      s.cost[threadIdx.x] = cost_of_rows<kEach, kParts>(rows);
+    }
+    __syncthreads();
+    return;
+  }
   __shared__ int2 sums[kWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  constexpr int kGroups = (ZC_MOE_MAX_EXPERTS + kThreads - 1) / kThreads;  // of a thread
+  constexpr int kGroups = (ZC_MOE_MAX_EXPERTS + kThreads - 1) / kThreads;  // of a thread, the most
+  const int each = p.groups <= kThreads ? 1 : kGroups;
   int begin[kGroups], rows[kGroups];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const int g = threadIdx.x * kGroups + i;
+    const int g = threadIdx.x * each + i;
     begin[i] = rows[i] = 0;
-    if (g < p.groups) {
-      const int a = p.offsets ? p.offsets[g] : 0, z = p.offsets ? p.offsets[g + 1] : p.rows;
+    if (i < each && g < p.groups) {
+      const int a = p.offsets[g], z = p.offsets[g + 1];
       bad |= a < 0 || z < a || z > p.rows || (g == 0 && a != 0);
       begin[i] = a;
       rows[i] = z - a;
@@ -211,19 +248,16 @@ __device__ __forceinline__ void find_passes(const Job& p, const Passes& s) {
   }
   if (bad) set_error(p.status, ZC_ERR_CORRUPT);
   bad = __syncthreads_or(bad);  // (then there are no passes: their rows could be anywhere)
-  const auto passes = [&](int i) { return (rows[i] + kEach - 1) / kEach; };
-  const auto cost = [&](int i) {
-    const int rest = rows[i] % kEach;
-    return rows[i] / kEach * cost_of(kEach * kParts) + (rest ? cost_of(rest * kParts) : 0);
-  };
-  int2 upto = make_int2(0, 0);
+  int2 upto = make_int2(0, 0), own[kGroups];
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
     if (bad) begin[i] = rows[i] = 0;
-    upto.x += passes(i);
-    upto.y += cost(i);
+    own[i] = make_int2((rows[i] + kEach - 1) / kEach, cost_of_rows<kEach, kParts>(rows[i]));
+    upto.x += own[i].x;
+    upto.y += own[i].y;
   }
   const int2 mine = upto;
+#pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const int x = __shfl_up_sync(~0u, upto.x, d), y = __shfl_up_sync(~0u, upto.y, d);
     if (lane >= d) upto.x += x, upto.y += y;
@@ -237,11 +271,13 @@ __device__ __forceinline__ void find_passes(const Job& p, const Passes& s) {
     if (w < warp) upto.x += sums[w].x, upto.y += sums[w].y;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const int g = threadIdx.x * kGroups + i;
-    if (g < p.groups) s.start[g] = begin[i], s.first[g] = upto.x, s.cost[g] = upto.y;
-    upto.x += passes(i);
-    upto.y += cost(i);
-    if (g == p.groups - 1) s.start[g + 1] = bad ? p.rows : begin[i] + rows[i], s.first[g + 1] = upto.x, s.cost[g + 1] = upto.y;
+    const int g = threadIdx.x * each + i;
+    if (i < each && g < p.groups) {
+      s.start[g] = begin[i], s.first[g] = upto.x, s.cost[g] = upto.y;
+      upto.x += own[i].x;
+      upto.y += own[i].y;
+      if (g == p.groups - 1) s.start[g + 1] = bad ? p.rows : begin[i] + rows[i], s.first[g + 1] = upto.x, s.cost[g + 1] = upto.y;
+    }
   }
   __syncthreads();
 }
@@ -259,17 +295,28 @@ __device__ __forceinline__ Pass pass_at(const Passes& s, int groups, int each, i
   const int g = group_of(s.first, groups, index), row = s.start[g] + (index - s.first[g]) * each;
   return {g, row, min(each, s.start[g + 1] - row)};
 }
-// The place, counted in lines of all passes, of a point of the total cost (`lines` times a pass's, line after line).
-template <int kEach, int kParts>
-__device__ __forceinline__ size_t line_at(const Passes& s, int groups, int lines, size_t point) {
-  const int g = group_of(s.cost, groups, static_cast<int>(point / lines));
-  if (point >= static_cast<size_t>(s.cost[groups]) * lines) return static_cast<size_t>(s.first[groups]) * lines;
-  const size_t in = point - static_cast<size_t>(s.cost[g]) * lines;
+// The place, counted in lines of all passes, of a point of the total cost (`lines` times a pass's, line after line).  In 32
+// bits where the total fits them: long divisions take a microsecond.
+template <int kEach, int kParts, typename U>
+__device__ __forceinline__ size_t line_at(const Passes& s, int groups, int lines, U point) {
+  if (point >= static_cast<U>(s.cost[groups]) * lines) return static_cast<size_t>(s.first[groups]) * lines;
+  const int g = group_of(s.cost, groups, static_cast<int>(point / static_cast<U>(lines)));
+  const U in = point - static_cast<U>(s.cost[g]) * lines;
   constexpr int kFull = cost_of(kEach * kParts);
   const int rows = s.start[g + 1] - s.start[g], full = rows / kEach;
-  const size_t before = static_cast<size_t>(full) * kFull * lines;  // of the group's whole passes
-  const size_t line = in < before ? in / kFull : static_cast<size_t>(full) * lines + (in - before) / cost_of(rows % kEach * kParts);
+  const U before = static_cast<U>(full) * kFull * lines;  // of the group's whole passes
+  const U line = in < before ? in / kFull : static_cast<U>(full) * lines + (in - before) / cost_of(rows % kEach * kParts);
   return static_cast<size_t>(s.first[g]) * lines + line;
+}
+// The first line of part b of `parts`, for which the total cost is shared out evenly.
+template <int kEach, int kParts>
+__device__ __forceinline__ size_t first_line(const Passes& s, int groups, int lines, unsigned b, unsigned parts) {
+  const size_t all = static_cast<size_t>(s.cost[groups]) * lines;
+  if (all < (size_t(1) << 31)) {
+    const unsigned n = static_cast<unsigned>(all), each = n / parts, more = n % parts;
+    return line_at<kEach, kParts>(s, groups, lines, b * each + min(b, more));
+  }
+  return line_at<kEach, kParts>(s, groups, lines, all / parts * b + min(static_cast<size_t>(b), all % parts));
 }
 
 // ------------------------------------------------------------------ the product
@@ -284,19 +331,17 @@ struct Phase {  // what a warp reads next: `count` records from this one on, and
   uint32_t record, apart;
   int count;
 };
-// Record rows side by side that a warp takes: with two, each fragment of x serves twice.
-template <int NT>
-constexpr int tiles_of_warp() { return NT <= 2 ? 2 : 1; }
+constexpr int kTiles = 2;            // record rows side by side that a warp takes: each fragment of x serves twice
+constexpr int kAhead = 4 / kTiles;  // blocks in flight for each warp: 4 KB
 template <int NT>
 struct Sums {
-  float of[kWarps][tiles_of_warp<NT>()][8 * NT][kColumnPitch];
+  float of[kWarps][kTiles][8 * NT][kColumnPitch];
 };
 
 template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_constant__ Job p) {
   extern __shared__ __align__(16) uint8_t shared[];
   constexpr int kParts = Parts<T>::n, kEach = 8 * NT / kParts;
-  constexpr int kTiles = tiles_of_warp<NT>(), kAhead = 4 / kTiles;  // blocks in flight for each warp: 4 KB
   Sums<NT>& sums = *reinterpret_cast<Sums<NT>*>(shared);
   uint4* xs = reinterpret_cast<uint4*>(shared + sizeof(Sums<NT>));
   int* tables = reinterpret_cast<int*>(xs + p.room * 128);
@@ -315,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
   // A line: kTiles record rows.
   const int record_rows = static_cast<int>(p.w.tiles()), blocks = static_cast<int>(p.w.blocks());
   const int lines_each = (record_rows + kTiles - 1) / kTiles;  // of a pass
-  const size_t all = static_cast<size_t>(passes.cost[p.groups]) * lines_each;
   // (Lanes 0 and 1 look up this CTA's first line and the next one's.)
-  const size_t bound = line_at<kEach, kParts>(passes, p.groups, lines_each, all * (blockIdx.x + (lane & 1)) / gridDim.x);
+  const size_t bound = first_line<kEach, kParts>(passes, p.groups, lines_each, blockIdx.x + (lane & 1), gridDim.x);
   const size_t begin = __shfl_sync(~0u, bound, 0);
   int left = static_cast<int>(__shfl_sync(~0u, bound, 1) - begin);
   if (left == 0) return;
 
-  int index = static_cast<int>(begin / lines_each);  // of the pass
+  int index = begin >> 32 ? static_cast<int>(begin / lines_each)  // of the pass
+                          : static_cast<int>(static_cast<unsigned>(begin) / static_cast<unsigned>(lines_each));
   int line = static_cast<int>(begin - static_cast<size_t>(index) * lines_each);
   Pass pass = pass_at(passes, p.groups, kEach, index);
 
@@ -349,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
   // How a pass's x lies in shared memory: eight columns to a tile, and as many blocks at a time as there is room for.
   const auto tiles_of = [&](const Pass& of) { return (of.rows * kParts + 7) / 8; };
   const auto chunk_of = [&](const Pass& of) {
-    const int room = p.room / tiles_of(of);
+    const int room = NT == 1 ? p.room : divide(p.room, tiles_of(of));
     return blocks <= room ? blocks : room / 2;
   };
   const auto length = [&](int chunk, int c) { return min(chunk, blocks - c * chunk); };
@@ -358,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
     return most > kWarps / 2 && most < kWarps * 3 / 4 ? kWarps / 2 : most;
   };
   const auto phase = [&](const Pass& of, int first, int lines, int c) {
-    const int chunk = chunk_of(of), sharing = kWarps / lines, part = warp / lines, len = length(chunk, c);
-    const int sub = (len + sharing - 1) / sharing, at = part * sub, row = (first + warp % lines) * kTiles;
+    const int chunk = chunk_of(of), sharing = divide(kWarps, lines), part = divide(warp, lines), len = length(chunk, c);
+    const int sub = divide(len + sharing - 1, sharing), at = part * sub, row = (first + warp - part * lines) * kTiles;
     // (A record row past the last one: the first of the warp again, for sums that no one reads.)
     return Phase{static_cast<uint32_t>((static_cast<size_t>(of.group) * record_rows + row) * blocks + c * chunk + at),
                  row + 1 < record_rows ? static_cast<uint32_t>(blocks) : 0u, part < sharing ? max(0, min(sub, len - at)) : 0};
@@ -372,11 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
   };
 
   int lines = lines_of(line);
+  bring(pass, 0, 0);  // (before the weights, behind which it would wait)
   Phase now = phase(pass, line, lines, 0);
   fetch_scales(now);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(i, now);
-  bring(pass, 0, 0);
   staged();
 
   for (;;) {
@@ -389,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       if (left > 0) next_pass = pass_at(passes, p.groups, kEach, ++index);
     }
     if (left > 0) next_lines = lines_of(next_line);
-    const int sharing = kWarps / lines, part = warp / lines, tiles = tiles_of(pass), chunk = chunk_of(pass);
-    const int chunks = (blocks + chunk - 1) / chunk;
+    const int sharing = divide(kWarps, lines), part = divide(warp, lines), tiles = tiles_of(pass), chunk = chunk_of(pass);
+    const int chunks = blocks <= chunk ? 1 : (blocks + chunk - 1) / chunk;
     const bool resident = chunks == 1;
 
     float sum[kTiles][NT][4];
@@ -410,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       // (Columns past the pass's hold whatever was there: they only reach sums that no one reads.)
       const auto blocks_of = [&](auto column_tiles) {
         constexpr int N = decltype(column_tiles)::value;
-        const uint4* x = xs + half * (p.room / 2 * 128) + part * ((length(chunk, c) + sharing - 1) / sharing) * (N * 128) + lane;
+        const int odd = (lane ^ 4) - lane;
+        const uint4* x = xs + half * (p.room / 2 * 128) + part * divide(length(chunk, c) + sharing - 1, sharing) * (N * 128) + lane;
         for (bool more = true; more;) {
           more = now.count > kAhead;
           const Phase then = more ? Phase{now.record + kAhead, now.apart, now.count - kAhead} : next;
@@ -424,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
               for (int q = 0; q < 4; ++q) {
                 uint4 v[N];
 #pragma unroll
-                for (int n = 0; n < N; ++n) v[n] = x[i * (N * 128) + (n * 4 + q) * 32];
+                for (int n = 0; n < N; ++n) v[n] = x[i * (N * 128) + (n * 4 + q) * 32 + (q % 2 ? odd : 0)];
 #pragma unroll
                 for (int h = 0; h < kTiles; ++h) {
                   const uint32_t wa = q == 0 ? a[i][h].x : q == 1 ? a[i][h].y : q == 2 ? a[i][h].z : a[i][h].w;
@@ -456,8 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
         }
       };
       if (NT == 1 || tiles == 1) blocks_of(std::integral_constant<int, 1>());
-      else if (NT == 2 || tiles == 2) blocks_of(std::integral_constant<int, NT < 2 ? NT : 2>());
-      else if (tiles == 3) blocks_of(std::integral_constant<int, NT < 3 ? NT : 3>());
       else blocks_of(std::integral_constant<int, NT>());
       if (!last) {
         staged();
@@ -473,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
         for (int i = 0; i < 4; ++i) sums.of[warp][h][8 * n + 2 * t + i % 2][g + i / 2 * 8] = sum[h][n][i];
     const auto result = [&](int at, int r, int c) {  // row r of the pass, weight row c of the at-th line
       float v = 0;
+#pragma unroll 4
       for (int h = 0; h < sharing; ++h)
 #pragma unroll
         for (int q = 0; q < kParts; ++q) v += sums.of[h * lines + at][c / kInt4Rows][r * kParts + q][c % kInt4Rows];
@@ -487,8 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       __syncwarp();
     } else {
       __syncthreads();
-      for (int i = threadIdx.x; i < pass.rows * lines * kWide; i += kThreads)
-        result(i / kWide % lines, i / kWide / lines, i % kWide);
+      for (int i = threadIdx.x; i < pass.rows * lines * kWide; i += kThreads) {
+        const int r = divide(i / kWide, lines);
+        result(i / kWide - r * lines, r, i % kWide);
+      }
     }
     if (next_lines == 0) return;
     if (next_line == 0) {  // another pass's x
@@ -524,12 +571,11 @@ cudaError_t run(Job p, const DeviceInfo& dev, cudaStream_t stream) {
                 sizeof(Sums<NT>) + static_cast<size_t>(p.room) * 2048 + tables, stream, p);
 }
 
+// Sixteen columns at a time, or eight where there are no more.  (Thirty-two leave the tensor cores, at 1024 products a
+// cycle and SM, no room to hide in: 256 rows over 16 experts of 2048 x 7168 took 83 us with it and 70 without.)
 template <typename T>
 cudaError_t by_rows(const Job& p, const DeviceInfo& dev, cudaStream_t stream) {
-  const size_t all = static_cast<size_t>(p.rows) * Parts<T>::n;
-  if (all <= 8) return run<T, 1>(p, dev, stream);
-  if (all <= 8 * static_cast<size_t>(p.groups)) return run<T, 2>(p, dev, stream);
-  return run<T, 4>(p, dev, stream);
+  return static_cast<size_t>(p.rows) * Parts<T>::n <= 8 ? run<T, 1>(p, dev, stream) : run<T, 2>(p, dev, stream);
 }
 
 }  // namespace
