@@ -1,9 +1,11 @@
 """A mixture-of-experts layer whose exchanges are compressed, forward and backward, on one GPU.
 
-Tokens are sorted by expert into a send buffer (``moe.dispatch``); the buffer crosses the all-to-all compressed, with the
+A router chooses each token's experts and their weights (``moe.route``); tokens are sorted by expert into a send buffer
+(``moe.dispatch``); the buffer crosses the all-to-all compressed, with the
 transfer itself taken out (``binding.loopback`` compresses and decodes in one launch); the experts' two products run in
 8-bit blocks (``fp8``); their outputs cross back the same way and are added with the router's weights (``moe.combine``).
-The backward step sends the gradients through the same exchanges in the other direction.
+The backward step sends the gradients through the same exchanges in the other direction, and the weights' gradients,
+with that of the loss that keeps the experts evenly used (``moe.balance``), to the router's logits.
 
     python examples/expert_layer.py [--tokens 4096] [--hidden 2048] [--inner 1024] [--experts 16] [--k 4]
 """
@@ -74,13 +76,17 @@ def main():
     layer = ExpertLayer(normal(a.experts, a.inner, a.hidden, scale=a.hidden ** -0.5),
                         normal(a.experts, a.hidden, a.inner, scale=a.inner ** -0.5))
     x, d_out = normal(a.tokens, a.hidden), normal(a.tokens, a.hidden, scale=1e-3)
-    top, experts_of = torch.randn((a.tokens, a.experts), generator=g, device="cuda").topk(a.k, 1)
-    weights = torch.softmax(top, 1)
+    logits = torch.randn((a.tokens, a.experts), generator=g, device="cuda")
+    d_loss = torch.full((), 0.01, device="cuda")
 
     def step():
-        return layer.forward(x, experts_of, weights), *layer.backward(d_out)
+        weights, experts_of = moe.route(logits, a.k)
+        balance = moe.balance(logits, experts_of)
+        out = layer.forward(x, experts_of, weights)
+        dx, d_weights, dw1, dw2 = layer.backward(d_out)
+        return out, balance, dx, dw1, dw2, moe.route_grad(d_weights, logits, experts_of, balance=(d_loss, balance))
 
-    step()
+    balance = step()[1]
     layer.exchanged, layer.sent = 0, []
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()
@@ -91,7 +97,7 @@ def main():
     flop = 3 * 2 * 2 * a.tokens * a.k * a.hidden * a.inner
     ms = begin.elapsed_time(end)
     print(f"forward and backward of {a.tokens} tokens x {a.k} of {a.experts} experts: {ms:.2f} ms, "
-          f"{flop / ms / 1e9:.0f} TFLOP/s; rows exchanged compress {layer.ratio():.3f}x")
+          f"{flop / ms / 1e9:.0f} TFLOP/s; rows exchanged compress {layer.ratio():.3f}x; balance loss {float(balance.loss):.3f}")
 
 
 if __name__ == "__main__":

@@ -284,6 +284,81 @@ def test_streams_and_graphs():
         assert torch.equal(y, int4.matmul(x, m, offsets)) and torch.equal(v, int4.quantize_weight(x).values())
 
 
+def test_weights_past_32_bit_offsets():
+    """The last of 1000 experts of 2048 x 4608 (4.7 GB of records) and its values (18.9 GB)."""
+    groups, n, k = 1000, 2048, 4608
+    data = torch.full((groups, n // 16, k // 128, 1024), 0x88, dtype=torch.uint8, device="cuda")
+    scales = torch.ones((groups, n // 16, k // 128, 16), dtype=torch.bfloat16, device="cuda")
+    one = int4.quantize_weight(torch.randn((n, k), generator=torch.Generator().manual_seed(1)).bfloat16().cuda())
+    data[-1], scales[-1] = one.data, one.scales
+    m = int4.Matrix(data, scales, n, k)
+    offsets = torch.full((groups + 1,), 3, dtype=torch.int32, device="cuda")
+    offsets[0], offsets[-1] = 0, 10
+    x = torch.randn((10, k), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    y = int4.matmul(x, m, offsets)
+    assert (y[:3] == 0).all()
+    offsets[:-1] = 0
+    z = int4.matmul(x, m, offsets)
+    alone = int4.matmul(x, one)
+    size = doubles(x.abs().float() @ one.values().abs().t())
+    bound = 2 * size * (3 * 128 * 2.0 ** -23 + (2 * k // 128 + 40) * 2.0 ** -24)  # (the cut of the work may differ)
+    for a, rows in ((y, slice(3, 10)), (z, slice(0, 10))):
+        d = np.abs(doubles(a[rows]) - doubles(alone[rows]))
+        assert (d <= bound[rows] + 2 * half_ulp(torch.bfloat16) * (np.abs(doubles(alone[rows])) + bound[rows])).all()
+    v = m.values(torch.bfloat16)
+    assert torch.equal(v[-1], one.values(torch.bfloat16)) and (v[-2] == 0).all()
+    q = int4.quantize_weight(v)
+    assert torch.equal(q.data[-1], int4.quantize_weight(v[-1]).data) and (q.data[0] == 0x88).all()
+
+
+def test_a_product_follows_the_kernels_that_make_its_operands():
+    """Rows and weights written just before, by kernels that let the next one start early."""
+    from lossless_bf16_compression_gb300 import moe
+
+    w = torch.randn((6, 96, 512), generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    xs = [torch.randn((40, 512), generator=torch.Generator().manual_seed(s)).bfloat16().cuda() for s in range(4)]
+    ids = torch.randint(-1, 6, (40, 2), generator=torch.Generator().manual_seed(5)).cuda()
+
+    def step(x):
+        rows, plan = moe.dispatch(x, ids, 6)
+        return int4.matmul(rows, int4.quantize_weight(w * x[0, 0]), plan.offsets)
+
+    want = []
+    for x in xs:
+        want.append(step(x))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        for y, x in zip(want, xs):
+            assert torch.equal(step(x), y)
+
+
+def test_two_streams_at_once():
+    m, _ = made(8, 300, 1000, 9)
+    offsets = torch.tensor([0, 3, 3, 9, 10, 22, 25, 25, 30], dtype=torch.int32, device="cuda")
+    xs = [torch.randn((30, 1000), generator=torch.Generator().manual_seed(s)).bfloat16().cuda() for s in (1, 2)]
+    want = [int4.matmul(x, m, offsets) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [int4.matmul(xs[i % 2], m, offsets, stream=streams[i % 2]) for i in range(40)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+def test_kernel_times_go_by_their_ids():
+    w = torch.ones((64, 256), device="cuda")
+    zc.zc_timing_enable(1)
+    try:
+        zc.zc_timing_collect()
+        m = int4.quantize_weight(w)
+        m.values()
+        int4.matmul(w, m)
+        torch.cuda.synchronize()
+        seen = [k for k, ms in zc.zc_timing_collect() if ms > 0]
+    finally:
+        zc.zc_timing_enable(0)
+    assert seen == [zc.ZC_KERNEL_INT4_WEIGHT, zc.ZC_KERNEL_INT4_VALUES, zc.ZC_KERNEL_INT4_PRODUCT]
+
+
 @pytest.mark.parametrize("bad", [[1, 2, 4, 6], [0, 4, 2, 6], [0, 2, 4, 9], [0, -3, 4, 6]])
 def test_offsets_that_do_not_fit_are_reported(bad):
     """Every access is clamped to the rows: nothing outside is touched, and the status says so."""

@@ -190,6 +190,23 @@ def test_equal_logits_go_by_expert(dtype):
     assert (w == 0.2).all()
 
 
+@pytest.mark.parametrize("experts,k", [(8, 3), (32, 4), (64, 8), (100, 16), (128, 20), (256, 8), (300, 8), (1024, 64)])
+def test_logits_that_differ_in_their_last_bits(experts, k):
+    """fp32 logits within a few of their last steps of each other, equal ones among them, next to far ones: the order is
+    that of the values, then of the experts."""
+    rng = np.random.default_rng(experts)
+    rows = []
+    for base in (1.0, -1.0, 3.0e-39, 1.7e38, -2.5):
+        bits = np.full(experts, np.float32(base).view(np.int32)) + rng.integers(0, 9, experts).astype(np.int32)
+        rows.append(bits.view(np.float32))
+        far = rows[-1].copy()
+        far[rng.random(experts) < 0.7] = np.float32(base) - np.float32(abs(base))  # (few near the top)
+        rows.append(far)
+    x = torch.from_numpy(np.stack(rows)).cuda()
+    _, ids = moe.route(x, k)
+    assert np.array_equal(ids.cpu().numpy(), oracle.choose(doubles(x), k))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("score,normalize", KINDS)
 def test_rows_with_little_or_nothing_left(dtype, score, normalize):
@@ -326,6 +343,53 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(kept, step()))
+
+
+def test_rows_past_32_bit_offsets():
+    """The last rows of 4.2 million x 1024 logits (8.6 GB), and of their gradient."""
+    tokens, experts = (1 << 22) + 7, 1024
+    x = torch.zeros((tokens, experts), dtype=torch.bfloat16, device="cuda")
+    tail = make(5, experts, torch.bfloat16, 3)
+    x[-5:] = tail
+    w, ids = moe.route(x, 2)
+    w2, ids2 = moe.route(tail, 2)
+    assert torch.equal(w[-5:], w2) and torch.equal(ids[-5:], ids2) and (ids[:-5] == torch.tensor([0, 1], device="cuda")).all()
+    b = moe.balance(x, ids)
+    assert int(b.counts.sum()) == 2 * tokens
+    d = moe.route_grad(torch.ones_like(w), x, ids, balance=(torch.ones((), device="cuda"), b))
+    assert torch.equal(d[-5:], moe.route_grad(torch.ones_like(w2), tail, ids2, balance=(torch.ones((), device="cuda"), b)))
+
+
+def test_kernel_times_go_by_their_ids():
+    x = make(3000, 64, torch.bfloat16, 1)
+    one = torch.ones((), device="cuda")
+    zc.zc_timing_enable(1)
+    try:
+        zc.zc_timing_collect()
+        w, ids = moe.route(x, 4)
+        b = moe.balance(x, ids)
+        moe.route_grad(w, x, ids, balance=(one, b))
+        torch.cuda.synchronize()
+        seen = [k for k, ms in zc.zc_timing_collect() if ms > 0]
+    finally:
+        zc.zc_timing_enable(0)
+    assert seen == [zc.ZC_KERNEL_MOE_ROUTE, zc.ZC_KERNEL_MOE_BALANCE, zc.ZC_KERNEL_MOE_BALANCE, zc.ZC_KERNEL_MOE_ROUTE_GRAD]
+
+
+def test_two_streams_at_once():
+    """Calls of the same sizes on two streams, each with a workspace of its own."""
+    xs = [make(5000, 64, torch.bfloat16, s) for s in (1, 2)]
+    ids = [moe.route(x, 4)[1] for x in xs]
+    want = [moe.balance(x, i) for x, i in zip(xs, ids)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for x, i, s in zip(xs, ids, streams):
+            got.append(moe.balance(x, i, stream=s))
+    torch.cuda.synchronize()
+    for n, b in enumerate(got):
+        assert all(torch.equal(p, q) for p, q in zip(b, want[n % 2]))
 
 
 def test_refusals():
