@@ -14,7 +14,8 @@ template <typename R>
 constexpr int rows_at_once() { return R::N <= 8 ? 4 : 1; }
 template <typename R>
 constexpr int balance_warps() { return R::N <= 8 ? 32 : 16; }
-constexpr int kSums = 8;  // rows of sums in shared memory
+template <typename R>
+constexpr int sum_rows() { return R::N <= 8 ? balance_warps<R>() : 8; }  // in shared memory, up to 32 KB
 constexpr size_t kMaxParts = 152;
 
 struct Parts {  // of each CTA: sums, counts, tokens
@@ -27,32 +28,25 @@ __host__ __device__ inline Parts parts_of(void* workspace, size_t ctas, size_t e
   return {s, c, c + ctas * experts};
 }
 
-// Counts and slopes of experts begin .. end - 1 from their sums and counts (of `tokens` tokens), and in thread 0 the CTA's
-// part of the loss.  Slopes are rounded once: one division in 64 bits, which is slow, for all.
-__device__ __forceinline__ float settle(const float* sums, const int* totals, int tokens, int begin, int end, int experts,
-                                        int k, int* counts, float* slope) {
-  __shared__ double unit;
-  __shared__ float parts[ZC_MOE_MAX_EXPERTS / 32];
-  if (threadIdx.x == 0) unit = tokens > 0 ? experts / (static_cast<double>(k) * tokens * tokens) : 0.0;
-  __syncthreads();
-  const int warps = (end - begin + 31) / 32;
-  for (int w = threadIdx.x / 32; w < warps; w += blockDim.x / 32) {
-    const int e = w * 32 + threadIdx.x % 32;
-    float mine = 0;
-    if (begin + e < end) {
-      const float s = static_cast<float>(unit * totals[e]);
-      counts[begin + e] = totals[e];
-      slope[begin + e] = s;
-      mine = s * sums[e];
-    }
-    mine = row_sum<32>(mine);
-    if (threadIdx.x % 32 == 0) parts[w] = mine;
+// experts / (k n^2) as the sum of two fp32 numbers, to 2^-44 of it, and a count's multiple of it, rounded once.  (By a
+// division in 64 bits, of which an SM makes few, the loss of one token takes 5.5 us instead of XXX.)
+struct Unit {
+  float hi, lo;
+};
+__device__ __forceinline__ Unit unit_of(int experts, int k, int n) {
+  if (n == 0) return {0, 0};
+  if (n > 1 << 28) {  // k n^2 would pass 63 bits
+    const double u = experts / (static_cast<double>(k) * n * n);
+    return {static_cast<float>(u), static_cast<float>(u - static_cast<float>(u))};
   }
-  __syncthreads();
-  float all = 0;
-  if (threadIdx.x == 0)
-    for (int w = 0; w < warps; ++w) all += parts[w];
-  return all;
+  const long long d = static_cast<long long>(k) * n * n;
+  const float dh = __ll2float_rn(d), dl = static_cast<float>(d - static_cast<long long>(dh));
+  const float hi = __fdiv_rn(experts, dh);
+  return {hi, __fdiv_rn(fmaf(-hi, dl, fmaf(-hi, dh, experts)), dh)};
+}
+__device__ __forceinline__ float times(int c, const Unit& u) {
+  const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<int>(ch)), p = ch * u.hi;
+  return p + (fmaf(ch, u.hi, -p) + fmaf(ch, u.lo, cl * u.hi));
 }
 
 template <typename R>
@@ -62,14 +56,16 @@ __global__ void __launch_bounds__(32 * balance_warps<R>())
   constexpr int N = R::N, W = R::W;
   constexpr int kRows = rows_at_once<R>(), kBalanceWarps = balance_warps<R>(), kBalanceThreads = 32 * kBalanceWarps;
   constexpr int kTokens = kBalanceThreads / W;  // side by side
+  constexpr int kSums = sum_rows<R>();
   extern __shared__ float sums[];  // [kSums][experts], then experts counts
-  __shared__ int live_of[kBalanceWarps];
+  __shared__ int live_of[32];
+  __shared__ float losses[32];
   int* found = reinterpret_cast<int*>(sums + kSums * experts);
   wait_for_previous();
   let_next_start();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   for (int e = threadIdx.x; e < experts; e += kBalanceThreads) found[e] = 0;
-  __syncthreads();
+  if (threadIdx.x < 32) live_of[lane] = 0;
   const size_t each = (tokens + gridDim.x - 1) / gridDim.x;
   const size_t begin = min(tokens, blockIdx.x * each), end = min(tokens, begin + each);
   float sum[N];
@@ -83,6 +79,7 @@ __global__ void __launch_bounds__(32 * balance_warps<R>())
       const size_t t = first + threadIdx.x / W + u * kTokens;
       r[u].load(logits + t * pitch, t < end ? experts : 0);  // (behind the last: a row of nothing)
     }
+    if (first == begin) __syncthreads();  // (the counts are cleared; the rows are on their way)
     // The slots of these tokens.
     const size_t slots = min(end - first, static_cast<size_t>(kTokens * kRows)) * k;
     for (size_t s = threadIdx.x; s < slots; s += kBalanceThreads) {
@@ -121,6 +118,7 @@ __global__ void __launch_bounds__(32 * balance_warps<R>())
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] += __shfl_xor_sync(~0u, sum[i], d);
   }
+  if (begin >= end) __syncthreads();
   if (lane == 0) live_of[warp] = live;
 #pragma unroll
   for (int round = 0; round < kBalanceWarps / kSums; ++round) {
@@ -134,24 +132,43 @@ __global__ void __launch_bounds__(32 * balance_warps<R>())
     }
     __syncthreads();
   }
-  int rows = 0;
-  for (int w = 0; w < kBalanceWarps; ++w) rows += live_of[w];
+  // The rows of sums, by several threads for each expert (row r becomes the sum of rows r, r + readers, ...).
+  const int readers = min(kSums, kBalanceThreads / experts), reader = threadIdx.x / experts;
+  if (readers > 1) {
+    if (reader < readers) {
+      float s = 0;
+      for (int w = threadIdx.x; w < kSums * experts; w += readers * experts) s += sums[w];
+      sums[threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+  const int rows = __reduce_add_sync(~0u, live_of[lane]), left = readers > 1 ? readers : kSums;
   const bool alone = gridDim.x == 1;
   const Parts parts = parts_of(workspace, gridDim.x, experts);
+  const Unit unit = alone ? unit_of(experts, k, rows) : Unit{0, 0};
+  float mine = 0;  // of the loss
   for (int e = threadIdx.x; e < experts; e += kBalanceThreads) {
     float s = 0;
-    for (int w = 0; w < kSums; ++w) s += sums[w * experts + e];
+#pragma unroll 8
+    for (int r = 0; r < left; ++r) s += sums[r * experts + e];
     if (alone) {
-      sums[e] = s;  // (read by this thread only: row 0 of column e)
+      const float u = times(found[e], unit);
+      counts[e] = found[e];
+      slope[e] = u;
+      mine += u * s;
     } else {
       parts.sums[blockIdx.x * static_cast<size_t>(experts) + e] = s;
       parts.counts[blockIdx.x * static_cast<size_t>(experts) + e] = found[e];
     }
   }
   if (alone) {
+    mine = row_sum<32>(mine);
+    if (lane == 0) losses[warp] = mine;
     __syncthreads();
-    const float all = settle(sums, found, rows, 0, experts, experts, k, counts, slope);
-    if (threadIdx.x == 0) *loss = all;
+    if (warp == 0) {
+      const float all = row_sum<32>(lane < kBalanceWarps ? losses[lane] : 0.0f);
+      if (lane == 0) *loss = all;
+    }
   } else if (threadIdx.x == 0) {
     parts.tokens[blockIdx.x] = rows;
   }
@@ -163,8 +180,10 @@ constexpr int kSettleThreads = 1024, kSettleCtas = 8;
 __global__ void __launch_bounds__(kSettleThreads) __cluster_dims__(kSettleCtas, 1, 1)
     settle_kernel(void* workspace, int ctas, int experts, int k, float* loss, int* counts, float* slope) {
   __shared__ float sums[kSettleThreads];
-  __shared__ int totals[kSettleThreads], live[32];
-  __shared__ float losses[kSettleCtas];
+  __shared__ int totals[kSettleThreads], live[kSettleThreads / 32];
+  __shared__ float losses[32];  // in the first CTA: of each CTA's first four warps
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (warp == 0) losses[lane] = 0;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // (waited for before the first CTA's memory is used)
   wait_for_previous();
   let_next_start();
@@ -173,7 +192,7 @@ __global__ void __launch_bounds__(kSettleThreads) __cluster_dims__(kSettleCtas, 
   const int begin = min(experts, rank * each), end = min(experts, begin + each);
   const int readers = min(32, kSettleThreads / each), reader = threadIdx.x / each, e = begin + threadIdx.x % each;
   float s = 0;
-  int c = 0, n = 0;
+  int c = 0;
   if (reader < readers && e < end) {
 #pragma unroll 8
     for (int b = reader; b < ctas; b += readers) {
@@ -181,41 +200,43 @@ __global__ void __launch_bounds__(kSettleThreads) __cluster_dims__(kSettleCtas, 
       c += parts.counts[static_cast<size_t>(b) * experts + e];
     }
   }
-  if (threadIdx.x < ctas) n = parts.tokens[threadIdx.x];
+  const int n = __reduce_add_sync(~0u, threadIdx.x < ctas ? parts.tokens[threadIdx.x] : 0);
   sums[threadIdx.x] = s;
   totals[threadIdx.x] = c;
-  n = __reduce_add_sync(~0u, n);
-  if (threadIdx.x % 32 == 0) live[threadIdx.x / 32] = n;
+  if (lane == 0) live[warp] = n;
   __syncthreads();
-  int tokens = 0;
-  for (int w = 0; w < kSettleThreads / 32; ++w) tokens += live[w];
-  if (threadIdx.x < each) {
-    for (int r = 1; r < readers; ++r) {
-      s += sums[r * each + threadIdx.x];
-      c += totals[r * each + threadIdx.x];
+  if (threadIdx.x < (each + 31) / 32 * 32) {  // whole warps
+    const Unit unit = unit_of(experts, k, __reduce_add_sync(~0u, live[lane]));
+    float mine = 0;
+    if (threadIdx.x < end - begin) {
+#pragma unroll 8
+      for (int r = 1; r < readers; ++r) {
+        s += sums[r * each + threadIdx.x];
+        c += totals[r * each + threadIdx.x];
+      }
+      const float u = times(c, unit);
+      counts[e] = c;
+      slope[e] = u;
+      mine = u * s;
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < each) {
-    sums[threadIdx.x] = s;
-    totals[threadIdx.x] = c;
-  }
-  __syncthreads();
-  const float all = settle(sums, totals, tokens, begin, end, experts, k, counts, slope);
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (threadIdx.x == 0) {  // into the first CTA
-    const auto at = static_cast<uint32_t>(__cvta_generic_to_shared(&losses[rank]));
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.f32 [a], %1;\n\t}" ::"r"(at),
-                 "f"(all)
-                 : "memory");
+    mine = row_sum<32>(mine);
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (lane == 0) {  // into the first CTA
+      const auto at = static_cast<uint32_t>(__cvta_generic_to_shared(&losses[rank * 4 + warp]));
+      asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.f32 [a], %1;\n\t}" ::"r"(at),
+                   "f"(mine)
+                   : "memory");
+    }
+  } else {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (rank == 0 && threadIdx.x == 0) {
-    float sum = 0;
-    for (int i = 0; i < kSettleCtas; ++i) sum += losses[i];
-    *loss = sum;
+  if (rank == 0 && warp == 0) {
+    const float all = row_sum<32>(losses[lane]);
+    if (lane == 0) *loss = all;
   }
 }
+static_assert((ZC_MOE_MAX_EXPERTS / kSettleCtas + 31) / 32 * kSettleCtas == 32, "a place for each warp's part of the loss");
 
 // CTAs for a call: one, which needs no second kernel, while its warps have two rows each at most; else as many as
 // SMs, while each warp has a row.
@@ -238,7 +259,7 @@ cudaError_t launch_balance(const RouterShape& s, const void* logits, size_t pitc
   const cudaError_t err = by_row(s.type, s.experts, true, {logits}, {pitch}, [&](auto row) {
     using R = decltype(row);
     return launch(ZC_KERNEL_MOE_BALANCE, balance_kernel<R>, ctas, 32 * balance_warps<R>(),
-                  sizeof(float) * (kSums + 1) * s.experts, stream, static_cast<const typename R::T*>(logits), pitch, ids,
+                  sizeof(float) * (sum_rows<R>() + 1) * s.experts, stream, static_cast<const typename R::T*>(logits), pitch, ids,
                   s.tokens, s.experts, s.k, s.score, loss, counts, slope, workspace);
   });
   if (err != cudaSuccess || ctas == 1) return err;

@@ -17,7 +17,7 @@ constexpr int kWarps = 8;
 
 // Dense: the balance loss or a softmax over the row takes part, so that all of a row is read; else only the chosen logits.
 template <typename R, bool Dense>
-constexpr int ctas() { return R::N > 8 ? 1 : Dense ? 4 : 6; }  // on an SM at a time
+constexpr int ctas() { return R::N > 8 ? 1 : Dense ? 4 : 8; }  // on an SM at a time
 
 template <typename R, bool Dense>
 __global__ void __launch_bounds__(32 * kWarps, (ctas<R, Dense>()))

@@ -120,7 +120,11 @@ __device__ __forceinline__ float row_sum(float v) {
 // The sum over the first `n` lanes, in all of those (lanes behind hold 0, or have no use for it).
 template <int W>
 __device__ __forceinline__ float slots_sum(float v, int n) {
-  for (int d = 1; d < min(n, W); d *= 2) v += __shfl_xor_sync(~0u, v, d);
+#pragma unroll
+  for (int d = 1; d < W; d *= 2) {
+    if (d >= n) break;
+    v += __shfl_xor_sync(~0u, v, d);
+  }
   return v;
 }
 // The larger value; NaN if there is one.
