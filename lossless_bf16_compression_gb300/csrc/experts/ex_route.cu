@@ -56,18 +56,44 @@ struct Keys {
     const __half2 r = __hadd2(__half2(a, b), __float2half2_rn(0.0f));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
+  // A lane's keys in descending order (eight of them: a network of 19 comparisons; more: as they are).
+  static constexpr bool kSorted = N == 8;
+  __device__ __forceinline__ void order(int a, int b) {
+    const uint32_t x = k[a], y = k[b];
+    k[a] = max(x, y);
+    k[b] = min(x, y);
+  }
+  __device__ __forceinline__ void sort() {
+    if constexpr (kSorted) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) order(i, i + 1);
+      order(0, 2), order(1, 3), order(4, 6), order(5, 7);
+      order(1, 2), order(5, 6);
+      order(0, 4), order(1, 5), order(2, 6), order(3, 7);
+      order(2, 4), order(3, 5);
+      order(1, 2), order(3, 4), order(5, 6);
+    }
+  }
   __device__ __forceinline__ uint32_t largest() const {
+    if (kSorted) return k[0];
     uint32_t best = k[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) best = max(best, k[i]);
     return best;
   }
-  // The largest below m; 0: there is none.  (Distances from m - 1 wrap around for the others.)
-  __device__ __forceinline__ uint32_t below(uint32_t m) const {
-    uint32_t least = m - 1 - k[0];
+  // The largest after m, which was this lane's (0: there is none).
+  __device__ __forceinline__ uint32_t after(uint32_t m) {
+    if constexpr (kSorted) {
 #pragma unroll
-    for (int i = 1; i < N; ++i) least = min(least, m - 1 - k[i]);
-    return least < m ? m - 1 - least : 0u;
+      for (int i = 0; i < N - 1; ++i) k[i] = k[i + 1];
+      k[N - 1] = 0;
+      return k[0];
+    } else {  // (distances from m - 1 wrap around for those that are not below m)
+      uint32_t least = m - 1 - k[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) least = min(least, m - 1 - k[i]);
+      return least < m ? m - 1 - least : 0u;
+    }
   }
 };
 
@@ -119,7 +145,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   const typename R::T* from = logits + (real ? t : 0) * pitch;
   R row;
   row.load(from, real ? experts : 0);
-  const K keys(row);
+  K keys(row);
+  keys.sort();
 
   int e[2] = {-1, -1};  // the columns in this lane's slots
   uint32_t best = keys.largest(), before = 0;
@@ -141,7 +168,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       if (W == 32 && j >= 32) e[1] = column;
       else e[0] = column;
     }
-    if (best == m) best = keys.below(m);
+    if (best == m) best = keys.after(m);
   }
   if (!K::kUnique) {
     const uint32_t m = row_max<W>(best);  // what is left may have been as large
