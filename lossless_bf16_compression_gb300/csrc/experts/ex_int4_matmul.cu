@@ -1,14 +1,18 @@
 // ex_int4_matmul.cu -- the experts' products on 4-bit weights, for few rows.
 //
-// out[r, i] = sum over b of s[i, b] * (sum over j in b of x[r, j] q[i, j]).  Bound by the weights' bytes.  A warp
-// takes 16 weight rows (one record for each 128 columns, read as 2 x 512 neighbouring bytes) and multiplies them by
-// up to 8 NT columns, the rows of x, on the warp-level matrix instructions: with so few rows the tensor cores are far
-// from busy, and what counts is the unpacking.  A 4-bit value u = q + 8 becomes 128 + u by one logic operation (the
-// low bits of a bfloat16 128) and q by a subtraction, both for two values at a time and exact.  The group's scale
+// out[r, i] = sum over b of s[i, b] * (sum over j in b of x[r, j] q[i, j]).  Bound by the weights' bytes, or by what it
+// takes to unpack them.  A warp takes 2 x 16 weight rows (a record of 1 KB for each 128 columns) and multiplies them by
+// eight or sixteen columns, the rows of x, on the warp-level matrix instructions: with so few rows the tensor cores
+// have time to spare (1024 products a cycle and SM by this way; the tensor-memory instructions want 128 weight
+// rows at a time, too coarse for one token's experts, and the unpacked weights written out first).  The group's scale
 // multiplies the group's sum, once for 128 products.
 //
-// x of 16 or 32 bits that bfloat16 does not hold is split into two or three bfloat16 values that add up to it exactly;
-// they are columns of their own, added at the end.
+// fp32 rows of x are split into three bfloat16 values that add up to them exactly; they are columns of their own, added
+// at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.1 us (59 MB; 2 us of launch,
+// 4 of looking up the work, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 105 us (485 MB: 4.9 TB/s, bound by
+// the unpacking: 82 us without any load, 76 with the loads alone), nine to sixteen 135 to 148.
+#include <type_traits>
+
 #include "ex_int4.cuh"
 
 namespace zc {
@@ -22,19 +26,32 @@ constexpr size_t kShared = 226 * 1024;
 __device__ __forceinline__ uint32_t shared_address(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+// The 16-bit type that x and the weights are multiplied in: x's own, or bfloat16 for the parts of fp32.
+template <typename T>
+using Form = std::conditional_t<std::is_same_v<T, __half>, __half, __nv_bfloat16>;
+
+// d (+)= a b for 16 weight rows and eight columns, 16 values of k.
+template <typename F, bool First>
 __device__ __forceinline__ void multiply(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (First && std::is_same_v<F, __half>)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else if constexpr (First)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else if constexpr (std::is_same_v<F, __half>)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void multiply_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                               uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
 // Two times 16 bytes, 512 apart, where `on` is set; else they are as they were, and not used.
 __device__ __forceinline__ void fetch_record(uint4& a, uint4& b, const void* p, int on) {
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %9, 0;\n\t"
@@ -51,37 +68,46 @@ __device__ __forceinline__ void fetch_scale(uint32_t& v, const void* p, int on) 
 }
 
 
-// The eight weights of a word as pairs of bfloat16 values, weights 2 p and 2 p + 1 in the p-th, each q / 64.  The bits of
-// a nibble alone, in the low eight bits of a bfloat16, are a number too small to be normal, u 2^-133 or 16 u 2^-133,
-// and one fused multiply-add makes u / 64 - 8 / 64 of either, exactly.
-constexpr float kWeightUnit = 64.0f;
+// The eight weights of a word as pairs of 16-bit numbers, weights 2 p and 2 p + 1 in the p-th, each q / weight_unit.  The bits
+// of a nibble alone, in the low eight bits of such a number, are one too small to be normal, u or 16 u times the smallest
+// (2^-133 or 2^-24), and one fused multiply-add makes (u - 8) / weight_unit of either, exactly: five logic operations and
+// four multiply-adds for eight weights.  (Or'ed into the low bits of 128, with a subtraction, they took seven and four:
+// 153 us where these take 147, 512 rows over 64 experts at the time.)
+template <typename F>
+constexpr float weight_unit() { return std::is_same_v<F, __half> ? 512.0f : 64.0f; }
+template <typename F>
 __device__ __forceinline__ uint32_t fma_pair(uint32_t v, uint32_t times, uint32_t plus) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(times), "r"(plus));
+  if constexpr (std::is_same_v<F, __half>) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(times), "r"(plus));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(times), "r"(plus));
   return r;
 }
 struct Four {
   uint32_t v[4];
 };
+template <typename F>
 __device__ __forceinline__ Four four(uint32_t word) {
+  constexpr bool kHalf = std::is_same_v<F, __half>;
+  constexpr uint32_t kLow = kHalf ? 0x78007800u : 0x7F007F00u;    // 2^15, 2^127
+  constexpr uint32_t kHigh = kHalf ? 0x68006800u : 0x7D007D00u;   // 2^11, 2^123
+  constexpr uint32_t kMinus = kHalf ? 0xA400A400u : 0xBE00BE00u;  // -8 / 512, -8 / 64
   const uint32_t up = word >> 8;
-  constexpr uint32_t k2_127 = 0x7F007F00u, k2_123 = 0x7D007D00u, kMinus = 0xBE00BE00u;
-  return {fma_pair(word & 0x000F000Fu, k2_127, kMinus), fma_pair(word & 0x00F000F0u, k2_123, kMinus),
-          fma_pair(up & 0x000F000Fu, k2_127, kMinus), fma_pair(up & 0x00F000F0u, k2_123, kMinus)};
+  return {fma_pair<F>(word & 0x000F000Fu, kLow, kMinus), fma_pair<F>(word & 0x00F000F0u, kHigh, kMinus),
+          fma_pair<F>(up & 0x000F000Fu, kLow, kMinus), fma_pair<F>(up & 0x00F000F0u, kHigh, kMinus)};
 }
 
 // a / b of whole numbers, 0 <= a < 2^20, without the long division: the quotient's error is below a / b 2^-21, the distance
 // of (a + 1/2) / b from a whole number at least 1 / 2b.
 __device__ __forceinline__ int divide(int a, int b) { return static_cast<int>((a + 0.5f) * __fdividef(1.0f, b)); }
 
-// ------------------------------------------------------------------ rows of x as columns of bfloat16
+// ------------------------------------------------------------------ rows of x as columns
 
 template <typename T>
 struct Parts;
 template <>
 struct Parts<__nv_bfloat16> { static constexpr int n = 1; };
 template <>
-struct Parts<__half> { static constexpr int n = 2; };
+struct Parts<__half> { static constexpr int n = 1; };
 template <>
 struct Parts<float> { static constexpr int n = 3; };
 
@@ -341,6 +367,7 @@ struct Sums {
 template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_constant__ Job p) {
   extern __shared__ __align__(16) uint8_t shared[];
+  using F = Form<T>;
   constexpr int kParts = Parts<T>::n, kEach = 8 * NT / kParts;
   Sums<NT>& sums = *reinterpret_cast<Sums<NT>*>(shared);
   uint4* xs = reinterpret_cast<uint4*>(shared + sizeof(Sums<NT>));
@@ -475,14 +502,15 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
                 for (int h = 0; h < kTiles; ++h) {
                   const uint32_t wa = q == 0 ? a[i][h].x : q == 1 ? a[i][h].y : q == 2 ? a[i][h].z : a[i][h].w;
                   const uint32_t wb = q == 0 ? b[i][h].x : q == 1 ? b[i][h].y : q == 2 ? b[i][h].z : b[i][h].w;
-                  const Four fa = four(wa), fb = four(wb);
+                  const Four fa = four<F>(wa), fb = four<F>(wb);
 #pragma unroll
                   for (int n = 0; n < N; ++n) {
-                    if (q == 0) multiply_first(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
-                    else multiply(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
+                    if (q == 0) multiply<F, true>(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
+                    else multiply<F, false>(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
                   }
 #pragma unroll
-                  for (int n = 0; n < N; ++n) multiply(block_sum[h][n], fa.v[2], fb.v[2], fa.v[3], fb.v[3], v[n].z, v[n].w);
+                  for (int n = 0; n < N; ++n)
+                    multiply<F, false>(block_sum[h][n], fa.v[2], fb.v[2], fa.v[3], fb.v[3], v[n].z, v[n].w);
                 }
               }
 #pragma unroll
@@ -522,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
 #pragma unroll
         for (int q = 0; q < kParts; ++q) v += sums.of[h * lines + at][c / kInt4Rows][r * kParts + q][c % kInt4Rows];
       const size_t column = static_cast<size_t>(line + at) * (kTiles * kInt4Rows) + c;
-      if (column < p.w.n) put(p, pass.row + r, column, kWeightUnit * v);
+      if (column < p.w.n) put(p, pass.row + r, column, weight_unit<F>() * v);
     };
     constexpr int kWide = kTiles * kInt4Rows;
     if (sharing == 1) {  // a warp's own

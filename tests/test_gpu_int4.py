@@ -220,6 +220,8 @@ def test_every_bit_of_x_counts(dtype):
     g = torch.Generator().manual_seed(5)
     x = (torch.randn((6, k), generator=g) * 2.0 ** torch.randint(-10, 10, (6, k), generator=g)).to(dtype).cuda()
     x[0, 0], x[0, 1], x[1, 5] = torch.finfo(dtype).max, -torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal
+    if dtype == torch.float16:  # numbers too small to be normal, the smallest among them
+        x[2] = torch.randint(-1023, 1024, (k,), generator=g).double().mul(2.0 ** -24).half()
     assert torch.equal(int4.matmul(x, m), x)
 
 
