@@ -2,7 +2,8 @@
 //
 // Each lane keeps the sums of its columns' probabilities in registers over all of its tokens; the warps' are added in
 // shared memory in their order, the CTAs' by a second kernel, in theirs, so nothing depends on timing.  The counts are
-// whole numbers, for which order does not matter.
+// whole numbers, for which order does not matter.  Bound by latency and by the exponentials: 64 x 64 5.6 us, 777 x 40 (and
+// from there on two launches) 7.4, 32768 x 64 in fp32 9.5, 16384 x 256 11, of which the second kernel takes 3.
 #include "ex_router.cuh"
 
 namespace zc {
@@ -28,8 +29,8 @@ __host__ __device__ inline Parts parts_of(void* workspace, size_t ctas, size_t e
   return {s, c, c + ctas * experts};
 }
 
-// experts / (k n^2) as the sum of two fp32 numbers, to 2^-44 of it, and a count's multiple of it, rounded once.  (By a
-// division in 64 bits, of which an SM makes few, the loss of one token takes 5.5 us instead of XXX.)
+// experts / (k n^2) as the sum of two fp32 numbers, to 2^-44 of it, and a count's multiple of it, rounded once.  (The 64-bit
+// division that stood here took the kernels 1500 cycles: an SM makes two 64-bit products a cycle.)
 struct Unit {
   float hi, lo;
 };

@@ -1,7 +1,9 @@
 // ex_route.cu -- a router's choice: the k largest logits of each token, and their weights.
 //
 // The largest of a row is found k times: each lane offers the largest of its own that is left, the row's largest wins,
-// and the lane that had it looks for its next one.  Bound by instructions: comparisons of every lane's values, k times.
+// and the lane that had it goes on to its next one.  Bound by instructions (integer comparisons and moves: that pipe is
+// busy 86% of the cycles at 32768 x 256): one token 2.4 us, 32768 x 64 in fp32, eight chosen, 6.2, 16384 x 256 in
+// bfloat16 8.5, in fp32 10.5.
 #include "ex_router.cuh"
 
 namespace zc {

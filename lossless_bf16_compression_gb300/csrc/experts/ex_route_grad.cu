@@ -6,7 +6,9 @@
 //   sigmoids                d_j = s_j (1 - s_j) g_j
 //   softmax of the row      d_i = p_i (g_i - sum g p), g_i the sum over the slots of expert i
 // and of the balance loss  d_i = d_loss p_i (slope_i - sum slope p), times 1 - s_i for sigmoids.
-// What belongs to chosen experts goes through a row in shared memory, so that a row is written once and whole.
+// What belongs to chosen experts goes through a row in shared memory, so that a row is written once and whole.  Bound by
+// instructions and the exchanges' latency: 16384 x 256, eight chosen, the weights' alone 7.8 us (fp32: 17 MB written, 2.6 us
+// at the copy rate), with the balance loss 11.6, 32768 x 64 5.0 and 7.1.
 #include "ex_router.cuh"
 
 namespace zc {
