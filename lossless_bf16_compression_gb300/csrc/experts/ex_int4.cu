@@ -1,6 +1,6 @@
 // ex_int4.cu -- weights in 4 bits: rounding them, and the values that they stand for.
 //
-// Bound by DRAM where rows are whole 16-byte vectors (16 x 2048 x 7168: bfloat16 98 us, 6.1 TB/s, fp32 181, 5.9; values in
+// Bound by DRAM where rows are whole 16-byte vectors (16 x 2048 x 7168: bfloat16 98 us, 6.0 TB/s, fp32 181, 5.9; values in
 // bfloat16 87, 6.8, in fp32 158, 6.7).  Unaligned rows are rounded value by value (4 x 2047 x 7167 in bfloat16 61 us).
 //
 // A warp takes one record, 16 rows x 128 columns: lane 4 g + t holds columns 8 (t + 4 c), c = 0 .. 3, of rows g and

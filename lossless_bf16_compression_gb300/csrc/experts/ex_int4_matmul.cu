@@ -9,8 +9,10 @@
 //
 // fp32 rows of x are split into three bfloat16 values that add up to them exactly; they are columns of their own, added
 // at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.1 us (59 MB; 2 us of launch,
-// 4 of looking up the work, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 105 us (485 MB: 4.9 TB/s, bound by
-// the unpacking: 82 us without any load, 76 with the loads alone), nine to sixteen 135 to 148.
+// 4 of looking up the work, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 105 us (485 MB: 4.9 TB/s; 81 without
+// the loads, 24 without loads, unpacking and products), nine to sixteen 135 to 148.  A scheduler's two cycles for each logic
+// operation and eight for a product make 40 us of unpacking and 25 of products (sixteen columns: 50); four warps, which is
+// what the registers hold, overlap these in part.
 #include <type_traits>
 
 #include "ex_int4.cuh"
