@@ -360,6 +360,41 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(d[-5:], moe.route_grad(torch.ones_like(w2), tail, ids2, balance=(torch.ones((), device="cuda"), b)))
 
 
+# The largest batches of one CTA, one more, the largest of a cluster, one more: by the experts of a row.
+@pytest.mark.parametrize("tokens,experts,k", [(512, 20, 3), (513, 20, 3), (4096, 32, 1), (4097, 32, 9), (257, 64, 8), (2048, 40, 6),
+                                              (2049, 64, 2), (129, 100, 5), (1024, 128, 3), (1025, 128, 3), (65, 256, 8),
+                                              (512, 200, 40), (513, 256, 8), (33, 1000, 8), (256, 1024, 64), (257, 999, 2)])
+@pytest.mark.parametrize("score,dtype", [("softmax", torch.bfloat16), ("sigmoid", torch.float32)])
+def test_balance_by_one_cta_a_cluster_or_two_kernels(tokens, experts, k, score, dtype):
+    x = make(tokens, experts, dtype, tokens + k, masked=0.1, padded=0.2)
+    ids = np.random.default_rng(tokens).integers(-1, experts + 1, (tokens, k)).astype(np.int32)
+    b = moe.balance(x, torch.from_numpy(ids).cuda(), score)
+    v = doubles(x)
+    loss, counts, slope = oracle.balance(v, ids, score)
+    assert np.array_equal(b.counts.cpu().numpy(), counts) and (np.abs(doubles(b.slope) - slope) <= E * slope).all()
+    assert abs(float(b.loss) - loss) <= (spread(v).max() + 260 + tokens / 16) * E * loss
+    again = moe.balance(x, torch.from_numpy(ids).cuda(), score)
+    assert all(torch.equal(p, q) for p, q in zip(b, again))
+
+
+def test_balance_of_more_rows_than_fp32_counts():
+    """2^24 + 3 rows, whose number is no fp32 value; all but one use expert 1, so p is 1/3, 2/3 and 0, 1 in the last."""
+    tokens = (1 << 24) + 3
+    x = torch.tensor([0.0, np.log(2.0)], dtype=torch.float32, device="cuda").repeat(tokens, 1)
+    x[-1, 0] = -np.inf
+    ids = torch.ones((tokens, 1), dtype=torch.int32, device="cuda")
+    ids[5] = 0
+    b = moe.balance(x, ids)
+    assert b.counts.tolist() == [1, tokens - 1]
+    slope = 2.0 * np.array([1, tokens - 1]) / (float(tokens) * tokens)
+    assert (np.abs(doubles(b.slope) - slope) <= E * slope).all()
+    p = np.exp(doubles(x[:1])[0])
+    p /= p.sum()
+    loss = slope[0] * p[0] * (tokens - 1) + slope[1] * (p[1] * (tokens - 1) + 1)
+    # A spread of 1; a lane of 152 CTAs' 256 rows at a time adds 432 values, and 200 additions join the lanes.
+    assert abs(float(b.loss) - loss) <= (1 + 60 + 432 + 200) * E * loss
+
+
 def test_kernel_times_go_by_their_ids():
     x = make(3000, 64, torch.bfloat16, 1)
     one = torch.ones((), device="cuda")
