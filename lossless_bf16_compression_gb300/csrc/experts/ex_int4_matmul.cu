@@ -235,9 +235,15 @@ constexpr int cost_of(int columns) { return 2 + (columns + 7) / 8; }
 struct Pass {
   int group, row, rows;
 };
-// In shared memory, of each group and past the last: its first row, first pass, and the cost before it.
+// In shared memory, of each group and past the last: its first row and first pass.
 struct Passes {
-  int *start, *first, *cost;
+  int *start, *first;
+};
+// A CTA's part of the list, in lines of all passes, one pass's after the other's; and where it begins.
+struct Part {
+  size_t begin, end;
+  Pass pass;
+  int index, line;
 };
 
 template <int kEach, int kParts>
@@ -245,66 +251,122 @@ __device__ __forceinline__ int cost_of_rows(int rows) {
   const int rest = rows % kEach;
   return rows / kEach * cost_of(kEach * kParts) + (rest ? cost_of(rest * kParts) : 0);
 }
+// The first point of part b of `all`, shared out evenly.
+template <typename U>
+__device__ __forceinline__ U share(U all, unsigned b, unsigned parts) {
+  return all / parts * b + min(static_cast<U>(b), all % parts);
+}
+// Of a group with `rows` rows, its first passes and cost and those of all groups: whether this CTA's part begins or ends
+// in it.  U holds the cost of all lines: in 32 bits where it fits them, as long divisions take a microsecond.
+template <int kEach, int kParts, typename U>
+__device__ __forceinline__ void find_part(Part& part, int group, int row, int rows, int2 before, int2 all, int lines, bool last) {
+  constexpr int kFull = cost_of(kEach * kParts);
+  const U total = static_cast<U>(all.y) * lines, lower = static_cast<U>(before.y) * lines,
+          upper = lower + static_cast<U>(cost_of_rows<kEach, kParts>(rows)) * lines;
+  const U begin = share(total, blockIdx.x, gridDim.x), end = share(total, blockIdx.x + 1, gridDim.x);
+  const int full = rows / kEach;
+  const auto line_at = [&](U point) {  // of the group's
+    const U in = point - lower, whole = static_cast<U>(full) * kFull * lines;
+    return in < whole ? in / kFull : static_cast<U>(full) * lines + (in - whole) / cost_of(rows % kEach * kParts);
+  };
+  const size_t first = static_cast<size_t>(before.x) * lines;
+  if (begin >= lower && begin < upper) {
+    const U line = line_at(begin);
+    const int pass = static_cast<int>(line / lines);
+    part.begin = first + line;
+    part.index = before.x + pass;
+    part.line = static_cast<int>(line - static_cast<U>(pass) * lines);
+    part.pass = {group, row + pass * kEach, min(kEach, rows - pass * kEach)};
+  }
+  if (end >= lower && end < upper) part.end = first + line_at(end);
+  if (last) {
+    if (begin >= total) part.begin = static_cast<size_t>(all.x) * lines;
+    if (end >= total) part.end = static_cast<size_t>(all.x) * lines;
+  }
+}
+// The passes, and this CTA's part of them.  Only the warps that have groups work (of all sixteen, each instruction costs
+// a scheduler eight cycles).
 template <int kEach, int kParts>
-__device__ __forceinline__ void find_passes(const Job& p, const Passes& s) {
+__device__ __forceinline__ void find_passes(const Job& p, const Passes& s, int lines, Part& part) {
+  const auto put_part = [&](int g, int row, int rows, int2 before, int2 all) {
+    const bool last = g == p.groups - 1;
+    s.start[g] = row;
+    s.first[g] = before.x;
+    if (last) s.first[g + 1] = all.x;
+    if (static_cast<size_t>(all.y) * lines < (size_t(1) << 31)) find_part<kEach, kParts, unsigned>(part, g, row, rows, before, all, lines, last);
+    else find_part<kEach, kParts, size_t>(part, g, row, rows, before, all, lines, last);
+  };
   if (p.offsets == nullptr) {  // one group
-    if (threadIdx.x < 2) {
-      const int rows = threadIdx.x ? p.rows : 0;
-      s.start[threadIdx.x] = rows;
-      s.first[threadIdx.x] = (rows + kEach - 1) / kEach;
-      s.cost[threadIdx.x] = cost_of_rows<kEach, kParts>(rows);
+    if (threadIdx.x == 0) {
+      s.start[1] = p.rows;
+      put_part(0, 0, p.rows, make_int2(0, 0), make_int2((p.rows + kEach - 1) / kEach, cost_of_rows<kEach, kParts>(p.rows)));
     }
     __syncthreads();
     return;
   }
-  __shared__ int2 sums[kWarps];
+  __shared__ int2 sums[kWarps];  // of each warp's groups: passes and cost (below 0: an offset is wrong)
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   constexpr int kGroups = (ZC_MOE_MAX_EXPERTS + kThreads - 1) / kThreads;  // of a thread, the most
-  const int each = p.groups <= kThreads ? 1 : kGroups;
+  const int each = p.groups <= kThreads ? 1 : kGroups, warps = (p.groups + 32 * each - 1) / (32 * each);
   int begin[kGroups], rows[kGroups];
-  bool bad = false;
+  int2 upto = make_int2(0, 0), mine = upto, own[kGroups];
+  if (warp < warps) {
+    bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const int g = threadIdx.x * each + i;
-    begin[i] = rows[i] = 0;
-    if (i < each && g < p.groups) {
-      const int a = p.offsets[g], z = p.offsets[g + 1];
-      bad |= a < 0 || z < a || z > p.rows || (g == 0 && a != 0);
-      begin[i] = a;
-      rows[i] = z - a;
+    for (int i = 0; i < kGroups; ++i) {
+      const int g = threadIdx.x * each + i;
+      begin[i] = rows[i] = 0;
+      if (i < each && g < p.groups) {
+        const int a = p.offsets[g], z = p.offsets[g + 1];
+        bad |= a < 0 || z < a || z > p.rows || (g == 0 && a != 0);
+        begin[i] = a;
+        rows[i] = z - a;
+      }
     }
-  }
-  if (bad) set_error(p.status, ZC_ERR_CORRUPT);
-  bad = __syncthreads_or(bad);  // (then there are no passes: their rows could be anywhere)
-  int2 upto = make_int2(0, 0), own[kGroups];
+    if (bad) set_error(p.status, ZC_ERR_CORRUPT);
+    bad = __any_sync(~0u, bad);
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    if (bad) begin[i] = rows[i] = 0;
-    own[i] = make_int2((rows[i] + kEach - 1) / kEach, cost_of_rows<kEach, kParts>(rows[i]));
-    upto.x += own[i].x;
-    upto.y += own[i].y;
-  }
-  const int2 mine = upto;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int x = __shfl_up_sync(~0u, upto.x, d), y = __shfl_up_sync(~0u, upto.y, d);
-    if (lane >= d) upto.x += x, upto.y += y;
-  }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  upto.x -= mine.x;
-  upto.y -= mine.y;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) upto.x += sums[w].x, upto.y += sums[w].y;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const int g = threadIdx.x * each + i;
-    if (i < each && g < p.groups) {
-      s.start[g] = begin[i], s.first[g] = upto.x, s.cost[g] = upto.y;
+    for (int i = 0; i < kGroups; ++i) {
+      own[i] = bad ? make_int2(0, 0) : make_int2((rows[i] + kEach - 1) / kEach, cost_of_rows<kEach, kParts>(rows[i]));
       upto.x += own[i].x;
       upto.y += own[i].y;
-      if (g == p.groups - 1) s.start[g + 1] = bad ? p.rows : begin[i] + rows[i], s.first[g + 1] = upto.x, s.cost[g + 1] = upto.y;
+    }
+    mine = upto;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(~0u, upto.x, d), y = __shfl_up_sync(~0u, upto.y, d);
+      if (lane >= d) upto.x += x, upto.y += y;
+    }
+    if (lane == 31) sums[warp] = bad ? make_int2(0, -1) : upto;
+    if (warps == 1) __syncwarp();
+  }
+  if (warps > 1) __syncthreads();
+  if (warp < warps) {
+    upto.x -= mine.x;
+    upto.y -= mine.y;
+    int2 all = make_int2(0, 0);
+    bool bad = false;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warps) {
+        const int2 of = sums[w];
+        bad |= of.y < 0;
+        if (w < warp) upto.x += of.x, upto.y += of.y;
+        all.x += of.x;
+        all.y += of.y;
+      }
+    }
+    if (bad) all = upto = make_int2(0, 0);  // (then there are no passes: their rows could be anywhere)
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int g = threadIdx.x * each + i;
+      if (i < each && g < p.groups) {
+        if (bad) begin[i] = rows[i] = 0, own[i] = make_int2(0, 0);
+        if (g == p.groups - 1) s.start[g + 1] = bad ? p.rows : begin[i] + rows[i];
+        put_part(g, begin[i], rows[i], upto, all);
+        upto.x += own[i].x;
+        upto.y += own[i].y;
+      }
     }
   }
   __syncthreads();
@@ -323,30 +385,6 @@ __device__ __forceinline__ Pass pass_at(const Passes& s, int groups, int each, i
   const int g = group_of(s.first, groups, index), row = s.start[g] + (index - s.first[g]) * each;
   return {g, row, min(each, s.start[g + 1] - row)};
 }
-// The place, counted in lines of all passes, of a point of the total cost (`lines` times a pass's, line after line).  In 32
-// bits where the total fits them: long divisions take a microsecond.
-template <int kEach, int kParts, typename U>
-__device__ __forceinline__ size_t line_at(const Passes& s, int groups, int lines, U point) {
-  if (point >= static_cast<U>(s.cost[groups]) * lines) return static_cast<size_t>(s.first[groups]) * lines;
-  const int g = group_of(s.cost, groups, static_cast<int>(point / static_cast<U>(lines)));
-  const U in = point - static_cast<U>(s.cost[g]) * lines;
-  constexpr int kFull = cost_of(kEach * kParts);
-  const int rows = s.start[g + 1] - s.start[g], full = rows / kEach;
-  const U before = static_cast<U>(full) * kFull * lines;  // of the group's whole passes
-  const U line = in < before ? in / kFull : static_cast<U>(full) * lines + (in - before) / cost_of(rows % kEach * kParts);
-  return static_cast<size_t>(s.first[g]) * lines + line;
-}
-// The first line of part b of `parts`, for which the total cost is shared out evenly.
-template <int kEach, int kParts>
-__device__ __forceinline__ size_t first_line(const Passes& s, int groups, int lines, unsigned b, unsigned parts) {
-  const size_t all = static_cast<size_t>(s.cost[groups]) * lines;
-  if (all < (size_t(1) << 31)) {
-    const unsigned n = static_cast<unsigned>(all), each = n / parts, more = n % parts;
-    return line_at<kEach, kParts>(s, groups, lines, b * each + min(b, more));
-  }
-  return line_at<kEach, kParts>(s, groups, lines, all / parts * b + min(static_cast<size_t>(b), all % parts));
-}
-
 // ------------------------------------------------------------------ the product
 //
 // The work is a list of record rows, pass after pass, of which each CTA takes a run of equal length.  It goes through
@@ -374,31 +412,25 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
   Sums<NT>& sums = *reinterpret_cast<Sums<NT>*>(shared);
   uint4* xs = reinterpret_cast<uint4*>(shared + sizeof(Sums<NT>));
   int* tables = reinterpret_cast<int*>(xs + p.room * 128);
-  const Passes passes{tables, tables + p.groups + 1, tables + 2 * (p.groups + 1)};
+  const Passes passes{tables, tables + p.groups + 1};
+  __shared__ Part part_of_list;
   wait_for_previous();
   let_next_start();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
 
-  find_passes<kEach, kParts>(p, passes);
+  // A line: kTiles record rows.
+  const int record_rows = static_cast<int>(p.w.tiles()), blocks = static_cast<int>(p.w.blocks());
+  const int lines_each = (record_rows + kTiles - 1) / kTiles;  // of a pass
+  find_passes<kEach, kParts>(p, passes, lines_each, part_of_list);
   // The rows behind the last group.
   if (const int end = passes.start[p.groups]; end < p.rows) {
     const size_t step = static_cast<size_t>(gridDim.x) * kThreads, last = static_cast<size_t>(p.rows - end) * p.w.n;
     for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < last; i += step)
       put(p, end + i / p.w.n, i % p.w.n, 0.0f);
   }
-  // A line: kTiles record rows.
-  const int record_rows = static_cast<int>(p.w.tiles()), blocks = static_cast<int>(p.w.blocks());
-  const int lines_each = (record_rows + kTiles - 1) / kTiles;  // of a pass
-  // (Lanes 0 and 1 look up this CTA's first line and the next one's.)
-  const size_t bound = first_line<kEach, kParts>(passes, p.groups, lines_each, blockIdx.x + (lane & 1), gridDim.x);
-  const size_t begin = __shfl_sync(~0u, bound, 0);
-  int left = static_cast<int>(__shfl_sync(~0u, bound, 1) - begin);
+  int left = static_cast<int>(part_of_list.end - part_of_list.begin), index = part_of_list.index, line = part_of_list.line;
   if (left == 0) return;
-
-  int index = begin >> 32 ? static_cast<int>(begin / lines_each)  // of the pass
-                          : static_cast<int>(static_cast<unsigned>(begin) / static_cast<unsigned>(lines_each));
-  int line = static_cast<int>(begin - static_cast<size_t>(index) * lines_each);
-  Pass pass = pass_at(passes, p.groups, kEach, index);
+  Pass pass = part_of_list.pass;
 
   // What is in flight, and the scales, in the lanes: lane 4 g + t holds those of rows g and g + 8 of record
   // t % kTiles of block t / kTiles.
@@ -589,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
 
 template <typename T, int NT>
 cudaError_t run(Job p, const DeviceInfo& dev, cudaStream_t stream) {
-  const size_t tables = 3 * sizeof(int) * (p.groups + 1);
+  const size_t tables = 2 * sizeof(int) * (p.groups + 1);
   const int most_room = static_cast<int>((kShared - sizeof(Sums<NT>) - tables) / 2048) / (2 * NT) * (2 * NT);
   const cudaError_t err = allow_shared_memory<int4_product_kernel<T, NT>>(kShared);
   if (err != cudaSuccess) return err;
