@@ -65,9 +65,6 @@ struct Row {
 
   __device__ __forceinline__ static int lane() { return threadIdx.x % W; }
   __device__ __forceinline__ static int column(int i) { return (i / V * W + lane()) * V + i % V; }
-  // Where a column is: its lane, and the place among the lane's.
-  __device__ __forceinline__ static int lane_of(int column) { return column / V % W; }
-  __device__ __forceinline__ static int place_of(int column) { return column / (V * W) * V + column % V; }
   // Values past the row's end are -infinity.
   __device__ __forceinline__ void load(const T* row, int experts) {
     union {

@@ -395,6 +395,39 @@ def test_balance_of_more_rows_than_fp32_counts():
     assert abs(float(b.loss) - loss) <= (1 + 60 + 432 + 200) * E * loss
 
 
+# From 20 tokens for each of 152 SMs on, with up to 16 slots on rows of more than 128 logits (or more slots than a row's
+# lanes), a warp takes the slots of several tokens at once: sizes around that, every number of slots that share a warp,
+# slots without an expert, of an expert that the token may not use, and of the same expert twice.
+@pytest.mark.parametrize("score,normalize,dtype", [("softmax", True, torch.bfloat16), ("softmax", True, torch.float32),
+                                                   ("sigmoid", True, torch.float16), ("sigmoid", False, torch.float32)])
+@pytest.mark.parametrize("tokens,experts,k", [(3039, 130, 8), (3041, 130, 1), (3050, 200, 3), (3047, 256, 4), (3333, 256, 8),
+                                              (3041, 199, 9), (4001, 257, 16), (3042, 1000, 5), (3100, 40, 16), (3101, 64, 9)])
+@pytest.mark.parametrize("odd_slots", [False, True])
+def test_gradients_of_many_tokens(tokens, experts, k, score, normalize, dtype, odd_slots):
+    x = make(tokens, experts, dtype, tokens + k, masked=0.2, padded=0.05, pitch=experts + 3, at=1) if k % 2 else \
+        make(tokens, experts, dtype, tokens + k, masked=0.2, padded=0.05)
+    w, ids = moe.route(x, k, score, normalize)
+    b = moe.balance(x, ids, score)
+    if odd_slots:
+        ids = torch.randint(-2, experts + 2, (tokens, k), generator=torch.Generator().manual_seed(tokens)).int().cuda()
+        ids[::3, -1] = ids[::3, 0]
+    dw = torch.randn((tokens, k), generator=torch.Generator().manual_seed(k)).cuda()
+    v, i, slope = doubles(x), ids.cpu().numpy(), doubles(b.slope)
+    i = np.where((i >= 0) & (i < experts) & (np.take_along_axis(v, i.clip(0, experts - 1), 1) > -np.inf), i, -1)
+    want = oracle.route_grad(doubles(dw), v, i, score, normalize)
+    bound = grad_bound(v, doubles(dw), i, score, normalize)
+    if odd_slots:  # one addition for each further slot of an expert, at most k
+        bound = bound * (1 + k * E)
+    d = moe.route_grad(dw, x, ids, score, normalize)
+    assert (np.abs(doubles(d) - want) <= bound + half_ulp(dtype) * (np.abs(want) + bound) + smallest(dtype)).all()
+    d = moe.route_grad(dw, x, ids, score, normalize, balance=(torch.full((), 3.0, device="cuda"), b))
+    p = oracle.probabilities(v, score)
+    want = want + oracle.balance_grad(3.0, v, slope, score)
+    bound = bound + 3.0 * p * (slope + (p * slope).sum(1, keepdims=True)) * (2 * spread(v) + 180) * E
+    bound = bound + 2 * E * (np.abs(want) + bound)
+    assert (np.abs(doubles(d) - want) <= bound + half_ulp(dtype) * (np.abs(want) + bound) + smallest(dtype)).all()
+
+
 def test_kernel_times_go_by_their_ids():
     x = make(3000, 64, torch.bfloat16, 1)
     one = torch.ones((), device="cuda")
