@@ -1,9 +1,8 @@
 // ex_route.cu -- a router's choice: the k largest logits of each token, and their weights.
 //
 // The largest of a row is found k times: each lane offers the largest of its own that is left, the row's largest wins,
-// and the lane that had it goes on to its next one.  Bound by instructions (integer comparisons and moves: that pipe is
-// busy 86% of the cycles at 32768 x 256): one token 2.4 us, 32768 x 64 in fp32, eight chosen, 6.2, 16384 x 256 in
-// bfloat16 8.5, in fp32 10.5.
+// and the lane that had it goes on to its next one.  Bound by instructions (integer comparisons and moves): one token 2.2 us,
+// 32768 x 64 in fp32, eight chosen, 5.7, 16384 x 256 in bfloat16 6.7, in fp32 8.2 (values of 16 bits, many of them equal, 10.2).
 #include "ex_router.cuh"
 
 namespace zc {
@@ -22,21 +21,22 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 }
 constexpr uint32_t kNone = 0x007FFFFFu;  // of -infinity
 
-// The keys that are searched for a row's largest logits.
-//   16 bits: the logit's order above 0xFFFF - column: no two are equal, and equal logits go by column.
-//   fp32: the order with its last bits given to the number of the lane's register, N - 1 - i.  Two logits that differ in
-//   those bits alone, or not at all, may come in the wrong order: that is seen, and the row is searched again.
+// The keys that are searched for a row's largest logits; no two of a row are equal.
+//   16 bits: the logit's order above 0xFFFF - column: equal logits go by column.
+//   fp32: the order with its last bits (eight for a row of 256) given to the column.  Two logits that differ in those bits
+//   alone may come in the wrong order: that is seen, and the row is searched again.  (With three bits, for the lane's register
+//   alone, and the lane by a vote, it happened less, but every row took longer: 16384 x 256 10.5 us.)
 template <typename R>
 struct Keys {
   using T = typename R::T;
   static constexpr int N = R::N;
-  static constexpr bool kUnique = sizeof(T) == 2;
-  static constexpr uint32_t kLow = kUnique ? 0xFFFFu : N - 1;
+  static constexpr bool kExact = sizeof(T) == 2;
+  static constexpr uint32_t kLow = kExact ? 0xFFFFu : R::W * N - 1;
   static constexpr uint32_t kLeast = sizeof(T) == 2 && std::is_same_v<T, __half> ? 0x03FFFFFFu : kNone;
   uint32_t k[N];
 
   __device__ __forceinline__ explicit Keys(const R& row) {
-    if constexpr (kUnique) {
+    if constexpr (kExact) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         uint32_t w = pair_plus_zero(row.v[i], row.v[i + 1]), sign;
@@ -47,7 +47,7 @@ struct Keys {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) k[i] = (ordered(row.v[i]) & ~kLow) | (N - 1 - i);
+      for (int i = 0; i < N; ++i) k[i] = (ordered(row.v[i]) & ~kLow) | (kLow - R::column(i));
     }
   }
   __device__ __forceinline__ static uint32_t pair_plus_zero(__nv_bfloat16 a, __nv_bfloat16 b) {
@@ -150,43 +150,66 @@ __global__ void __launch_bounds__(32 * kWarps)
   K keys(row);
   keys.sort();
 
-  int e[2] = {-1, -1};  // the columns in this lane's slots
-  uint32_t best = keys.largest(), before = 0;
-  bool unsure = false;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t m = row_max<W>(best);
-    if (W == 32 && m <= K::kLeast) break;
-    int column;
-    if (K::kUnique) {
-      column = 0xFFFF - static_cast<int>(m & 0xFFFFu);
-    } else {
-      const unsigned who = __ballot_sync(~0u, best == m) >> (threadIdx.x % 32 / W * W) & (W == 32 ? ~0u : (1u << W % 32) - 1);
-      const int i = N - 1 - static_cast<int>(m & K::kLow);
-      column = (i / R::V * W + __ffs(who) - 1) * R::V + i % R::V;
-      unsure |= m > K::kLeast && ((who & (who - 1)) != 0 || (m ^ before) <= K::kLow);
-      before = m;
+  uint32_t got[2] = {0, 0}, best = keys.largest();  // the keys in this lane's slots; its largest one that is left
+  if (K::kSorted && k <= N) {
+    // (As many of a lane's keys go up as may still be asked for; the last may stay behind and look like one too near.)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (j == k) break;
+      const uint32_t m = row_max<W>(keys.k[0]);
+      if (lane == j) got[0] = m;
+      if (keys.k[0] == m) {
+#pragma unroll
+        for (int i = 0; i < N - 1 && i < N - j; ++i) keys.k[i] = keys.k[i + 1];
+      }
     }
-    if (m > K::kLeast && lane == (j & (W - 1))) {
-      if (W == 32 && j >= 32) e[1] = column;
-      else e[0] = column;
+    best = keys.k[0];
+  } else {
+    for (int j = 0; j < k; ++j) {
+      const uint32_t m = row_max<W>(best);
+      if (W == 32 && m <= K::kLeast) break;
+      if (lane == (j & (W - 1))) {
+        if (W == 32 && j >= 32) got[1] = m;
+        else got[0] = m;
+      }
+      if (best == m) best = keys.after(m);
     }
-    if (best == m) best = keys.after(m);
   }
-  if (!K::kUnique) {
-    const uint32_t m = row_max<W>(best);  // what is left may have been as large
-    unsure |= m > K::kLeast && (m ^ before) <= K::kLow;
+  const bool many = W == 32 && k > 32, softmax = score == ZC_SCORE_SOFTMAX;
+  int e[2];  // the columns
+#pragma unroll
+  for (int h = 0; h < 2; ++h) e[h] = got[h] > K::kLeast ? static_cast<int>(K::kLow - (got[h] & K::kLow)) : -1;
+  float x[2];  // (the chosen logits again, from the L1)
+  const auto gather = [&] {
+    x[0] = e[0] >= 0 ? to_float(from[e[0]]) : -kInf;
+    x[1] = many && e[1] >= 0 ? to_float(from[e[1]]) : -kInf;
+  };
+  gather();
+  if (!K::kExact) {
+    // Slots whose keys are near have to be in order by their logits, and the largest key that is left must not be near.
+    const uint32_t left = row_max<W>(best);
+    bool unsure = false;
+    const auto check = [&](int slot, uint32_t key, float v, uint32_t next_key, float next) {
+      if (slot >= k || key <= K::kLeast) return;
+      unsure |= slot == k - 1 ? (key ^ left) <= K::kLow : (key ^ next_key) <= K::kLow && !(v >= next);
+    };
+    uint32_t next_key = __shfl_down_sync(~0u, got[0], 1, W);
+    float next = __shfl_down_sync(~0u, x[0], 1, W);
+    if (many) {
+      const uint32_t first_key = __shfl_sync(~0u, got[1], 0);
+      const float first = __shfl_sync(~0u, x[1], 0);
+      if (lane == 31) next_key = first_key, next = first;
+    }
+    check(lane, got[0], x[0], next_key, next);
+    if (many) check(lane + 32, got[1], x[1], __shfl_down_sync(~0u, got[1], 1), __shfl_down_sync(~0u, x[1], 1));
     if (__any_sync(~0u, unsure)) {
       const int2 again = search_again<R>(from, real ? experts : 0, k);
       e[0] = again.x;
       e[1] = again.y;
+      gather();
     }
   }
 
-  // (The chosen logits again, from the L1.)
-  const bool many = W == 32 && k > 32, softmax = score == ZC_SCORE_SOFTMAX;
-  float x[2] = {-kInf, -kInf};
-  if (e[0] >= 0) x[0] = to_float(from[e[0]]);
-  if (many && e[1] >= 0) x[1] = to_float(from[e[1]]);
   const float top = __shfl_sync(~0u, x[0], 0, W);
   const auto value = [&](int h) {
     return e[h] < 0 ? 0.0f : softmax ? expf(x[h] - top) : scaled_sigmoid(x[h], normalize ? fminf(top, 0.0f) : 0.0f).s;

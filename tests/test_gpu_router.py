@@ -360,6 +360,33 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(d[-5:], moe.route_grad(torch.ones_like(w2), tail, ids2, balance=(torch.ones((), device="cuda"), b)))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("experts", [32, 64, 100, 128, 256])
+def test_all_chosen_logits_in_one_lane(experts, dtype):
+    """A lane holds eight neighbouring columns of 16 bits, or four and the four half a row of lanes further on."""
+    half = max(16, 1 << (experts - 1).bit_length() - 1)
+    x = make(64, experts, dtype, 5)
+    for t in range(64):
+        first = t * 4 % (experts - 8)
+        cols = [c for c in range(first // 8 * 8, first // 8 * 8 + 8)] if t % 2 else \
+            [c for c in range(first % half, first % half + 4)] + [c + half for c in range(first % half, first % half + 4) if c + half < experts]
+        x[t, cols] = torch.linspace(20, 30 + t % 3, len(cols), device="cuda").to(dtype)
+    for k in (1, 7, 8, 9, 16):
+        check_route(x, k, "softmax", True)
+
+
+@pytest.mark.parametrize("experts,k", [(64, 8), (256, 8), (256, 5), (40, 6), (1000, 8), (256, 40), (64, 64)])
+def test_fp32_logits_that_are_close(experts, k):
+    """Values a step or a few apart, in groups that the choice cuts through, and equal ones."""
+    rng = np.random.default_rng(experts + k)
+    x = np.repeat(rng.standard_normal((200, -(-experts // 5))).astype(np.float32), 5, 1)[:, :experts]
+    steps = rng.integers(-3, 4, x.shape) * (rng.random((200, 1)) < 0.7)
+    x = (x.view(np.int32) + steps.astype(np.int32)).view(np.float32)
+    x = rng.permuted(x, axis=1)
+    check_route(torch.from_numpy(x).cuda(), k, "softmax", True)
+    check_route(torch.from_numpy(x).cuda(), k, "sigmoid", False)
+
+
 # The largest batches of one CTA, one more, the largest of a cluster, one more: by the experts of a row.
 @pytest.mark.parametrize("tokens,experts,k", [(512, 20, 3), (513, 20, 3), (4096, 32, 1), (4097, 32, 9), (257, 64, 8), (2048, 40, 6),
                                               (2049, 64, 2), (129, 100, 5), (1024, 128, 3), (1025, 128, 3), (65, 256, 8),
