@@ -215,6 +215,7 @@ struct Job {
   int rows, groups, out_type;
   int room;  // for x in shared memory: blocks of eight columns
   bool aligned;
+  unsigned parts_inverse, lines_inverse;  // of the CTAs, and of a pass's lines
 };
 
 __device__ __forceinline__ void put(const Job& p, size_t row, size_t col, float v) {
@@ -251,28 +252,34 @@ __device__ __forceinline__ int cost_of_rows(int rows) {
   const int rest = rows % kEach;
   return rows / kEach * cost_of(kEach * kParts) + (rest ? cost_of(rest * kParts) : 0);
 }
-// The first point of part b of `all`, shared out evenly.
-template <typename U>
-__device__ __forceinline__ U share(U all, unsigned b, unsigned parts) {
-  return all / parts * b + min(static_cast<U>(b), all % parts);
+// a / b, with inverse = floor((2^32 - 1) / b): the product's upper half is the quotient or one less.
+__device__ __forceinline__ unsigned quotient(unsigned a, unsigned b, unsigned inverse) {
+  const unsigned q = __umulhi(a, inverse);
+  return q + (a - q * b >= b);
 }
+__device__ __forceinline__ size_t quotient(size_t a, unsigned b, unsigned) { return a / b; }
 // Of a group with `rows` rows, its first passes and cost and those of all groups: whether this CTA's part begins or ends
 // in it.  U holds the cost of all lines: in 32 bits where it fits them, as long divisions take a microsecond.
 template <int kEach, int kParts, typename U>
-__device__ __forceinline__ void find_part(Part& part, int group, int row, int rows, int2 before, int2 all, int lines, bool last) {
+__device__ __forceinline__ void find_part(const Job& p, Part& part, int group, int row, int rows, int2 before, int2 all, int lines,
+                                          bool last) {
   constexpr int kFull = cost_of(kEach * kParts);
   const U total = static_cast<U>(all.y) * lines, lower = static_cast<U>(before.y) * lines,
           upper = lower + static_cast<U>(cost_of_rows<kEach, kParts>(rows)) * lines;
-  const U begin = share(total, blockIdx.x, gridDim.x), end = share(total, blockIdx.x + 1, gridDim.x);
+  const U each = quotient(total, gridDim.x, p.parts_inverse), more = total - each * gridDim.x;  // shared out evenly
+  const U begin = each * blockIdx.x + min(static_cast<U>(blockIdx.x), more), end = begin + each + (blockIdx.x < more);
   const int full = rows / kEach;
   const auto line_at = [&](U point) {  // of the group's
-    const U in = point - lower, whole = static_cast<U>(full) * kFull * lines;
-    return in < whole ? in / kFull : static_cast<U>(full) * lines + (in - whole) / cost_of(rows % kEach * kParts);
+    const U in = point - lower, whole = static_cast<U>(full) * kFull * lines, rest = in - whole;
+    if (in < whole) return in / kFull;
+    const int cost = cost_of(rows % kEach * kParts);
+    return static_cast<U>(full) * lines + (cost == 3 ? rest / 3 : rest / 4);
   };
+  static_assert(cost_of(1) == 3 && cost_of(16) == 4);
   const size_t first = static_cast<size_t>(before.x) * lines;
   if (begin >= lower && begin < upper) {
     const U line = line_at(begin);
-    const int pass = static_cast<int>(line / lines);
+    const int pass = static_cast<int>(quotient(line, lines, p.lines_inverse));
     part.begin = first + line;
     part.index = before.x + pass;
     part.line = static_cast<int>(line - static_cast<U>(pass) * lines);
@@ -293,8 +300,8 @@ __device__ __forceinline__ void find_passes(const Job& p, const Passes& s, int l
     s.start[g] = row;
     s.first[g] = before.x;
     if (last) s.first[g + 1] = all.x;
-    if (static_cast<size_t>(all.y) * lines < (size_t(1) << 31)) find_part<kEach, kParts, unsigned>(part, g, row, rows, before, all, lines, last);
-    else find_part<kEach, kParts, size_t>(part, g, row, rows, before, all, lines, last);
+    if (static_cast<size_t>(all.y) * lines < (size_t(1) << 31)) find_part<kEach, kParts, unsigned>(p, part, g, row, rows, before, all, lines, last);
+    else find_part<kEach, kParts, size_t>(p, part, g, row, rows, before, all, lines, last);
   };
   if (p.offsets == nullptr) {  // one group
     if (threadIdx.x == 0) {
@@ -344,17 +351,15 @@ __device__ __forceinline__ void find_passes(const Job& p, const Passes& s, int l
   if (warp < warps) {
     upto.x -= mine.x;
     upto.y -= mine.y;
-    int2 all = make_int2(0, 0);
-    bool bad = false;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warps) {
-        const int2 of = sums[w];
-        bad |= of.y < 0;
-        if (w < warp) upto.x += of.x, upto.y += of.y;
-        all.x += of.x;
-        all.y += of.y;
-      }
+    const int2 of = lane < warps ? sums[lane] : make_int2(0, 0);
+    const bool bad = __any_sync(~0u, of.y < 0);
+    int2 all = of;
+    if (warps > 1) {
+      all = make_int2(__reduce_add_sync(~0u, of.x), __reduce_add_sync(~0u, of.y));
+      upto.x += __reduce_add_sync(~0u, lane < warp ? of.x : 0);
+      upto.y += __reduce_add_sync(~0u, lane < warp ? of.y : 0);
+    } else {
+      all = make_int2(__shfl_sync(~0u, of.x, 0), __shfl_sync(~0u, of.y, 0));
     }
     if (bad) all = upto = make_int2(0, 0);  // (then there are no passes: their rows could be anywhere)
 #pragma unroll
@@ -629,7 +634,10 @@ cudaError_t run(Job p, const DeviceInfo& dev, cudaStream_t stream) {
   p.room = wanted < most_room ? wanted : most_room;
   const size_t passes = (static_cast<size_t>(p.rows) * Parts<T>::n + 8 * NT - 1) / (8 * NT) + (p.groups < p.rows ? p.groups : p.rows);
   const size_t most = passes * p.w.tiles(), sms = static_cast<size_t>(dev.sm_count);
-  return launch(ZC_KERNEL_INT4_PRODUCT, int4_product_kernel<T, NT>, static_cast<unsigned>(most < sms ? most : sms), kThreads,
+  const unsigned ctas = static_cast<unsigned>(most < sms ? most : sms);
+  p.parts_inverse = ~0u / ctas;
+  p.lines_inverse = ~0u / static_cast<unsigned>((p.w.tiles() + kTiles - 1) / kTiles);
+  return launch(ZC_KERNEL_INT4_PRODUCT, int4_product_kernel<T, NT>, ctas, kThreads,
                 sizeof(Sums<NT>) + static_cast<size_t>(p.room) * 2048 + tables, stream, p);
 }
 
