@@ -25,9 +25,6 @@ constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kColumnPitch = 20;  // of 16 partial sums (in fp32), free of bank conflicts
 constexpr size_t kShared = 226 * 1024;
 
-__device__ __forceinline__ uint32_t shared_address(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 // The 16-bit type that x and the weights are multiplied in: x's own, or bfloat16 for the parts of fp32.
 template <typename T>
 using Form = std::conditional_t<std::is_same_v<T, __half>, __half, __nv_bfloat16>;
@@ -146,8 +143,11 @@ __device__ __forceinline__ void split(const T (&v)[8], uint4 (&out)[Parts<T>::n]
 
 // Puts `count` blocks of `rows` rows of x, from block `first` on, where the products read them: for each block and
 // eight columns 4 x 512 bytes, in the c-th of which lane 4 g + t finds values 32 t + 8 c .. + 7 of column g (in the place of
-// lane 4 (g ^ 1) + t for odd c, so that the rows that come in meet in half as many banks).  bfloat16 on whole vectors is
-// copied asynchronously: staged() waits for it.
+// lane 4 (g ^ 1) + t for odd c, so that the rows that come in meet in half as many banks).  By loads and stores, four
+// vectors at a time: asynchronous copies to such scattered places take longer even where there is something to do meanwhile
+// (one row of 4096 x 7168 8.5 us instead of 6.9, eight rows 15.4 and 9.3, 256 rows over 16 experts 69 and 60), eight at
+// a time a little longer.
+constexpr int kBatch = 4;
 template <typename T>
 __device__ __forceinline__ void stage(const T* x, size_t pitch, int rows, int first, int count, size_t k, bool aligned,
                                       int tiles, uint4* to) {
@@ -161,45 +161,46 @@ __device__ __forceinline__ void stage(const T* x, size_t pitch, int rows, int fi
     const auto place = [&](int column) {
       return to + ((block * tiles + column / 8) * 4 + c) * 32 + ((column % 8 * 4 + t) ^ (c & 1) * 4);
     };
-    for (int r = row0; r < rows; r += side) {
-      const T* from = x + r * pitch + col;
-      if constexpr (Parts<T>::n == 1) {
-        if (aligned) {  // (past the end of the row: zeros)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(place(r))), "l"(col < k ? from : x),
-                       "r"(col < k ? 16 : 0)
-                       : "memory");
-          continue;
-        }
+    constexpr int kVectors = 8 * sizeof(T) / 16, kEach = 16 / sizeof(T), kRows = kBatch / kVectors;
+    const auto put_row = [&](int row, const T(&values)[8]) {
+      uint4 out[Parts<T>::n];
+      split<T>(values, out);
+#pragma unroll
+      for (int p = 0; p < Parts<T>::n; ++p) *place(row * Parts<T>::n + p) = out[p];
+    };
+    if (aligned) {
+      for (int r = row0; r < rows; r += kRows * side) {
+        alignas(16) T in[kRows][8];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int j = 0; j < kVectors; ++j)  // (past the end of the row: zeros)
+            reinterpret_cast<uint4*>(in[i])[j] =
+                load_if(x + (r + i * side) * pitch + col + j * kEach, col + j * kEach < k && r + i * side < rows);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (r + i * side < rows) put_row(r + i * side, in[i]);
       }
-      // Whole vectors, or each put together from the two aligned ones that hold it; zeros past the row's end.
-      constexpr int kVectors = 8 * sizeof(T) / 16, kEach = 16 / sizeof(T);
+      continue;
+    }
+    for (int r = row0; r < rows; r += side) {
+      // Each vector put together from the two aligned ones that hold it; zeros past the row's end.
+      const T* from = x + r * pitch + col;
       alignas(16) T in[8];
       uint4* whole = reinterpret_cast<uint4*>(in);
-      if (aligned) {
+      const unsigned shift = low4(from);
+      const uint8_t *at = reinterpret_cast<const uint8_t*>(from) - shift, *end = reinterpret_cast<const uint8_t*>(x + r * pitch + k);
+      uint4 w[kVectors + 1];
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) whole[j] = load_if(from + j * kEach, col + j * kEach < k);
-      } else {
-        const unsigned shift = low4(from);
-        const uint8_t *at = reinterpret_cast<const uint8_t*>(from) - shift, *end = reinterpret_cast<const uint8_t*>(x + r * pitch + k);
-        uint4 w[kVectors + 1];
+      for (int j = 0; j <= kVectors; ++j) w[j] = load_if(at + 16 * j, at + 16 * j < end && (j < kVectors || shift != 0));
 #pragma unroll
-        for (int j = 0; j <= kVectors; ++j) w[j] = load_if(at + 16 * j, at + 16 * j < end && (j < kVectors || shift != 0));
+      for (int j = 0; j < kVectors; ++j) whole[j] = shift_bytes<true>(w[j], w[j + 1], shift);
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) whole[j] = shift_bytes<true>(w[j], w[j + 1], shift);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j >= k) in[j] = from_float<T>(0.0f);
-      }
-      uint4 out[Parts<T>::n];
-      split<T>(in, out);
-#pragma unroll
-      for (int p = 0; p < Parts<T>::n; ++p) *place(r * Parts<T>::n + p) = out[p];
+      for (int j = 0; j < 8; ++j)
+        if (col + j >= k) in[j] = from_float<T>(0.0f);
+      put_row(r, in);
     }
   }
-}
-__device__ __forceinline__ void staged() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
 }
 
 struct Job {
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
   fetch_scales(now);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(i, now);
-  staged();
+  __syncthreads();
 
   for (;;) {
     // The round after this one.
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       if (NT == 1 || tiles == 1) blocks_of(std::integral_constant<int, 1>());
       else blocks_of(std::integral_constant<int, NT>());
       if (!last) {
-        staged();
+        __syncthreads();
         half ^= 1;
       }
     }
@@ -609,9 +610,9 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       __syncthreads();
       half = 0;
       bring(next_pass, 0, 0);
-      staged();
+      __syncthreads();
     } else if (!resident) {  // on its way
-      staged();
+      __syncthreads();
       half ^= 1;
     } else if (sharing > 1) {
       __syncthreads();
