@@ -1,7 +1,7 @@
 // ex_int4.cu -- weights in 4 bits: rounding them, and the values that they stand for.
 //
 // Bound by DRAM where rows are whole 16-byte vectors (16 x 2048 x 7168: bfloat16 98 us, 6.0 TB/s, fp32 181, 5.9; values in
-// bfloat16 87, 6.8, in fp32 158, 6.7).  Unaligned rows are rounded value by value (4 x 2047 x 7167 in bfloat16 61 us).
+// bfloat16 87, 6.8, in fp32 158, 6.7).  Unaligned rows: 4 x 2047 x 7167 in bfloat16 47 us, in fp32 72.
 //
 // A warp takes one record, 16 rows x 128 columns: lane 4 g + t holds columns 8 (t + 4 c), c = 0 .. 3, of rows g and
 // g + 8, so that four lanes read 64 neighbouring values and the lanes of a row share its group's scale by two
@@ -48,6 +48,20 @@ struct Eight {
     if (Aligned) {
 #pragma unroll
       for (int i = 0; i < kVectors; ++i) v[i] = load_if(row + col + i * kEach, col + i * kEach < cols);
+    } else if constexpr (sizeof(T) == 2) {
+      // Put together from the two aligned vectors that hold it.  (4 x 2047 x 7167 47 us, and 63 value by value; fp32, which
+      // has three for two, 82 and 72.)
+      const unsigned shift = low4(row + col);
+      const uint8_t *at = reinterpret_cast<const uint8_t*>(row + col) - shift, *end = reinterpret_cast<const uint8_t*>(row + cols);
+      const uint4 a = load_if(at, at < end), b = load_if(at + 16, at + 16 < end && shift != 0);
+      Pack<T, 16> p;
+      p.raw = shift_bytes<true>(a, b, shift);
+      if (col + 8 > cols) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j >= cols) p.v[j] = from_float<T>(0.0f);
+      }
+      v[0] = p.raw;
     } else {
       Pack<T, 16> p[kVectors];
 #pragma unroll
