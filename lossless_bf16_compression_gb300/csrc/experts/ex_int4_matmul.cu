@@ -8,11 +8,11 @@
 // multiplies the group's sum, once for 128 products.
 //
 // fp32 rows of x are split into three bfloat16 values that add up to them exactly; they are columns of their own, added
-// at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.1 us (59 MB; 2 us of launch,
-// 4 of looking up the work, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 105 us (485 MB: 4.9 TB/s; 81 without
-// the loads, 24 without loads, unpacking and products), nine to sixteen 135 to 148.  A scheduler's two cycles for each logic
-// operation and eight for a product make 40 us of unpacking and 25 of products (sixteen columns: 50); four warps, which is
-// what the registers hold, overlap these in part.
+// at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.0 us (59 MB; 2 us of launch,
+// 3 of finding the work and bringing x, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 100 us (485 MB: 4.9 TB/s;
+// without the loads about 80, without unpacking and products too 24), nine to sixteen 128 to 132.  A scheduler's two cycles
+// for each logic operation and eight for a product make 40 us of unpacking and 25 of products (sixteen columns: 50); four
+// warps, which is what the registers hold, overlap these in part.
 #include <type_traits>
 
 #include "ex_int4.cuh"
@@ -391,13 +391,15 @@ __device__ __forceinline__ Pass pass_at(const Passes& s, int groups, int each, i
   const int g = group_of(s.first, groups, index), row = s.start[g] + (index - s.first[g]) * each;
   return {g, row, min(each, s.start[g + 1] - row)};
 }
+
 // ------------------------------------------------------------------ the product
 //
-// The work is a list of record rows, pass after pass, of which each CTA takes a run of equal length.  It goes through
+// The work is a list of record rows, pass after pass, of which each CTA takes a run of equal cost.  It goes through
 // them in rounds of up to a record row for each warp, of one pass; where fewer are left the warps share the blocks of
 // each, and their sums are added in their order.  The pass's x lies in shared memory, all of it where it fits, else
-// in chunks of k, one read while the next one comes in.  A warp asks for the first blocks of its next record row (or
-// chunk) while it works on the last ones of this.
+// in chunks of k, two at a time: the next one is brought before this one is read, so that warps that are done with this one
+// wait for the others alone.  A warp asks for the first blocks of its next record row (or chunk) while it works on the last
+// ones of this.
 
 struct Phase {  // what a warp reads next: `count` records from this one on, and as many `apart` further on
   uint32_t record, apart;
@@ -643,7 +645,8 @@ cudaError_t run(Job p, const DeviceInfo& dev, cudaStream_t stream) {
 }
 
 // Sixteen columns at a time, or eight where there are no more.  (Thirty-two leave the tensor cores, at 1024 products a
-// cycle and SM, no room to hide in: 256 rows over 16 experts of 2048 x 7168 took 83 us with it and 70 without.)
+// cycle and SM, no room to hide in: 256 rows over 16 experts of 2048 x 7168 took 83 us with it and 70 without, while x
+// came by asynchronous copies.)
 template <typename T>
 cudaError_t by_rows(const Job& p, const DeviceInfo& dev, cudaStream_t stream) {
   return static_cast<size_t>(p.rows) * Parts<T>::n <= 8 ? run<T, 1>(p, dev, stream) : run<T, 2>(p, dev, stream);

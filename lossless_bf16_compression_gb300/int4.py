@@ -6,9 +6,9 @@
 ``offsets`` is int32 [experts + 1] on the device, as ``moe.Plan.offsets``; None stands for one group of all the rows.
 A group's values are whole numbers of -7 to 7 times a bfloat16 scale, the smallest that reaches a seventh of the group's
 largest magnitude.  The products take x as it is (bfloat16, float16 or float32, any row stride), sum in float32 and round
-once.  They are made for a few rows for each expert, where the weights' bytes count: from about a dozen rows for an expert on
-``fp8.matmul`` is the faster one (16 experts of 2048 x 7168, one row each: 33 us against 48 with ``fp8.quantize``; eight 39
-and 49, sixteen 56 and 49, 128 260 and 60).  Any number is right.  Every call runs on ``stream`` (default: the current one) and does not
+once.  They are made for a few rows for each expert, where the weights' bytes count: from about sixteen rows for an expert on
+``fp8.matmul`` is the faster one (16 experts of 2048 x 7168, one row each: 33 us against 48 with ``fp8.quantize``; eight 36
+and 49, sixteen 49 and 49, 128 237 and 60).  Any number is right.  Every call runs on ``stream`` (default: the current one) and does not
 synchronize.
 
 Results have no autograd history, and these weights have no gradients: a tensor that requires one is refused while
