@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * balance_warps<R>())
 
 // The CTAs' parts added: one cluster, each of its CTAs a share of the experts, for every expert several threads that
 // read at the same time.
-constexpr int kSettleThreads = 1024, kSettleCtas = 8;
+constexpr int kSettleThreads = 1024, kSettleCtas = 8, kAtOnce = 5;  // (parts that a thread asks for together: all, of 256 experts)
 __global__ void __launch_bounds__(kSettleThreads) __cluster_dims__(kSettleCtas, 1, 1)
     settle_kernel(void* workspace, int ctas, int experts, int k, int each, float inverse, float* loss, int* counts, float* slope) {
   __shared__ float sums[kSettleThreads];
@@ -241,29 +241,46 @@ __global__ void __launch_bounds__(kSettleThreads) __cluster_dims__(kSettleCtas, 
   // (Divisions by a factor: the distance of (a + 1/2) / b from a whole number is at least 1 / 2b, and a is at most 1024.)
   const auto over_each = [&](int a) { return static_cast<int>((a + 0.5f) * inverse); };
   const int readers = min(32, over_each(kSettleThreads)), reader = over_each(threadIdx.x), e = begin + threadIdx.x - reader * each;
+  int n = threadIdx.x < ctas ? parts.tokens[threadIdx.x] : 0;
   float s = 0;
   int c = 0;
   if (reader < readers && e < end) {
-#pragma unroll 8
-    for (int b = reader; b < ctas; b += readers) {
-      s += parts.sums[static_cast<size_t>(b) * experts + e];
-      c += parts.counts[static_cast<size_t>(b) * experts + e];
+    for (int first = reader; first < ctas; first += kAtOnce * readers) {
+      float sum[kAtOnce];
+      int count[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int b = first + i * readers;
+        sum[i] = b < ctas ? parts.sums[static_cast<size_t>(b) * experts + e] : 0.0f;
+        count[i] = b < ctas ? parts.counts[static_cast<size_t>(b) * experts + e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) s += sum[i], c += count[i];
     }
   }
-  const int n = __reduce_add_sync(~0u, threadIdx.x < ctas ? parts.tokens[threadIdx.x] : 0);
+  n = __reduce_add_sync(~0u, n);
   sums[threadIdx.x] = s;
   totals[threadIdx.x] = c;
   if (lane == 0) live[warp] = n;
+  __syncthreads();
+  // The readers' sums (up to 32), to eight and then to one.
+  if (threadIdx.x < 8 * each && readers > 8) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      const int at = threadIdx.x + i * 8 * each;
+      if (at < readers * each) s += sums[at], c += totals[at];
+    }
+    sums[threadIdx.x] = s;
+    totals[threadIdx.x] = c;
+  }
   __syncthreads();
   if (threadIdx.x < (each + 31) / 32 * 32) {  // whole warps
     const Unit unit = unit_of(experts, k, __reduce_add_sync(~0u, live[lane]));
     float mine = 0;
     if (threadIdx.x < end - begin) {
-#pragma unroll 8
-      for (int r = 1; r < readers; ++r) {
-        s += sums[r * each + threadIdx.x];
-        c += totals[r * each + threadIdx.x];
-      }
+#pragma unroll
+      for (int r = 1; r < 8; ++r)
+        if (r < readers) s += sums[r * each + threadIdx.x], c += totals[r * each + threadIdx.x];
       const float u = times(c, unit);
       counts[e] = c;
       slope[e] = u;
