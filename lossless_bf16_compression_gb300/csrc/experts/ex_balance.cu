@@ -3,8 +3,9 @@
 // Each lane keeps the sums of its columns' probabilities in registers over all of its tokens; the warps' are added in
 // shared memory in their order, the CTAs' by the first of a cluster or by a second kernel, in theirs, so nothing depends on
 // timing.  The counts are whole numbers, for which order does not matter.  Bound by latency and by the exponentials: 64 x 64
-// 4.4 us, 777 x 40 5.1 (a cluster; by two kernels 7.5 and by this one 6.9 while divisions and one id at a time stood in
-// the way), 32768 x 64 in fp32 8.4, 16384 x 256 in bfloat16 9.5, of which the second kernel takes about 2.5.
+// 4.3 us, 777 x 40 5.1 (a cluster; by two kernels 7.5 and by this one 6.9 while divisions and one id at a time stood in
+// the way), 32768 x 64 in fp32 7.0, 16384 x 256 in bfloat16 8.6, of which the second kernel takes about 1.5 (2.5 while a
+// thread asked for one part after the other).
 #include "ex_router.cuh"
 
 namespace zc {

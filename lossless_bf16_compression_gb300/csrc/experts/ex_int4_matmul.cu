@@ -587,10 +587,21 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
         for (int i = 0; i < 4; ++i) sums.of[warp][h][8 * n + 2 * t + i % 2][g + i / 2 * 8] = sum[h][n][i];
     const auto result = [&](int at, int r, int c) {  // row r of the pass, weight row c of the at-th line
       float v = 0;
-#pragma unroll 4
-      for (int h = 0; h < sharing; ++h)
+      const auto add = [&](auto most) {  // of up to `most` warps, all asked for together
+        float part[decltype(most)::value][kParts];
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) v += sums.of[h * lines + at][c / kInt4Rows][r * kParts + q][c % kInt4Rows];
+        for (int h = 0; h < decltype(most)::value; ++h)
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+            part[h][q] = h < sharing ? sums.of[h * lines + at][c / kInt4Rows][r * kParts + q][c % kInt4Rows] : 0.0f;
+#pragma unroll
+        for (int h = 0; h < decltype(most)::value; ++h)
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) v += part[h][q];
+      };
+      if (sharing == 1) add(std::integral_constant<int, 1>());
+      else if (sharing <= 4) add(std::integral_constant<int, 4>());
+      else add(std::integral_constant<int, kWarps>());
       const size_t column = static_cast<size_t>(line + at) * (kTiles * kInt4Rows) + c;
       if (column < p.w.n) put(p, pass.row + r, column, weight_unit<F>() * v);
     };
