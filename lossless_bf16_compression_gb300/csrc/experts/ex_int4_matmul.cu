@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       Phase next{0, 0, 0};
       if (!last) next = phase(pass, line, lines, c + 1);
       else if (next_lines > 0) next = phase(next_pass, next_line, next_lines, 0);
-      // The chunk after this one, into the other half: of this pass, in this round or the next.
+      // The chunk after this one, into the other half: of this pass, for the same lines or the next ones.
       if (!resident && (!last || (next_lines > 0 && next_line > 0))) bring(pass, last ? 0 : c + 1, half ^ 1);
       // (Columns past the pass's hold whatever was there: they only reach sums that no one reads.)
       const auto blocks_of = [&](auto column_tiles) {
