@@ -50,7 +50,8 @@ int zc_moe_balance(const void* logits, size_t pitch, int type, const int* ids, s
 /* The gradient with respect to the logits: of sum over slots of d_weights * weights (zc_moe_route with the same
  * score, normalize and scale, and the ids that it chose), plus d_loss times that of the balance loss with this
  * slope.  Either part may be left out: d_weights and ids null, or d_loss and slope null (not both).  Slots with an
- * id outside [0, experts) add nothing; logits of -infinity and rows of padding get 0.  Sums in fp32, rounded once.
+ * id outside [0, experts), or whose logit is -infinity, add nothing, whatever their d_weights; logits of -infinity and
+ * rows of padding get 0.  Sums in fp32, rounded once.
  *   d_weights  tokens x k fp32;  d_loss  1 fp32;  d_logits  rows like logits, of the same type. */
 int zc_moe_route_grad(const float* d_weights, const int* ids, const float* d_loss, const float* slope,
                       const void* logits, size_t pitch, int type, size_t tokens, int experts, int k, int score,

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(32 * kWarps, (ctas<R, Dense>()))
   // (A warp goes on while it has a token: its first is the one that ends last.)
   for (; t - threadIdx.x % 32 / W < tokens; t += step) {
     const T* row = logits + t * pitch;
-    // A slot without an expert, or one that the token may not use, has e = -1 and g = 0.
+    // A slot without an expert has x = -infinity, e = -1 and g = 0; so has, below, one that the token may not use.
     float g[2] = {0, 0}, x[2] = {-kInf, -kInf};
     int e[2] = {-1, -1};
 #pragma unroll
@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(32 * kWarps, (ctas<R, Dense>()))
     if (Dense)
       whole_row(r, a, softmax, [&](float largest) {
         if (!whole) return 0.0f;
-        return (e[0] < 0 ? 0.0f : g[0] * expf(x[0] - largest)) + (!many || e[1] < 0 ? 0.0f : g[1] * expf(x[1] - largest));
+        // (Asked of x, not of e, which still names experts that the token may not use: their g may be anything.)
+        return (x[0] == -kInf ? 0.0f : g[0] * expf(x[0] - largest)) + (x[1] == -kInf ? 0.0f : g[1] * expf(x[1] - largest));
       }, d, top, factor);
     if (Slots) {
       float c[2] = {0, 0};
