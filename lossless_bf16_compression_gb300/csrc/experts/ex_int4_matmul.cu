@@ -7,8 +7,8 @@
 // rows at a time, too coarse for one token's experts, and the unpacked weights written out first).  The group's scale
 // multiplies the group's sum, once for 128 products.
 //
-// fp32 rows of x are split into three bfloat16 values that add up to them exactly; they are columns of their own, added
-// at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.0 us (59 MB; 2 us of launch,
+// fp32 rows of x are split into three bfloat16 values that add up to them exactly, the second held 2^8 times its size and the
+// third 2^16 times; they are columns of their own, added at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.0 us (59 MB; 2 us of launch,
 // 3 of finding the work and bringing x, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 100 us (485 MB: 4.9 TB/s;
 // without the loads about 80, without unpacking and products too 24), nine to sixteen 128 to 132.  A scheduler's two cycles
 // for each logic operation and eight for a product make 40 us of unpacking and 25 of products (sixteen columns: 50); four
@@ -119,7 +119,10 @@ __device__ __forceinline__ uint32_t lead(float& v) {
   return top >> 16;
 }
 
-// Eight neighbouring values as `Parts` vectors of eight bfloat16.
+// Eight neighbouring values as `Parts` vectors of eight bfloat16, each part kPartUnit^-1 times its size: so lifted a part is as
+// large as the one before it at most twice, which fp32's largest value allows, and its last bit is not below bfloat16's smallest
+// number where x's is not below fp32's.  (Unlifted, x below 2^-110 lost its last bits, and large scales showed it.)
+constexpr float kPartUnit = 0x1p-8f;
 template <typename T>
 __device__ __forceinline__ void split(const T (&v)[8], uint4 (&out)[Parts<T>::n]) {
   if constexpr (Parts<T>::n == 1) {
@@ -135,6 +138,8 @@ __device__ __forceinline__ void split(const T (&v)[8], uint4 (&out)[Parts<T>::n]
       for (int j = 0; j < 4; ++j) {
         const uint32_t lo = lead(f[2 * j]);
         w[j] = lo | lead(f[2 * j + 1]) << 16;
+        f[2 * j] *= 1 / kPartUnit;
+        f[2 * j + 1] *= 1 / kPartUnit;
       }
       out[p] = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
 #pragma unroll
         for (int h = 0; h < decltype(most)::value; ++h)
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) v += part[h][q];
+          for (int q = 0; q < kParts; ++q) v = fmaf(part[h][q], q == 0 ? 1.0f : q == 1 ? kPartUnit : kPartUnit * kPartUnit, v);
       };
       if (sharing == 1) add(std::integral_constant<int, 1>());
       else if (sharing <= 4) add(std::integral_constant<int, 4>());
