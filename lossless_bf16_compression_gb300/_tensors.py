@@ -1,4 +1,4 @@
-""": the native calls, streams, the C entry points."""
+"""What the tensor-level calls of ``moe``, ``fp8`` and ``int4`` share: the native calls, streams, the C entry points."""
 from __future__ import annotations
 
 import ctypes
