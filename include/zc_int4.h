@@ -35,7 +35,8 @@ extern "C" {
 /* Weights, `groups` matrices of n x k (contiguous, of `type`), in 4 bits.  A group's scale is the smallest
  * bfloat16 value of at least a seventh of its largest magnitude (1 for a group of zeros), and q is weight / s
  * rounded to nearest, ties to even (decided on the exact quotient).  A group that holds an infinity or a NaN gets
- * the scale NaN and q = 0, so all of its values are NaN. values and scales: 16-byte aligned. */
+ * the scale NaN and q = 0, so all of its values are NaN.  (7 s may pass a group's largest magnitude by up to a 128th: next to
+ * the type's largest number such a value is an infinity.)  values and scales: 16-byte aligned. */
 int zc_int4_quantize(const void* w, int type, int groups, size_t n, size_t k, void* values, void* scales,
                      cudaStream_t stream);
 

@@ -20,7 +20,8 @@ constexpr int balance_warps() { return R::N <= 8 ? 32 : 16; }
 template <typename R>
 constexpr int sum_rows() { return R::N <= 8 ? balance_warps<R>() : 8; }  // in shared memory, up to 32 KB
 constexpr int kIds = 4;  // of a thread, asked for together
-constexpr size_t kMaxParts = 152, kCluster = 8;  // CTAs
+// CTAs: at most as many as a GB300 has SMs (written down: how long the workspace is is said without a device), a cluster's.
+constexpr size_t kMaxParts = 152, kCluster = 8;
 
 struct Parts {  // of each CTA: sums, counts, tokens
   float* sums;

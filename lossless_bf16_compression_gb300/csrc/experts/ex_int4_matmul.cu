@@ -3,14 +3,16 @@
 // out[r, i] = sum over b of s[i, b] * (sum over j in b of x[r, j] q[i, j]).  Bound by the weights' bytes, or by what it
 // takes to unpack them.  A warp takes 2 x 16 weight rows (a record of 1 KB for each 128 columns) and multiplies them by
 // eight or sixteen columns, the rows of x, on the warp-level matrix instructions: with so few rows the tensor cores
-// have time to spare (1024 products a cycle and SM by this way; the tensor-memory instructions want 128 weight
-// rows at a time, too coarse for one token's experts, and the unpacked weights written out first).  The group's scale
-// multiplies the group's sum, once for 128 products.
+// have time to spare (1024 products a cycle and SM by this way; the tensor-memory instructions want 128 weight rows at a
+// time, too coarse for one token's experts, and the unpacked weights written to tensor or shared memory first; for many rows
+// of an expert, where they would serve more columns at a time, they were not tried).  The group's scale multiplies the group's
+// sum, once for 128 products.
 //
 // fp32 rows of x are split into three bfloat16 values that add up to them exactly, the second held 2^8 times its size and the
-// third 2^16 times; they are columns of their own, added at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 17.0 us (59 MB; 2 us of launch,
-// 3 of finding the work and bringing x, 9 at 6.5 TB/s); 64 experts, one to eight rows each, 98 to 100 us (485 MB: 4.9 TB/s;
-// without the loads about 80, without unpacking and products too 24), nine to sixteen 128 to 132.  A scheduler's two cycles
+// third 2^16 times; they are columns of their own, added at the end.  Measured (2048 x 7168, graph replays): eight experts of 64, a row each, 15.7 to 17.8 us (59 MB, 8.7 us at the
+// copy rate; 2 us of launch, 3 of finding the work and bringing x, the rest not accounted for); 64 experts, one to eight rows
+// each, 96 to 100 us (485 MB: 4.9 TB/s; without the loads about 80, without unpacking and products too 24), nine to sixteen 128 to
+// 132; fp32 rows, one, five and eight each, 97, 144 and 254.  A scheduler's two cycles
 // for each logic operation and eight for a product make 40 us of unpacking and 25 of products (sixteen columns: 50); four
 // warps, which is what the registers hold, overlap these in part.
 #include <type_traits>

@@ -119,7 +119,8 @@ def route_grad(d_weights, logits, experts_of, score: str = "softmax", normalize:
                balance: tuple[torch.Tensor, Balance] | None = None, stream=None) -> torch.Tensor:
     """The gradient of route's weights with respect to the logits, of the logits' type.
 
-    ``score``, ``normalize``, ``scale`` and ``experts_of`` are those of the forward call.  With ``balance`` = (d_loss, what
+    ``score``, ``normalize``, ``scale`` and ``experts_of`` are those of the forward call; slots without an expert, or with one whose
+    logit is -infinity, add nothing, whatever their ``d_weights``.  With ``balance`` = (d_loss, what
     balance returned for the same score), that loss's gradient is added before the one rounding."""
     if d_weights is None or experts_of is None:
         raise TypeError("d_weights and experts_of must be CUDA tensors")
