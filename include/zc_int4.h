@@ -48,8 +48,8 @@ int zc_int4_values(const void* values, const void* scales, int groups, size_t n,
  * offsets[g] .. offsets[g + 1] - 1 of x belong to group g (null: one group of all the rows), rows from
  * offsets[groups] on to none, they get zeros.  x is rows x k of `type`, out rows x n of out_type, each with a pitch
  * in values.  Products are exact (with every bit of x, the smallest numbers too), sums are in fp32, a block's before
- * its scale; out is rounded once.  (Sums are held a 64th or, for fp16, a 512th of their size: results below 2^-110 may
- * lose bits.)
+ * its scale; out is rounded once.  (Sums are held a 64th of their size, a 128th for fp32 and a 512th for fp16:
+ * results below 2^-110 may lose bits.)
  * Offsets that do not start at 0, go back or pass `rows` are reported (ZC_ERR_CORRUPT), and nothing outside the
  * rows is touched; which rows are then written is not said.  values and scales: 16-byte aligned. */
 int zc_int4_matmul(const void* x, size_t x_pitch, int type, size_t rows, const void* values, const void* scales,

@@ -69,13 +69,14 @@ __device__ __forceinline__ void fetch_scale(uint32_t& v, const void* p, int on) 
 }
 
 
-// The eight weights of a word as pairs of 16-bit numbers, weights 2 p and 2 p + 1 in the p-th, each q / weight_unit.  The bits
-// of a nibble alone, in the low eight bits of such a number, are one too small to be normal, u or 16 u times the smallest
-// (2^-133 or 2^-24), and one fused multiply-add makes (u - 8) / weight_unit of either, exactly: five logic operations and
-// four multiply-adds for eight weights.  (Or'ed into the low bits of 128, with a subtraction, they took seven and four:
-// 153 us where these take 147, 512 rows over 64 experts at the time.)
-template <typename F>
-constexpr float weight_unit() { return std::is_same_v<F, __half> ? 512.0f : 64.0f; }
+// The eight weights of a word as pairs of 16-bit numbers, weights 2 p and 2 p + 1 in the p-th, each q / weight_unit (128 for fp32
+// rows, whose second and third parts are held up to twice as large as the first).  The bits of a nibble alone, in the low
+// eight bits of such a number, are one too small to be normal, u or 16 u times the smallest (2^-133 or 2^-24), and one fused
+// multiply-add makes (u - 8) / weight_unit of either, exactly: five logic operations and four multiply-adds for eight weights.
+// (Or'ed into the low bits of 128, with a subtraction, they took seven and four: 153 us where these take 147, 512 rows over 64
+// experts at the time.)
+template <typename T>
+constexpr float weight_unit() { return std::is_same_v<T, __half> ? 512.0f : std::is_same_v<T, float> ? 128.0f : 64.0f; }
 template <typename F>
 __device__ __forceinline__ uint32_t fma_pair(uint32_t v, uint32_t times, uint32_t plus) {
   uint32_t r;
@@ -86,12 +87,13 @@ __device__ __forceinline__ uint32_t fma_pair(uint32_t v, uint32_t times, uint32_
 struct Four {
   uint32_t v[4];
 };
-template <typename F>
+template <typename T>
 __device__ __forceinline__ Four four(uint32_t word) {
-  constexpr bool kHalf = std::is_same_v<F, __half>;
-  constexpr uint32_t kLow = kHalf ? 0x78007800u : 0x7F007F00u;    // 2^15, 2^127
-  constexpr uint32_t kHigh = kHalf ? 0x68006800u : 0x7D007D00u;   // 2^11, 2^123
-  constexpr uint32_t kMinus = kHalf ? 0xA400A400u : 0xBE00BE00u;  // -8 / 512, -8 / 64
+  using F = Form<T>;
+  constexpr bool kHalf = std::is_same_v<T, __half>, kFloat = std::is_same_v<T, float>;
+  constexpr uint32_t kLow = kHalf ? 0x78007800u : kFloat ? 0x7E807E80u : 0x7F007F00u;    // 2^15, 2^126, 2^127
+  constexpr uint32_t kHigh = kHalf ? 0x68006800u : kFloat ? 0x7C807C80u : 0x7D007D00u;   // 2^11, 2^122, 2^123
+  constexpr uint32_t kMinus = kHalf ? 0xA400A400u : kFloat ? 0xBD80BD80u : 0xBE00BE00u;  // -8 / 512, -8 / 128, -8 / 64
   const uint32_t up = word >> 8;
   return {fma_pair<F>(word & 0x000F000Fu, kLow, kMinus), fma_pair<F>(word & 0x00F000F0u, kHigh, kMinus),
           fma_pair<F>(up & 0x000F000Fu, kLow, kMinus), fma_pair<F>(up & 0x00F000F0u, kHigh, kMinus)};
@@ -121,9 +123,10 @@ __device__ __forceinline__ uint32_t lead(float& v) {
   return top >> 16;
 }
 
-// Eight neighbouring values as `Parts` vectors of eight bfloat16, each part kPartUnit^-1 times its size: so lifted a part is as
-// large as the one before it at most twice, which fp32's largest value allows, and its last bit is not below bfloat16's smallest
-// number where x's is not below fp32's.  (Unlifted, x below 2^-110 lost its last bits, and large scales showed it.)
+// Eight neighbouring values as `Parts` vectors of eight bfloat16, each part kPartUnit^-1 times its size: so lifted a part is at
+// most twice as large as the first, which fp32's largest value and the weights' unit allow, and its last bit is not below
+// bfloat16's smallest number where x's is not below fp32's.  (Unlifted, x below 2^-110 lost its last bits, and large scales
+// showed it.)
 constexpr float kPartUnit = 0x1p-8f;
 template <typename T>
 __device__ __forceinline__ void split(const T (&v)[8], uint4 (&out)[Parts<T>::n]) {
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
                 for (int h = 0; h < kTiles; ++h) {
                   const uint32_t wa = q == 0 ? a[i][h].x : q == 1 ? a[i][h].y : q == 2 ? a[i][h].z : a[i][h].w;
                   const uint32_t wb = q == 0 ? b[i][h].x : q == 1 ? b[i][h].y : q == 2 ? b[i][h].z : b[i][h].w;
-                  const Four fa = four<F>(wa), fb = four<F>(wb);
+                  const Four fa = four<T>(wa), fb = four<T>(wb);
 #pragma unroll
                   for (int n = 0; n < N; ++n) {
                     if (q == 0) multiply<F, true>(block_sum[h][n], fa.v[0], fb.v[0], fa.v[1], fb.v[1], v[n].x, v[n].y);
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_product_kernel(const __grid_
       else if (sharing <= 4) add(std::integral_constant<int, 4>());
       else add(std::integral_constant<int, kWarps>());
       const size_t column = static_cast<size_t>(line + at) * (kTiles * kInt4Rows) + c;
-      if (column < p.w.n) put(p, pass.row + r, column, weight_unit<F>() * v);
+      if (column < p.w.n) put(p, pass.row + r, column, weight_unit<T>() * v);
     };
     constexpr int kWide = kTiles * kInt4Rows;
     if (sharing == 1) {  // a warp's own
